@@ -17,6 +17,8 @@ confidence  The draft-side confidence step before it: each draft row's top-1
          probability and the draft length an early-stop threshold implies.
 lmhead   The step fed from hidden states through the LM heads: logits as the
          fp64 product of hidden states and head weights, then verify.
+tree    Tree drafting: attention over a paged cache, greedy verify of a tree,
+        append and eviction by attention weight, and a beam step.
 
 Parity status of each function is stated in its docstring.  Two readings are
 "parity unpinned" by the pages (the repetition-penalty formula and the top-p
@@ -34,5 +36,9 @@ from .verify import (
 )
 from .confidence import top1_prob, draft_lengths, draft_confidence_ref
 from .lmhead import lmhead_logits, lmhead_verify_sample_ref, lmhead_verify_greedy_ref
+from .tree import (
+    visible_nodes, tree_attention_ref, tree_verify_greedy_ref, commit_weights_ref, evict_ref,
+    beam_select_ref,
+)
 
 __all__ = [n for n in dir() if not n.startswith("_")]

@@ -13,6 +13,9 @@ Functions mirror the C entry points:
     workspace_bytes(...) -> sd_verify_workspace_bytes
     strerror(code)       -> sd_strerror
     debug_process_rows(...), debug_uniforms(...)  (test exports)
+The operators for drafted trees (include/sd_tree.h) are in tree.py and are
+exported here too: tree_attention, tree_verify_greedy, cache_commit,
+cache_evict, beam_select, beam_reorder.
 """
 import ctypes
 import os
@@ -429,3 +432,10 @@ def debug_lmhead_logits(args, out_target, out_draft=None, workspace=None, stream
                                     _ptr(out_draft), _stream(stream))
     if rc != SD_OK:
         raise SdVerifyError(rc, "sd_debug_lmhead_logits")
+
+
+from .tree import (  # noqa: E402  (needs the loaded library)
+    SD_F16, SD_MAX_BEAMS, SD_MAX_NODES, SD_ST_BAD_LEN, SD_ST_BAD_NODES, SD_ST_BAD_PAGE,
+    SD_ST_BAD_PATH, SD_ST_BAD_TREE, SD_ST_TREE_INVALID_MASK, beam_reorder, beam_select,
+    cache_commit, cache_evict, make_tree_attention_args, tree_attention, tree_verify_greedy,
+)

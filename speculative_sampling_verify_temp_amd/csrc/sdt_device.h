@@ -1,0 +1,129 @@
+// What the tree-drafting kernels share on gfx950: the cache's addressing, the
+// per-request checks, element conversions and the host checks of the cache
+// descriptor.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <math.h>
+
+#include "sd_tree.h"
+#include "sdv_device.h"
+
+namespace sdt {
+
+using sdv::WAVE;
+
+// The cache as the kernels see it.
+struct Cache {
+  char* k;
+  char* v;
+  int64_t page_stride, head_stride, slot_stride;   // bytes
+  const int32_t* table;
+  int64_t ld_table;
+  const int32_t* lens;
+  int B, H, page_shift, page_mask, num_pages, cap;
+};
+
+// Nodes of one request; T = 0 and a status bit where the offsets are wrong.
+struct Nodes {
+  int first, T;
+  uint32_t st;
+};
+
+__device__ __forceinline__ Nodes request_nodes(const int32_t* off, int b, int N, int max_nodes) {
+  const int a = off[b], e = off[b + 1];
+  Nodes n{a, e - a, 0u};
+  if (a < 0 || e < a || e > N || e - a > max_nodes) n = Nodes{0, 0, SD_ST_BAD_NODES};
+  return n;
+}
+
+// Slots of request b in use; 0 and a status bit where the length is wrong.
+__device__ __forceinline__ int request_ctx(const Cache& c, int b, uint32_t& st) {
+  const int n = c.lens[b];
+  if (n >= 0 && n <= c.cap) return n;
+  st |= SD_ST_BAD_LEN;
+  return 0;
+}
+
+// Byte offset of (slot, head) in k and in v, -1 on a bad page.  Page indexes
+// times strides pass 32 bits in a large pool: 64-bit arithmetic.
+__device__ __forceinline__ int64_t slot_offset(const Cache& c, const int32_t* row, int slot, int h) {
+  const int p = row[slot >> c.page_shift];
+  if ((unsigned)p >= (unsigned)c.num_pages) return -1;
+  return p * c.page_stride + h * c.head_stride + (slot & c.page_mask) * c.slot_stride;
+}
+
+__device__ __forceinline__ const int32_t* table_row(const Cache& c, int b) {
+  return c.table + b * c.ld_table;
+}
+
+// A 16-bit element as fp32.
+template <int DT>
+__device__ __forceinline__ float to_f32(uint16_t u) {
+  if constexpr (DT == SD_BF16) return __uint_as_float((uint32_t)u << 16);
+  _Float16 h;
+  __builtin_memcpy(&h, &u, 2);
+  return (float)h;
+}
+
+// fp32 rounded to a 16-bit element (to nearest, ties to even).
+template <int DT>
+__device__ __forceinline__ uint16_t from_f32(float x) {
+  uint16_t u;
+  if constexpr (DT == SD_BF16) {
+    const __bf16 h = (__bf16)x;
+    __builtin_memcpy(&u, &h, 2);
+  } else {
+    const _Float16 h = (_Float16)x;
+    __builtin_memcpy(&u, &h, 2);
+  }
+  return u;
+}
+
+// ---- host side ----
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
+
+// SD_OK or the code of the first defect of a cache descriptor.
+inline int check_cache(const sd_kv_cache_t& c) {
+  if (!c.k || !c.v || !c.page_table || !c.context_lens || !aligned16(c.k) || !aligned16(c.v))
+    return SD_EINVAL;
+  if (c.dtype != SD_BF16 && c.dtype != SD_F16) return SD_EINVAL;
+  if (c.B < 1 || c.H_kv < 1 || c.D < 1 || c.page_size < 1 || c.num_pages < 1 || c.max_pages < 1 ||
+      c.ld_table < c.max_pages)
+    return SD_EINVAL;
+  if (c.page_stride < 0 || c.head_stride < 0 || c.slot_stride < c.D || c.page_stride % 8 ||
+      c.head_stride % 8 || c.slot_stride % 8)
+    return SD_EINVAL;
+  if (c.D != 64 && c.D != 128) return SD_EUNSUPPORTED;
+  if ((c.page_size & (c.page_size - 1)) || c.page_size > SD_MAX_PAGE_SIZE) return SD_EUNSUPPORTED;
+  if ((int64_t)c.max_pages * c.page_size > 0x7FFFFFFF - 4096) return SD_EUNSUPPORTED;
+  if (c.B > 65535 || c.H_kv > 65535) return SD_EUNSUPPORTED;
+  return SD_OK;
+}
+
+inline Cache device_cache(const sd_kv_cache_t& c) {
+  Cache d;
+  d.k = static_cast<char*>(c.k);
+  d.v = static_cast<char*>(c.v);
+  d.page_stride = c.page_stride * 2;
+  d.head_stride = c.head_stride * 2;
+  d.slot_stride = c.slot_stride * 2;
+  d.table = c.page_table;
+  d.ld_table = c.ld_table;
+  d.lens = c.context_lens;
+  d.B = c.B;
+  d.H = c.H_kv;
+  d.page_shift = __builtin_ctz((unsigned)c.page_size);
+  d.page_mask = c.page_size - 1;
+  d.num_pages = c.num_pages;
+  d.cap = c.max_pages * c.page_size;
+  return d;
+}
+
+// Strides of packed node rows: 16-byte aligned rows.
+inline bool rows_ok(const void* p, int64_t node, int64_t head) {
+  return p && aligned16(p) && node >= 0 && head >= 0 && node % 8 == 0 && head % 8 == 0;
+}
+
+}  // namespace sdt

@@ -1,0 +1,467 @@
+"""Tree drafting on MI355X: Python binding of include/sd_tree.h.
+
+Functions mirror the C entry points; like the rest of the package they only
+check and marshal arguments.
+    tree_attention(...)      -> sd_tree_attention
+    tree_verify_greedy(...)  -> sd_tree_verify_greedy
+    cache_commit(...)        -> sd_cache_commit
+    cache_evict(...)         -> sd_cache_evict
+    beam_select(...)         -> sd_beam_select
+    beam_reorder(...)        -> sd_beam_reorder
+
+The cache is a pair of tensors [pages][H_kv][page_size][D] (any strides with
+contiguous rows, the same for both), with a page table [B][max_pages] and the
+slots in use [B], both int32.  Outputs and workspaces that are not passed in
+are allocated on the current stream; with `stream` given they are kept from
+reuse until that stream is done with them.
+"""
+import ctypes
+
+from . import (SD_BF16, SD_F32, SD_OK, SD_ST_INVALID_MASK, SdVerifyError, _ptr, _stream, lib)
+
+SD_F16 = 2
+SD_MAX_NODES = 64
+SD_MAX_BEAMS = 64
+SD_MAX_PAGE_SIZE = 1024
+SD_MAX_GROUP = 32
+SD_ST_BAD_LEN, SD_ST_BAD_NODES, SD_ST_BAD_PAGE = 1 << 8, 1 << 9, 1 << 10
+SD_ST_BAD_TREE, SD_ST_BAD_PATH = 1 << 11, 1 << 12
+SD_ST_TREE_INVALID_MASK = SD_ST_INVALID_MASK | SD_ST_BAD_LEN | SD_ST_BAD_NODES | SD_ST_BAD_PATH
+
+_P, _I32, _I64, _U32, _F, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
+                                 ctypes.c_float, ctypes.c_size_t)
+
+
+class SdKvCache(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("page_stride", _I64), ("head_stride", _I64),
+                ("slot_stride", _I64), ("page_table", _P), ("ld_table", _I64),
+                ("context_lens", _P), ("dtype", _I32), ("B", _I32), ("H_kv", _I32), ("D", _I32),
+                ("page_size", _I32), ("num_pages", _I32), ("max_pages", _I32)]
+
+
+class SdTreeAttentionArgs(ctypes.Structure):
+    _fields_ = [("cache", SdKvCache), ("q", _P), ("k_new", _P), ("v_new", _P),
+                ("q_node", _I64), ("q_head", _I64), ("k_node", _I64), ("k_head", _I64),
+                ("v_node", _I64), ("v_head", _I64), ("node_offsets", _P), ("parents", _P),
+                ("tree_mask", _P), ("N", _I32), ("max_nodes", _I32), ("H_q", _I32), ("scale", _F)]
+
+
+class SdTreeVerifyArgs(ctypes.Structure):
+    _fields_ = [("logits", _P), ("ld", _I64), ("tokens", _P), ("parents", _P),
+                ("node_offsets", _P), ("dtype", _I32), ("B", _I32), ("N", _I32), ("V", _I32),
+                ("max_nodes", _I32), ("flags", _U32)]
+
+
+class SdCacheCommitArgs(ctypes.Structure):
+    _fields_ = [("cache", SdKvCache), ("k_new", _P), ("v_new", _P), ("k_node", _I64),
+                ("k_head", _I64), ("v_node", _I64), ("v_head", _I64), ("node_offsets", _P),
+                ("path", _P), ("ld_path", _I64), ("path_lens", _P), ("N", _I32),
+                ("max_nodes", _I32), ("q", _P), ("q_node", _I64), ("q_head", _I64), ("lse", _P),
+                ("H_q", _I32), ("scale", _F), ("decay", _F), ("mass_in", _P), ("mass_out", _P),
+                ("ld_mass", _I64), ("positions", _P), ("seen", _P)]
+
+
+class SdCacheEvictArgs(ctypes.Structure):
+    _fields_ = [("cache", SdKvCache), ("mass_in", _P), ("mass_out", _P), ("positions_in", _P),
+                ("positions_out", _P), ("ld_mass", _I64), ("seen", _P), ("budget", _I32),
+                ("recent", _I32), ("sinks", _I32)]
+
+
+class SdBeamSelectArgs(ctypes.Structure):
+    _fields_ = [("logits", _P), ("ld", _I64), ("scores", _P), ("ended", _P), ("dtype", _I32),
+                ("B", _I32), ("W", _I32), ("V", _I32), ("n_out", _I32), ("eos_id", _I32)]
+
+
+class SdBeamReorderArgs(ctypes.Structure):
+    _fields_ = [("in_", _P), ("out", _P), ("in_layer", _I64), ("in_request", _I64),
+                ("in_beam", _I64), ("in_seg", _I64), ("out_layer", _I64), ("out_request", _I64),
+                ("out_beam", _I64), ("out_seg", _I64), ("parents", _P), ("lengths", _P),
+                ("unit_bytes", _I64), ("layers", _I32), ("B", _I32), ("W_in", _I32),
+                ("W_out", _I32), ("segs", _I32), ("max_units", _I32)]
+
+
+def _declare():
+    def entry(name, struct, *rest):
+        f = getattr(lib, name)
+        f.argtypes = [ctypes.POINTER(struct), *rest]
+        f.restype = ctypes.c_int
+
+    size = ctypes.POINTER(_SZ)
+    entry("sd_tree_attention_workspace_bytes", SdTreeAttentionArgs, size)
+    entry("sd_tree_attention", SdTreeAttentionArgs, _P, _SZ, _P, _P, _P, _P)
+    entry("sd_tree_verify_workspace_bytes", SdTreeVerifyArgs, size)
+    entry("sd_tree_verify_greedy", SdTreeVerifyArgs, _P, _SZ, _P, _P, _P, _P, _P)
+    entry("sd_cache_commit", SdCacheCommitArgs, _P, _P, _P)
+    entry("sd_cache_evict_workspace_bytes", SdCacheEvictArgs, size)
+    entry("sd_cache_evict", SdCacheEvictArgs, _P, _SZ, _P, _P, _P)
+    entry("sd_beam_select_workspace_bytes", SdBeamSelectArgs, size)
+    entry("sd_beam_select", SdBeamSelectArgs, _P, _SZ, _P, _P, _P, _P, _P, _P)
+    entry("sd_beam_reorder", SdBeamReorderArgs, _P)
+
+
+_declare()
+
+
+# ---- argument checks ----
+
+def _here(first, *rest):
+    """All tensors on the current GPU, which is where the call's work goes."""
+    import torch
+    dev = first.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current GPU")
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors of a call must be on the same GPU")
+
+
+def _ints(t, name, *shape):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _floats(t, name, *shape):
+    import torch
+    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _status(status, B):
+    return None if status is None else _ints(status, "status", B)
+
+
+def _rows(t, name, like, N, H, D):
+    """Packed node rows [N][H][D] of the cache's element type: (pointer, strides)."""
+    if t.dtype != like.dtype or tuple(t.shape) != (N, H, D):
+        raise ValueError(f"{name} must be {like.dtype} of shape {[N, H, D]}")
+    if D > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _cache(k, v, table, lens):
+    import torch
+    if k.dtype == torch.bfloat16:
+        code = SD_BF16
+    elif k.dtype == torch.float16:
+        code = SD_F16
+    else:
+        raise TypeError(f"the cache must be bfloat16 or float16 (got {k.dtype})")
+    if k.dim() != 4 or k.shape != v.shape or v.dtype != k.dtype or k.stride() != v.stride():
+        raise ValueError("k_cache and v_cache must be [pages][H_kv][page_size][D] with the same "
+                         "type, shape and strides")
+    pages, H, page, D = k.shape
+    ps, hs, ss, es = k.stride()
+    if es != 1 and D > 1:
+        raise ValueError("the elements of a cache row must be contiguous")
+    if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("page_table must be int32 [B][max_pages] with contiguous rows")
+    B, cols = table.shape
+    return SdKvCache(k.data_ptr(), v.data_ptr(), ps, hs, ss, table.data_ptr(),
+                     table.stride(0) if B > 1 else max(cols, table.stride(0)),
+                     _ints(lens, "context_lens", B), code, B, H, D, page, pages, cols)
+
+
+def _bytes(name, a):
+    n = _SZ()
+    rc = getattr(lib, name + "_workspace_bytes")(ctypes.byref(a), ctypes.byref(n))
+    if rc != SD_OK:
+        raise SdVerifyError(rc, name)
+    return n.value
+
+
+def _workspace(name, a, given, like, keep):
+    """The given workspace or a new one: (tensor, bytes)."""
+    import torch
+    if given is not None:
+        if not given.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
+        _here(like, given)
+        return given, given.numel() * given.element_size()
+    n = _bytes(name, a)
+    ws = torch.empty(max(16, n), dtype=torch.uint8, device=like.device)
+    keep.append(ws)
+    return ws, n
+
+
+def _done(rc, name, stream, keep):
+    if rc != SD_OK:
+        raise SdVerifyError(rc, name)
+    if stream is not None:
+        for t in keep:
+            t.record_stream(stream)
+
+
+# ---- attention of a drafted tree ----
+
+def make_tree_attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens,
+                             node_offsets, max_nodes, parents=None, tree_mask=None, scale=None):
+    """Fill sd_tree_attention_args_t from tensors: q [N][H_q][D], k_new and
+    v_new [N][H_kv][D], node_offsets [B + 1], parents [N] int32 or tree_mask
+    [N] int64 (bit j: node j of the request is seen) or neither (a chain);
+    scale defaults to 1 / sqrt(D)."""
+    import torch
+    c = _cache(k_cache, v_cache, page_table, context_lens)
+    N, Hq, D = q.shape
+    if c.D != D:
+        raise ValueError("queries and cache must have the same head size")
+    qp, qn, qh = _rows(q, "q", k_cache, N, Hq, D)
+    kp, kn, kh = _rows(k_new, "k_new", k_cache, N, c.H_kv, D)
+    vp, vn, vh = _rows(v_new, "v_new", k_cache, N, c.H_kv, D)
+    mask = None
+    if tree_mask is not None:
+        if tree_mask.dtype != torch.int64 or tuple(tree_mask.shape) != (N,) or not tree_mask.is_contiguous():
+            raise ValueError("tree_mask must be a contiguous int64 tensor of shape [N]")
+        mask = tree_mask.data_ptr()
+    return SdTreeAttentionArgs(c, qp, kp, vp, qn, qh, kn, kh, vn, vh,
+                               _ints(node_offsets, "node_offsets", c.B + 1),
+                               None if parents is None else _ints(parents, "parents", N), mask, N,
+                               max_nodes, Hq, D ** -0.5 if scale is None else scale)
+
+
+def tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets,
+                   max_nodes, parents=None, tree_mask=None, scale=None, want_lse=False, out=None,
+                   lse=None, status=None, workspace=None, stream=None):
+    """Attention of the packed nodes of B drafted trees over the paged cache
+    and each other; returns (out [N][H_q][D], lse [N][H_q] or None).
+
+    out, lse: optional preallocated contiguous outputs; status: optional [B]
+    int32 tensor for the per-request bits."""
+    import torch
+    _here(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets, parents,
+          tree_mask, out, lse, status)
+    a = make_tree_attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens,
+                                 node_offsets, max_nodes, parents, tree_mask, scale)
+    N, Hq, D = q.shape
+    keep = []
+    if out is None:
+        out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+        keep.append(out)
+    elif out.dtype != q.dtype or tuple(out.shape) != (N, Hq, D) or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's type and shape")
+    if lse is not None:
+        _floats(lse, "lse", N, Hq)
+    elif want_lse:
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        keep.append(lse)
+    ws, n = _workspace("sd_tree_attention", a, workspace, q, keep)
+    rc = lib.sd_tree_attention(ctypes.byref(a), ws.data_ptr(), n, out.data_ptr(), _ptr(lse),
+                               _status(status, a.cache.B), _stream(stream))
+    _done(rc, "sd_tree_attention", stream, keep)
+    return out, lse
+
+
+# ---- greedy verify of a tree ----
+
+def _logits(t, name):
+    """Rows with unit element stride: (pointer, row stride, type code)."""
+    import torch
+    if t.dtype == torch.float32:
+        code = SD_F32
+    elif t.dtype == torch.bfloat16:
+        code = SD_BF16
+    else:
+        raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+    V = t.shape[-1]
+    if V > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the logits of a row must be contiguous")
+    ld = t.stride(-2)
+    if t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * ld:
+        raise ValueError(f"{name} must have its rows back to back")
+    rows = t.numel() // max(1, V)
+    return t.data_ptr(), (ld if rows > 1 else max(ld, -(-V // 8) * 8)), code
+
+
+def tree_verify_greedy(logits, tokens, parents, node_offsets, max_nodes, flags=0, status=None,
+                       out=None, workspace=None, stream=None):
+    """Greedy verify of B drafted trees: logits [N][V], tokens and parents
+    [N], node_offsets [B + 1].  Returns (accepted [B], path [B][max_nodes],
+    tokens [B][max_nodes]).
+
+    out: optional dict of preallocated outputs (accepted, path, tokens)."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [N][V]")
+    N, V = logits.shape
+    B = node_offsets.numel() - 1
+    o = out or {}
+    acc, path, tok = o.get("accepted"), o.get("path"), o.get("tokens")
+    _here(logits, tokens, parents, node_offsets, status, acc, path, tok)
+    ptr, ld, code = _logits(logits, "logits")
+    a = SdTreeVerifyArgs(ptr, ld, _ints(tokens, "tokens", N), _ints(parents, "parents", N),
+                         _ints(node_offsets, "node_offsets", B + 1), code, B, N, V, max_nodes, flags)
+    keep = []
+    ws, n = _workspace("sd_tree_verify", a, workspace, logits, keep)
+
+    def output(t, name, *shape):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.int32, device=logits.device)
+            keep.append(t)
+        else:
+            _ints(t, name, *shape)
+        return t
+
+    acc = output(acc, "accepted", B)
+    path, tok = output(path, "path", B, max_nodes), output(tok, "tokens", B, max_nodes)
+    rc = lib.sd_tree_verify_greedy(ctypes.byref(a), ws.data_ptr(), n, acc.data_ptr(),
+                                   path.data_ptr(), tok.data_ptr(), _status(status, B),
+                                   _stream(stream))
+    _done(rc, "sd_tree_verify_greedy", stream, keep)
+    return acc, path, tok
+
+
+# ---- append to and eviction from the cache ----
+
+def cache_commit(k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets, max_nodes,
+                 path, path_lens, out_context, q=None, lse=None, scale=None, mass_in=None,
+                 mass_out=None, decay=1.0, positions=None, seen=None, status=None, stream=None):
+    """Append the nodes path[b][: path_lens[b]] to the cache; out_context [B]
+    receives the new lengths.
+
+    With mass_out [B][H_kv][L] the attention weight of these rows is
+    accumulated from q, lse (of tree_attention) and mass_in (mass_out's own
+    values when None); positions [B][H_kv][L] and seen [B] record where the
+    appended tokens stand."""
+    if mass_out is not None and (q is None or lse is None):
+        raise ValueError("weights need q and lse")
+    if mass_out is not None and mass_in is None:
+        mass_in = mass_out
+    _here(k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets, path, path_lens,
+          out_context, q, lse, mass_in, mass_out, positions, seen, status)
+    c = _cache(k_cache, v_cache, page_table, context_lens)
+    N, B = k_new.shape[0], c.B
+    kp, kn, kh = _rows(k_new, "k_new", k_cache, N, c.H_kv, c.D)
+    vp, vn, vh = _rows(v_new, "v_new", k_cache, N, c.H_kv, c.D)
+    a = SdCacheCommitArgs(c, kp, vp, kn, kh, vn, vh, _ints(node_offsets, "node_offsets", B + 1),
+                          _ints(path, "path", B, path.shape[-1]), path.shape[-1],
+                          _ints(path_lens, "path_lens", B), N, max_nodes)
+    L = None
+    if mass_out is not None:
+        L = mass_out.shape[-1]
+        a.q, a.q_node, a.q_head = _rows(q, "q", k_cache, N, q.shape[1], c.D)
+        a.H_q = q.shape[1]
+        a.lse = _floats(lse, "lse", N, a.H_q)
+        a.scale = c.D ** -0.5 if scale is None else scale
+        a.decay = decay
+        a.mass_in = _floats(mass_in, "mass_in", B, c.H_kv, L)
+        a.mass_out = _floats(mass_out, "mass_out", B, c.H_kv, L)
+        a.ld_mass = L
+    if positions is not None:
+        if seen is None:
+            raise ValueError("positions need seen")
+        L = positions.shape[-1] if L is None else L
+        a.positions = _ints(positions, "positions", B, c.H_kv, L)
+        a.seen = _ints(seen, "seen", B)
+        a.ld_mass = L
+    rc = lib.sd_cache_commit(ctypes.byref(a), _ints(out_context, "out_context", B),
+                             _status(status, B), _stream(stream))
+    _done(rc, "sd_cache_commit", stream, ())
+    return out_context
+
+
+def cache_evict(k_cache, v_cache, page_table, context_lens, mass_in, mass_out, positions_in,
+                positions_out, seen, out_context, budget, recent=0, sinks=0, status=None,
+                workspace=None, stream=None):
+    """Cut every request's cache to its `budget` slots of the largest mass,
+    keeping positions below `sinks` and the last `recent` ones; out_context
+    [B] receives the new lengths.  mass_* [B][H_kv][L] float32 and positions_*
+    [B][H_kv][L] int32 (or None, None, with recent = sinks = 0); outputs may
+    be the inputs."""
+    _here(k_cache, v_cache, page_table, context_lens, mass_in, mass_out, positions_in,
+          positions_out, seen, out_context, status)
+    c = _cache(k_cache, v_cache, page_table, context_lens)
+    B, L = c.B, mass_in.shape[-1]
+    if (positions_in is None) != (positions_out is None):
+        raise ValueError("positions_in and positions_out go together")
+    a = SdCacheEvictArgs(c, _floats(mass_in, "mass_in", B, c.H_kv, L),
+                         _floats(mass_out, "mass_out", B, c.H_kv, L),
+                         None if positions_in is None else _ints(positions_in, "positions_in", B, c.H_kv, L),
+                         None if positions_out is None else _ints(positions_out, "positions_out", B, c.H_kv, L),
+                         L, None if seen is None else _ints(seen, "seen", B), budget, recent, sinks)
+    keep = []
+    ws, n = _workspace("sd_cache_evict", a, workspace, k_cache, keep)
+    rc = lib.sd_cache_evict(ctypes.byref(a), ws.data_ptr(), n,
+                            _ints(out_context, "out_context", B), _status(status, B),
+                            _stream(stream))
+    _done(rc, "sd_cache_evict", stream, keep)
+    return out_context
+
+
+# ---- a beam step ----
+
+def beam_select(logits, scores, n_out, ended=None, eos_id=-1, out_ended=None, status=None,
+                out=None, workspace=None, stream=None):
+    """The n_out best continuations over the beams of each request: logits
+    [B][W][V] (float32 or bfloat16), scores [B][W] float32, ended [B][W] uint8
+    or None.  Returns (scores [B][n_out], parents [B][n_out], tokens
+    [B][n_out]); out_ended: optional [B][n_out] uint8 output.
+
+    out: optional dict of preallocated outputs (scores, parents, tokens)."""
+    import torch
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B][W][V]")
+    B, W, V = logits.shape
+    o = out or {}
+    sc, par, tok = o.get("scores"), o.get("parents"), o.get("tokens")
+    _here(logits, scores, ended, out_ended, status, sc, par, tok)
+    for t, name, shape in ((ended, "ended", (B, W)), (out_ended, "out_ended", (B, n_out))):
+        if t is not None and (t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {list(shape)}")
+    ptr, ld, code = _logits(logits, "logits")
+    a = SdBeamSelectArgs(ptr, ld, _floats(scores, "scores", B, W),
+                         None if ended is None else ended.data_ptr(), code, B, W, V, n_out, eos_id)
+    keep = []
+    ws, n = _workspace("sd_beam_select", a, workspace, logits, keep)
+
+    def output(t, name, dtype, check):
+        if t is None:
+            t = torch.empty((B, n_out), dtype=dtype, device=logits.device)
+            keep.append(t)
+        else:
+            check(t, name, B, n_out)
+        return t
+
+    sc = output(sc, "scores", torch.float32, _floats)
+    par, tok = output(par, "parents", torch.int32, _ints), output(tok, "tokens", torch.int32, _ints)
+    rc = lib.sd_beam_select(ctypes.byref(a), ws.data_ptr(), n, sc.data_ptr(), par.data_ptr(),
+                            tok.data_ptr(), _ptr(out_ended), _status(status, B), _stream(stream))
+    _done(rc, "sd_beam_select", stream, keep)
+    return sc, par, tok
+
+
+def beam_reorder(state, parents, lengths=None, out=None, stream=None):
+    """Move beam states to the beams that continue them: state
+    [layers][B][W][segs][units][..] (the trailing part of a unit contiguous,
+    a multiple of 16 bytes), parents [B][W_out] int32, lengths [B] int32 units
+    in use or None.  In place without `out`; returns the tensor written."""
+    if state.dim() < 5:
+        raise ValueError("state must be [layers][B][W][segs][units][..]")
+    dst = state if out is None else out
+    _here(state, dst, parents, lengths)
+    layers, B, W, segs, units = state.shape[:5]
+    if parents.dim() != 2 or parents.shape[0] != B:
+        raise ValueError("parents must be [B][W_out]")
+    W_out = parents.shape[1]
+    if dst.dtype != state.dtype or tuple(dst.shape) != (layers, B, W_out, segs, *state.shape[4:]):
+        raise ValueError("out must have state's type and shape, with W_out beams")
+    es, unit = state.element_size(), 1
+    for n in state.shape[5:]:
+        unit *= n
+    for t in (state, dst):
+        want = unit * es
+        for n, s in zip((*t.shape[5:], 1), t.stride()[4:]):
+            if s * es != want:
+                raise ValueError("the units of a state row must be contiguous")
+            want //= max(1, n)
+    if out is not None and out is not state and out.data_ptr() == state.data_ptr() and out.stride() != state.stride():
+        raise ValueError("out must not overlap state")
+    a = SdBeamReorderArgs(state.data_ptr(), dst.data_ptr(), *(s * es for s in state.stride()[:4]),
+                          *(s * es for s in dst.stride()[:4]), _ints(parents, "parents", B, W_out),
+                          None if lengths is None else _ints(lengths, "lengths", B), unit * es,
+                          layers, B, W, W_out, segs, units)
+    rc = lib.sd_beam_reorder(ctypes.byref(a), _stream(stream))
+    _done(rc, "sd_beam_reorder", stream, ())
+    return dst
