@@ -1,10 +1,10 @@
 // Append to and eviction from a paged key/value cache on gfx950.
 //
 // sd_cache_commit:
-//   k_commit_append  one workgroup per request: the branch's keys, values and
-//                    positions into the slots behind the context;
-//   k_commit_mass    one thread per (slot, KV head): the slot's weight, a sum
-//                    of exp(scale q . k - lse) over the branch's query rows.
+//   k_commit       one workgroup per (run of slots, KV head, request): the
+//                  slots' weights, sums of exp(scale q . k - lse) over the
+//                  branch's query rows, by MFMA; the first run's also
+//                  appends the branch's keys, values and positions.
 // sd_cache_evict:
 //   k_evict_select   one workgroup per (request, KV head): the budget-th
 //                    largest key by a radix search, then the freed slots
@@ -19,6 +19,9 @@ using namespace sdv;
 using namespace sdt;
 
 namespace {
+
+constexpr int NT_C = 256;   // threads of a commit workgroup: 64 keys a wave
+constexpr int QB = 128;     // query rows in LDS
 
 struct CommitArgs {
   Cache c;
@@ -70,14 +73,14 @@ __device__ __forceinline__ Branch request_branch(const CommitArgs& a, int b) {
   return r;
 }
 
+// Append of head h: keys, values and positions; the first head's workgroup
+// also leaves the length and the status.
 template <int D>
-__global__ __launch_bounds__(256) void k_commit_append(CommitArgs a) {
+__device__ void append(const CommitArgs& a, const Branch& r, int b, int h) {
   constexpr int LPR = D / 8;   // lanes of one row
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const Branch r = request_branch(a, b);
+  const int tid = threadIdx.x, d = (tid % LPR) * 16;
   const int32_t* tab = table_row(a.c, b);
-  for (int u = tid / LPR; u < r.m * a.c.H; u += 256 / LPR) {
-    const int i = u / a.c.H, h = u % a.c.H, d = (tid % LPR) * 16;
+  for (int i = tid / LPR; i < r.m; i += NT_C / LPR) {
     const int64_t at = slot_offset(a.c, tab, r.ctx + i, h);
     const int64_t row = r.first + a.path[b * a.ld_path + i];
     if (at >= 0) {
@@ -87,7 +90,7 @@ __global__ __launch_bounds__(256) void k_commit_append(CommitArgs a) {
     if (a.positions && d == 0)
       a.positions[((int64_t)b * a.c.H + h) * a.ld_mass + r.ctx + i] = a.seen[b] + i;
   }
-  if (tid >= WAVE) return;
+  if (h || tid >= WAVE) return;
   if (tid == 0) a.out_ctx[b] = (r.st & SD_ST_BAD_LEN) ? a.c.lens[b] : r.ctx + r.m;
   if (!a.status) return;
   bool bad_page = false;
@@ -97,35 +100,122 @@ __global__ __launch_bounds__(256) void k_commit_append(CommitArgs a) {
   if (tid == 0) a.status[b] = st;
 }
 
+// grid (chunks of `chunk` slots, H, B).  A wave holds 64 keys in registers as
+// MFMA operands straight from the cache and meets the branch's query rows, 16
+// at a time from LDS: S = Q . K^T, so a lane holds 4 rows of one key and the
+// sum over the rows is in its own registers but for two lane swaps at the end.
+// The keys are read once (bound by HBM up to about 150 rows); row blocks past
+// the first are staged again for every tile.
 template <int DT, int D>
-__global__ __launch_bounds__(256) void k_commit_mass(CommitArgs a) {
-  const int b = blockIdx.z, h = blockIdx.y;
-  const Branch r = request_branch(a, b);
-  if (r.st) return;
+__global__ __launch_bounds__(NT_C, 2) void k_commit(CommitArgs a, int chunk) {
+  constexpr int KS = D / 32, CPR = D / 8;
+  __shared__ __align__(16) char sq[QB * D * 2];
+  __shared__ __align__(16) float se[QB];
+  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, l = tid % WAVE, w = tid / WAVE;
+  const int n = l & 15, g4 = l >> 4;
+  const Branch br = request_branch(a, b);
+  if (blockIdx.x == 0) append<D>(a, br, b, h);
+  const int end = br.ctx + br.m;
+  int base = blockIdx.x * chunk;
+  const int stop = base + min(chunk, max(0, end - base));
+  if (!a.mass_out || br.st || base >= stop) return;
   const int32_t* tab = table_row(a.c, b);
-  for (int t = blockIdx.x * 256 + threadIdx.x; t < r.ctx + r.m; t += gridDim.x * 256) {
-    const bool fresh = t >= r.ctx;
-    const char* k = nullptr;
-    if (fresh) {
-      const int64_t row = r.first + a.path[b * a.ld_path + t - r.ctx];
-      k = a.kn + row * a.k_node + h * a.k_head;
-    } else {
-      const int64_t at = slot_offset(a.c, tab, t, h);
-      if (at >= 0) k = a.c.k + at;
+  const int rows = br.m * a.G;
+  const float c = a.scale * 1.4426950408889634f;
+
+  auto stage = [&](int q0) {       // query rows q0 .. q0 + QB - 1, zeros and +inf past the last
+    __syncthreads();
+    for (int u = tid; u < QB * CPR; u += NT_C) {
+      const int lr = u / CPR, col = u % CPR, r = q0 + lr;
+      if (lr >= ((rows - q0 + 15) & ~15)) break;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int64_t node = br.first + a.path[b * a.ld_path + r / a.G];
+        v = *(const uint4*)(a.q + node * a.q_node + (h * a.G + r % a.G) * a.q_head + col * 16);
+      }
+      *(uint4*)(sq + lr * (D * 2) + ((col ^ swz<D>(lr)) * 16)) = v;
     }
-    float w = 0.0f;
-    for (int i = fresh ? t - r.ctx : 0; k && i < r.m; ++i) {
-      const int64_t row = r.first + a.path[b * a.ld_path + i];
-      for (int g = h * a.G; g < (h + 1) * a.G; ++g) {
-        const uint16_t* q = (const uint16_t*)(a.q + row * a.q_node + g * a.q_head);
-        float x = 0.0f;
-        for (int d = 0; d < D; ++d) x = fmaf(to_f32<DT>(q[d]), to_f32<DT>(((const uint16_t*)k)[d]), x);
-        w += expf(x * a.scale - a.lse[row * a.Hq + g]);
+    for (int lr = tid; lr < QB; lr += NT_C) {
+      const int r = q0 + lr;
+      float e = INFINITY;
+      if (r < rows) {
+        const int64_t node = br.first + a.path[b * a.ld_path + r / a.G];
+        e = a.lse[node * a.Hq + h * a.G + r % a.G] * 1.4426950408889634f;
+      }
+      se[lr] = e;
+    }
+    __syncthreads();
+  };
+
+  s16x8 k[4][KS];
+  uint32_t on = 0;                  // bit s: this lane's key of subtile s is there
+  auto load = [&](int from) {
+    on = 0;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int t = from + w * 64 + s * 16 + n;
+      const char* p = nullptr;
+      if (t < br.ctx) {
+        const int64_t at = slot_offset(a.c, tab, t, h);
+        if (at >= 0) p = a.c.k + at;
+      } else if (t < end) {
+        p = a.kn + (int64_t)(br.first + a.path[b * a.ld_path + t - br.ctx]) * a.k_node + h * a.k_head;
+      }
+      on |= (p ? 1u : 0u) << s;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) k[s][ks] = p ? *(const s16x8*)(p + ks * 64 + g4 * 16) : s16x8{};
+    }
+  };
+
+  const int64_t row = ((int64_t)b * a.c.H + h) * a.ld_mass;
+  bool staged = false;
+  for (; base < stop; base += NT_C) {
+    load(base);
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const bool fresh = base + w * 64 + 64 > br.ctx;
+    for (int q0 = 0; q0 < rows; q0 += QB) {
+      if (!staged) stage(q0);
+      staged = rows <= QB;
+      const int tiles = (min(rows - q0, QB) + 15) / 16;
+      for (int rt = 0; rt < tiles; ++rt) {
+        s16x8 q[KS];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const int lr = rt * 16 + n;
+          q[ks] = *(const s16x8*)(sq + lr * (D * 2) + (((ks * 4 + g4) ^ swz<D>(lr)) * 16));
+        }
+        const f32x4 e = *(const f32x4*)(se + rt * 16 + g4 * 4);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) x = mfma<DT>(q[ks], k[s][ks], x);
+          if (fresh) {              // row i sees the appended slots 0 .. i
+            const int j = base + w * 64 + s * 16 + n - br.ctx;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int i = (q0 + rt * 16 + g4 * 4 + r) / a.G;
+              sum[s] += j <= i ? fast_exp2(fmaf(x[r], c, -e[r])) : 0.0f;
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[s] += fast_exp2(fmaf(x[r], c, -e[r]));
+          }
+        }
       }
     }
-    const int64_t at = ((int64_t)b * a.c.H + h) * a.ld_mass + t;
-    if (!fresh && a.decay != 0.0f) w += a.decay * a.mass_in[at];
-    a.mass_out[at] = w;
+    // lane (n, g4) leaves key 16 g4 + n of the wave's 64
+    float mine = 0.0f;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const float v = quad_sum(sum[s]);
+      if (g4 == s) mine = (on >> s & 1) ? v : 0.0f;
+    }
+    const int t = base + w * 64 + l;
+    if (t < stop) {
+      if (t < br.ctx && a.decay != 0.0f) mine = fmaf(a.decay, a.mass_in[row + t], mine);
+      a.mass_out[row + t] = mine;
+    }
   }
 }
 
@@ -324,18 +414,20 @@ extern "C" int sd_cache_commit(const sd_cache_commit_args_t* args, int32_t* out_
     a.Hq = args->H_q, a.G = args->H_q / a.c.H;
     a.scale = args->scale, a.decay = args->decay;
     a.mass_in = args->mass_in;
-    const dim3 grid(std::min((a.c.cap + 255) / 256, 1024), a.c.H, a.c.B);
-    if (args->cache.dtype == SD_BF16) {
-      if (D == 64) hipLaunchKernelGGL((k_commit_mass<SD_BF16, 64>), grid, dim3(256), 0, st, a);
-      else hipLaunchKernelGGL((k_commit_mass<SD_BF16, 128>), grid, dim3(256), 0, st, a);
-    } else {
-      if (D == 64) hipLaunchKernelGGL((k_commit_mass<SD_F16, 64>), grid, dim3(256), 0, st, a);
-      else hipLaunchKernelGGL((k_commit_mass<SD_F16, 128>), grid, dim3(256), 0, st, a);
-    }
-    if (hipGetLastError() != hipSuccess) return SD_EHIP;
   }
-  if (D == 64) hipLaunchKernelGGL(k_commit_append<64>, dim3(a.c.B), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(k_commit_append<128>, dim3(a.c.B), dim3(256), 0, st, a);
+  // Slots of a workgroup: 256 (one tile) unless that makes more than about
+  // 2048 workgroups, since each stages the query rows anew.
+  const int64_t tiles = (a.c.cap + NT_C - 1) / NT_C;
+  const int64_t per = std::max<int64_t>(1, std::min(tiles, tiles * a.c.H * a.c.B / 2048));
+  const int chunk = (int)per * NT_C;
+  const dim3 grid(a.mass_out ? (unsigned)((tiles + per - 1) / per) : 1u, a.c.H, a.c.B);
+  if (args->cache.dtype == SD_BF16) {
+    if (D == 64) hipLaunchKernelGGL((k_commit<SD_BF16, 64>), grid, dim3(NT_C), 0, st, a, chunk);
+    else hipLaunchKernelGGL((k_commit<SD_BF16, 128>), grid, dim3(NT_C), 0, st, a, chunk);
+  } else {
+    if (D == 64) hipLaunchKernelGGL((k_commit<SD_F16, 64>), grid, dim3(NT_C), 0, st, a, chunk);
+    else hipLaunchKernelGGL((k_commit<SD_F16, 128>), grid, dim3(NT_C), 0, st, a, chunk);
+  }
   return hipGetLastError() == hipSuccess ? SD_OK : SD_EHIP;
 }
 
