@@ -147,7 +147,7 @@ typedef struct sd_tree_verify_args {
   int32_t        dtype;
   int32_t        B;
   int32_t        N;
-  int32_t        V;
+  int32_t        V;              /* < 2^28                                      */
   int32_t        max_nodes;
   uint32_t       flags;          /* SD_NO_BONUS                                 */
 } sd_tree_verify_args_t;

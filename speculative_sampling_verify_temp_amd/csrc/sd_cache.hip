@@ -9,8 +9,7 @@
 //   k_evict_select   one workgroup per (request, KV head): the budget-th
 //                    largest key by a radix search, then the freed slots
 //                    below the budget and the kept ones past it, in order;
-//   k_evict_move     16 bytes a lane: each kept row past the budget into its
-//                    freed slot.
+//   k_evict_move     each kept row past the budget into its freed slot.
 #include <algorithm>
 
 #include "sdt_device.h"
@@ -221,7 +220,10 @@ __global__ __launch_bounds__(NT_C, 2) void k_commit(CommitArgs a, int chunk) {
 
 // ---- eviction ----
 
-constexpr int NT_E = 1024;
+constexpr int NT_E = 1024;     // threads of a selection
+constexpr int WE = NT_E / WAVE;
+constexpr int HB = 2048;        // digits of the histogram
+constexpr int MV = 64;         // rows of a move workgroup's round
 
 struct EvictArgs {
   Cache c;
@@ -239,101 +241,216 @@ struct EvictArgs {
 };
 
 // Rank key of a slot: protected positions above every mass, NaN as -inf.
-__device__ __forceinline__ uint32_t evict_key(const EvictArgs& a, int64_t row, int t, int recent_from) {
-  if (a.pos_in) {
-    const int p = a.pos_in[row + t];
-    if (p < a.sinks || p >= recent_from) return 0xFFFFFFFFu;
-  }
-  const float m = a.mass_in[row + t];
+__device__ __forceinline__ uint32_t rank_key(const EvictArgs& a, float m, int p, int recent_from) {
+  if (a.pos_in && (p < a.sinks || p >= recent_from)) return 0xFFFFFFFFu;
   return ord_key(m != m ? -INFINITY : m);
 }
 
+__device__ __forceinline__ uint32_t evict_key(const EvictArgs& a, int64_t row, int t, int recent_from) {
+  return rank_key(a, a.mass_in[row + t], a.pos_in ? a.pos_in[row + t] : 0, recent_from);
+}
+
+// The digit at which the `want` largest keys of the histogram end, and how
+// many keys of that digit belong to them; thread 0 has the highest digits.
+__device__ __forceinline__ void find_digit(const int* hist, int want, int* scratch, int* digit, int* left) {
+  const int top = HB - 1 - 2 * (int)threadIdx.x;
+  const int c0 = hist[2 * top] + hist[2 * top + 1], c1 = hist[2 * top - 2] + hist[2 * top - 1];
+  int total;
+  const int above = block_excl_scan_int<NT_E>(c0 + c1, scratch, &total);
+  if (above < want && want <= above + c0) *digit = top, *left = want - above;
+  if (above + c0 < want && want <= above + c0 + c1) *digit = top - 1, *left = want - above - c0;
+}
+
+// One workgroup per (KV head, request).  The rank keys of up to LCAP slots are
+// kept in LDS, so mass and positions are read once; longer contexts compute
+// them again in each of the 5 to 6 passes.  Bound by what one CU reads (about
+// 30 GB/s) and by LDS atomics: four copies of the histogram keep the lanes of a
+// quad apart.
+template <int LCAP>
 __global__ __launch_bounds__(NT_E) void k_evict_select(EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int scratch[NT_E / WAVE];
+  __shared__ uint32_t keys[LCAP];
+  __shared__ int hist[2 * HB];
   __shared__ int sel[2];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  __shared__ int scratch[WE];
+  __shared__ int counts[3][WE];
+  // slots a thread loads at once, and steps of 64 slots a wave of the last
+  // passes takes at once: more of them only where contexts are long
+  constexpr int UE = LCAP > 4096 ? 16 : 4, UP = LCAP > 4096 ? 8 : 4;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, l = tid % WAVE, w = tid / WAVE;
   uint32_t st = 0;
   const int n = request_ctx(a.c, b, st);
   const int bh = b * a.c.H + h;
   const int64_t row = (int64_t)bh * a.ld;
-  if (st) {
+  if (st || n <= a.budget) {
+    for (int t = tid; t < n; t += NT_E) {
+      if (a.mass_out != a.mass_in) a.mass_out[row + t] = a.mass_in[row + t];
+      if (a.pos_in && a.pos_out != a.pos_in) a.pos_out[row + t] = a.pos_in[row + t];
+    }
     if (tid == 0) a.count[bh] = 0;
     return;
   }
-  const int64_t from = a.pos_in && a.recent > 0 ? (int64_t)a.seen[b] - a.recent : 0x7FFFFFFF;
-  const int recent_from = a.pos_in && a.recent > 0 ? (int)max(from, (int64_t)INT_MIN) : INT_MAX;
-  // the budget-th largest key, eight bits at a time; `want` slots of the
-  // keys equal to it are kept, the lowest
+  const int recent_from = a.pos_in && a.recent > 0
+      ? (int)max((int64_t)a.seen[b] - a.recent, (int64_t)INT_MIN) : INT_MAX;
+  const bool held = n <= LCAP;
+  auto key = [&](int t) { return held ? keys[t] : evict_key(a, row, t, recent_from); };
+
+  // the budget-th largest key, 11, 11 and 10 bits at a time; of the slots
+  // equal to it the lowest `want` are kept
   uint32_t cut = 0;
   int want = a.budget;
-  const bool all = n <= a.budget;
-  for (int shift = 24; !all && shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += NT_E) hist[i] = 0;
+  for (int digit = 0; digit < 3; ++digit) {
+    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+    const uint32_t mask = digit == 2 ? 1023u : 2047u;
+    const int known = digit == 0 ? 31 : digit == 1 ? 21 : 10;      // bits below the digits found
+    for (int i = tid; i < 2 * HB; i += NT_E) hist[i] = 0;
     __syncthreads();
-    for (int t = tid; t < n; t += NT_E) {
-      const uint32_t k = evict_key(a, row, t, recent_from);
-      if (shift == 24 || (k >> (shift + 8)) == (cut >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+    auto count = [&](uint32_t k) {
+      if (digit == 0 || (k >> known) == (cut >> known)) atomicAdd(&hist[((k >> shift) & mask) * 2 + (l & 1)], 1);
+    };
+    if (digit > 0 && held) {
+#pragma unroll 8
+      for (int t = tid; t < n; t += NT_E) count(keys[t]);
+    } else {
+      for (int t0 = tid; t0 < n; t0 += NT_E * UE) {
+        float m[UE];
+        int p[UE];
+#pragma unroll
+        for (int u = 0; u < UE; ++u) {
+          const int t = min(t0 + u * NT_E, n - 1);
+          m[u] = a.mass_in[row + t];
+          p[u] = a.pos_in ? a.pos_in[row + t] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < UE; ++u) {
+          const int t = t0 + u * NT_E;
+          if (t >= n) break;
+          const uint32_t k = rank_key(a, m[u], p[u], recent_from);
+          if (held) keys[t] = k;
+          count(k);
+        }
+      }
     }
     __syncthreads();
-    if (tid == 0) {
-      int w = want, i = 255;
-      while (i > 0 && hist[i] < w) w -= hist[i--];
-      sel[0] = i, sel[1] = w;
-    }
+    find_digit(hist, want, scratch, &sel[0], &sel[1]);
     __syncthreads();
     cut |= (uint32_t)sel[0] << shift;
     want = sel[1];
+  }
+  const int at_cut = (int)(cut & 1023u) * 2;
+  const int equal = hist[at_cut] + hist[at_cut + 1];
+
+  // a contiguous run of slots per wave: ballots order the slots within it,
+  // the waves' counts the runs
+  const int len = ((n + WE - 1) / WE + WAVE - 1) / WAVE * WAVE;
+  const int lo = min(n, w * len), hi = min(n, lo + len);
+  auto before = [&](int which) {
+    int s = 0;
+    for (int i = 0; i < w; ++i) s += counts[which][i];
+    return s;
+  };
+  int eq = 0;
+  if (equal != want) {
+    for (int t0 = lo; t0 < hi; t0 += WAVE) eq += __popcll(__ballot(t0 + l < hi && key(min(t0 + l, n - 1)) == cut));
+    if (l == 0) counts[0][w] = eq;
     __syncthreads();
+    eq = before(0);
   }
-  int equal = 0, holes = 0, late = 0;
-  for (int t0 = 0; t0 < n; t0 += NT_E) {
-    const int t = t0 + tid;
-    uint32_t k = 0;
-    if (t < n) k = evict_key(a, row, t, recent_from);
-    bool keep = t < n && all;
-    if (!all) {
-      int tot;
-      const int e = t < n && k == cut;
-      const int at = equal + block_excl_scan_int<NT_E>(e, scratch, &tot);
-      equal += tot;
-      keep = t < n && (k > cut || (e && at < want));
+  // first the waves' counts of freed and displaced slots, then the lists
+  const uint64_t below = (1ull << l) - 1;
+  int holes = 0, late = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int e = eq, hp = holes, lp = late;
+    const bool copy = pass && a.mass_out != a.mass_in, copy_pos = pass && a.pos_in && a.pos_out != a.pos_in;
+    for (int t1 = lo; t1 < hi; t1 += WAVE * UP) {
+      uint32_t k[UP];
+      float m[UP];
+      int p[UP];
+#pragma unroll
+      for (int u = 0; u < UP; ++u) {
+        const int t = min(t1 + u * WAVE + l, n - 1);
+        k[u] = key(t);
+        m[u] = copy && t1 < a.budget ? a.mass_in[row + t] : 0.0f;
+        p[u] = copy_pos && t1 < a.budget ? a.pos_in[row + t] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < UP; ++u) {
+        const int t = t1 + u * WAVE + l;
+        const bool in = t < hi;
+        bool keep = in && k[u] >= cut;
+        if (equal != want) {
+          const uint64_t same = __ballot(in && k[u] == cut);
+          if (k[u] == cut) keep = in && e + __popcll(same & below) < want;
+          e += __popcll(same);
+        }
+        const bool move = keep && t >= a.budget, hole = in && !keep && t < a.budget;
+        const uint64_t mh = __ballot(hole), ml = __ballot(move);
+        if (pass) {
+          if (hole) a.holes[(int64_t)bh * a.moves + hp + __popcll(mh & below)] = t;
+          if (move) a.late[(int64_t)bh * a.moves + lp + __popcll(ml & below)] = t;
+          if (keep && !move) {
+            if (copy) a.mass_out[row + t] = m[u];
+            if (copy_pos) a.pos_out[row + t] = p[u];
+          }
+        }
+        hp += __popcll(mh);
+        lp += __popcll(ml);
+      }
     }
-    const bool hole = t < n && t < a.budget && !keep, move = keep && t >= a.budget;
-    int tot;
-    const int hp = holes + block_excl_scan_int<NT_E>(hole, scratch, &tot);
-    holes += tot;
-    const int lp = late + block_excl_scan_int<NT_E>(move, scratch, &tot);
-    late += tot;
-    if (hole) a.holes[(int64_t)bh * a.moves + hp] = t;
-    if (move) a.late[(int64_t)bh * a.moves + lp] = t;
-    if (keep && !move) {
-      a.mass_out[row + t] = a.mass_in[row + t];
-      if (a.pos_in) a.pos_out[row + t] = a.pos_in[row + t];
+    if (pass == 0) {
+      if (l == 0) counts[1][w] = hp, counts[2][w] = lp;
+      __syncthreads();
+      holes = before(1), late = before(2);
+    } else if (tid == NT_E - 1) {
+      a.count[bh] = lp;
     }
   }
-  if (tid == 0) a.count[bh] = late;
 }
 
+// Rows of up to MV moves a round: their addresses once into LDS, then all
+// loads of a round before its stores.  Bound by HBM: each moved row is read and
+// written once.
 template <int D>
 __global__ __launch_bounds__(256) void k_evict_move(EvictArgs a) {
-  constexpr int LPR = D / 8;
+  constexpr int LPR = D / 8, RPI = 256 / LPR, IT = MV / RPI;
+  __shared__ int64_t from[MV], to[MV];
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int bh = b * a.c.H + h, n = a.count[bh];
   const int64_t row = (int64_t)bh * a.ld, list = (int64_t)bh * a.moves;
   const int32_t* tab = table_row(a.c, b);
   const int d = (tid % LPR) * 16;
-  for (int i = blockIdx.x * (256 / LPR) + tid / LPR; i < n; i += gridDim.x * (256 / LPR)) {
-    const int src = a.late[list + i], dst = a.holes[list + i];
-    const int64_t s = slot_offset(a.c, tab, src, h), t = slot_offset(a.c, tab, dst, h);
-    if (s >= 0 && t >= 0) {
-      *(uint4*)(a.c.k + t + d) = *(const uint4*)(a.c.k + s + d);
-      *(uint4*)(a.c.v + t + d) = *(const uint4*)(a.c.v + s + d);
+  for (int i0 = blockIdx.x * MV; i0 < n; i0 += gridDim.x * MV) {
+    if (tid < MV) {
+      int64_t s = -1, t = -1;
+      if (i0 + tid < n) {
+        const int src = a.late[list + i0 + tid], dst = a.holes[list + i0 + tid];
+        s = slot_offset(a.c, tab, src, h);
+        t = slot_offset(a.c, tab, dst, h);
+        a.mass_out[row + dst] = a.mass_in[row + src];
+        if (a.pos_in) a.pos_out[row + dst] = a.pos_in[row + src];
+      }
+      from[tid] = t < 0 ? -1 : s;
+      to[tid] = t;
     }
-    if (d == 0) {
-      a.mass_out[row + dst] = a.mass_in[row + src];
-      if (a.pos_in) a.pos_out[row + dst] = a.pos_in[row + src];
+    __syncthreads();
+    uint4 k[IT], v[IT];
+#pragma unroll
+    for (int u = 0; u < IT; ++u) {
+      const int64_t s = from[u * RPI + tid / LPR];
+      k[u] = v[u] = make_uint4(0, 0, 0, 0);
+      if (s >= 0) {
+        k[u] = *(const uint4*)(a.c.k + s + d);
+        v[u] = *(const uint4*)(a.c.v + s + d);
+      }
     }
+#pragma unroll
+    for (int u = 0; u < IT; ++u) {
+      const int64_t t = to[u * RPI + tid / LPR];
+      if (from[u * RPI + tid / LPR] >= 0) {
+        *(uint4*)(a.c.k + t + d) = k[u];
+        *(uint4*)(a.c.v + t + d) = v[u];
+      }
+    }
+    __syncthreads();
   }
   if (h == 0 && blockIdx.x == 0 && tid < WAVE) {
     uint32_t st = 0;
@@ -462,9 +579,13 @@ extern "C" int sd_cache_evict(const sd_cache_evict_args_t* args, void* workspace
   a.out_ctx = out_context;
   a.status = out_status;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(k_evict_select, dim3(a.c.H, a.c.B), dim3(NT_E), 0, st, a);
+  // rank keys in LDS: 16 KB leave room for other workgroups, 136 KB do not
+  if (a.c.cap <= 4096)
+    hipLaunchKernelGGL(k_evict_select<4096>, dim3(a.c.H, a.c.B), dim3(NT_E), 0, st, a);
+  else
+    hipLaunchKernelGGL(k_evict_select<34816>, dim3(a.c.H, a.c.B), dim3(NT_E), 0, st, a);
   if (hipGetLastError() != hipSuccess) return SD_EHIP;
-  const int chunks = std::max(1, std::min((a.moves + 63) / 64, 256));
+  const int chunks = std::max(1, std::min((a.moves + MV - 1) / MV, 1024));
   const dim3 grid(chunks, a.c.H, a.c.B);
   if (args->cache.D == 64) hipLaunchKernelGGL(k_evict_move<64>, grid, dim3(256), 0, st, a);
   else hipLaunchKernelGGL(k_evict_move<128>, grid, dim3(256), 0, st, a);

@@ -1,10 +1,19 @@
 // Greedy verify of a drafted tree on gfx950.
 //
-// Two launches on the caller's stream:
-//   k_tree_argmax  one workgroup per (node row, slice of the vocabulary): the
-//                  slice's maximum and its lowest id as one 64-bit key;
-//   k_tree_walk    one wave per request: from the root, the row's maximum
-//                  over the slices, then the first child with that token.
+// Bound by the bytes of logits read.  Which rows the walk visits is known one
+// row at a time, so there are two ways (rule at walk_rows):
+//   few rows in all    k_tree_argmax finds the maximum of every row, a
+//                      workgroup per (row, slice of the vocabulary), and
+//                      k_tree_walk, one wave per request, follows the tree;
+//   many rows          k_tree_descend, one workgroup per request, reads only
+//                      the rows that its walk visits, one after another.
+//
+// The scan of a row takes 1.5 operations a logit: packed (bf16) or plain (fp32)
+// integer maxima of the raw bits.  As signed numbers they order the values
+// that are not negative and put a positive NaN above +inf; as unsigned ones they
+// order the negative ones downwards and put a negative NaN above -inf.  A thread
+// only keeps which group of its vectors holds its maximum; the token is looked
+// up afterwards by the threads that hold the row's.
 #include <algorithm>
 
 #include "sdt_device.h"
@@ -14,7 +23,9 @@ using namespace sdt;
 
 namespace {
 
-constexpr int NT_A = 256;
+constexpr int NT_A = 256;    // threads of a (row, slice)
+constexpr int NT_D = 1024;   // threads of a walk that reads its own rows
+constexpr int UD = 19;       // vectors a thread of such a walk loads at once: 155648 bf16 logits
 
 struct VerifyArgs {
   const char* logits;
@@ -44,80 +55,223 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t x) {
 }
 
 template <int DT>
-__global__ __launch_bounds__(NT_A) void k_tree_argmax(VerifyArgs a) {
-  constexpr int E = DT == SD_BF16 ? 8 : 4;
-  __shared__ uint64_t sm[NT_A / WAVE];
-  const int row = blockIdx.x, sl = blockIdx.y, tid = threadIdx.x;
-  const char* p = a.logits + row * a.row_bytes;
-  const int nvec = (a.V + E - 1) / E;
-  const int lo = sl * a.slice_vecs, hi = min(nvec, lo + a.slice_vecs);
-  uint64_t best = 0;
-  for (int k = lo + tid; k < hi; k += NT_A) {
-    const uint4 w = reinterpret_cast<const uint4*>(p)[k];
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float z = DT == SD_BF16 ? __uint_as_float(e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16)
-                                    : __uint_as_float(u[e]);
-      const int id = k * E + e;
-      if (id < a.V) {
-        const uint64_t key = arg_key(z, id);
-        best = key > best ? key : best;
-      }
+__device__ __forceinline__ float to_float(const char* row, int i) {
+  if constexpr (DT == SD_BF16) return __uint_as_float((uint32_t)((const uint16_t*)row)[i] << 16);
+  return ((const float*)row)[i];
+}
+
+// Running extremes of raw words: per 16-bit half (bf16) or whole (fp32).
+template <int DT>
+struct Extremes {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  uint32_t smax, umax, umin;
+  __device__ void clear() {
+    constexpr uint32_t NINF = DT == SD_BF16 ? 0xFF80FF80u : 0xFF800000u;
+    smax = umax = umin = NINF;
+  }
+  __device__ void add(uint32_t w) {
+    if constexpr (DT == SD_BF16) {
+      const s16x2 s = __builtin_elementwise_max(__builtin_bit_cast(s16x2, smax), __builtin_bit_cast(s16x2, w));
+      const u16x2 u = __builtin_elementwise_max(__builtin_bit_cast(u16x2, umax), __builtin_bit_cast(u16x2, w));
+      const u16x2 v = __builtin_elementwise_min(__builtin_bit_cast(u16x2, umin), __builtin_bit_cast(u16x2, w));
+      smax = __builtin_bit_cast(uint32_t, s);
+      umax = __builtin_bit_cast(uint32_t, u);
+      umin = __builtin_bit_cast(uint32_t, v);
+    } else {
+      smax = (uint32_t)max((int)smax, (int)w);
+      umax = max(umax, w);
+      umin = min(umin, w);
     }
   }
-  best = wave_max_u64(best);
-  if (tid % WAVE == 0) sm[tid / WAVE] = best;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < NT_A / WAVE; ++w) best = sm[w] > best ? sm[w] : best;
-    a.part[(int64_t)row * a.slices + sl] = best;
+  // Largest value, and whether a NaN was seen.
+  __device__ float value(bool& nan) const {
+    if constexpr (DT == SD_BF16) {
+      const int s = max((int)(short)(smax & 0xFFFF), (int)(short)(smax >> 16));
+      const uint32_t u = max(umax & 0xFFFFu, umax >> 16), v = min(umin & 0xFFFFu, umin >> 16);
+      nan |= s > 0x7F80 || u > 0xFF80u;
+      return __uint_as_float((s >= 0 ? (uint32_t)s : v) << 16);
+    } else {
+      nan |= (int)smax > 0x7F800000 || umax > 0xFF800000u;
+      return __uint_as_float((int)smax >= 0 ? smax : umin);
+    }
   }
+};
+
+// Lowest id in the thread's UG vectors of a group at k0 whose logit is z, or -1.
+template <int DT, int NT, int UG>
+__device__ __forceinline__ int find_in(const uint4 (&w)[UG], int k0, int last, float z) {
+  constexpr int E = DT == SD_BF16 ? 8 : 4;
+  int id = -1;
+#pragma unroll
+  for (int u = UG - 1; u >= 0; --u) {
+    const int k = min(k0 + u * NT + (int)threadIdx.x, last);
+    const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+    for (int e = E - 1; e >= 0; --e) {
+      const float y = DT == SD_BF16 ? __uint_as_float(e & 1 ? q[e / 2] & 0xFFFF0000u : q[e / 2] << 16)
+                                    : __uint_as_float(q[e]);
+      if (y == z) id = k * E + e;
+    }
+  }
+  return id;
 }
+
+template <int NT, int UG>
+__device__ __forceinline__ void load_group(const uint4* row, int k0, int last, uint4 (&w)[UG]) {
+#pragma unroll
+  for (int u = 0; u < UG; ++u) w[u] = row[min(k0 + u * NT + (int)threadIdx.x, last)];
+}
+
+// The maximum of the whole vectors [lo, hi) of a row, and of its last V % E
+// logits if `tail`, with its lowest id, as arg_key, in every thread.  Threads
+// past the end read the last vector again, which changes no maximum.
+// sm: 2 NT / WAVE words.
+template <int DT, int NT, int UG>
+__device__ uint64_t row_best(const char* p, int lo, int hi, int V, bool tail, uint64_t* sm) {
+  constexpr int E = DT == SD_BF16 ? 8 : 4;
+  const uint4* const row = reinterpret_cast<const uint4*>(p);
+  const int tid = threadIdx.x, last = hi - 1;
+  float best = -INFINITY;
+  int at = -1;                  // first vector of the group that holds it, -2: the tail
+  bool nan = false;
+  uint4 w[UG];
+  for (int k0 = lo; k0 < hi; k0 += NT * UG) {
+    load_group<NT, UG>(row, k0, last, w);
+    Extremes<DT> x;
+    x.clear();
+#pragma unroll
+    for (int u = 0; u < UG; ++u) {
+      x.add(w[u].x);
+      x.add(w[u].y);
+      x.add(w[u].z);
+      x.add(w[u].w);
+    }
+    const float z = x.value(nan);
+    if (z > best || at < 0) best = z, at = k0;
+  }
+  if (tail && tid < V % E) {
+    const float z = to_float<DT>(p, V - V % E + tid);
+    nan |= z != z;
+    if (z > best || at < 0) best = z, at = -2;
+  }
+  uint64_t key = at == -1 ? 0 : arg_key(nan ? __builtin_nanf("") : best, 0) & ~0xFFFFFFFFull;
+  uint64_t top = wave_max_u64(key);
+  if (tid % WAVE == 0) sm[tid / WAVE] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NT / WAVE; ++i) top = sm[i] > top ? sm[i] : top;
+  // the holders of the maximum find its first place in their group, which is
+  // still in registers if the row has only one
+  key = key == top ? key : 0;
+  if (key && !nan) {
+    int id;
+    if (at == -2) {
+      id = V - V % E + tid;
+    } else {
+      if (hi - lo > NT * UG) load_group<NT, UG>(row, at, last, w);
+      id = find_in<DT, NT, UG>(w, at, last, best);
+    }
+    key = top | (uint32_t)~id;
+  }
+  key = wave_max_u64(key);
+  sm += NT / WAVE;
+  if (tid % WAVE == 0) sm[tid / WAVE] = key;
+  __syncthreads();
+  key = 0;
+#pragma unroll
+  for (int i = 0; i < NT / WAVE; ++i) key = sm[i] > key ? sm[i] : key;
+  return key;
+}
+
+template <int DT>
+__global__ __launch_bounds__(NT_A) void k_tree_argmax(VerifyArgs a) {
+  constexpr int E = DT == SD_BF16 ? 8 : 4;
+  __shared__ uint64_t sm[2 * NT_A / WAVE];
+  const int row = blockIdx.x, sl = blockIdx.y;
+  const int lo = sl * a.slice_vecs, hi = min(a.V / E, lo + a.slice_vecs);
+  const uint64_t best = row_best<DT, NT_A, 4>(a.logits + row * a.row_bytes, lo, hi, a.V, sl == a.slices - 1, sm);
+  if (threadIdx.x == 0) a.part[(int64_t)row * a.slices + sl] = best;
+}
+
+// The tree of one request in the lanes of a wave: lane l holds node l.
+struct Walk {
+  Nodes nd;
+  uint32_t st;
+  int tok, up;
+  int cur = 0, count = 0, my_path = -1, my_tok = -1;
+
+  __device__ Walk(const VerifyArgs& a, int b) {
+    const int l = threadIdx.x % WAVE;
+    nd = request_nodes(a.off, b, a.N, a.max_nodes);
+    st = nd.T > 0 ? nd.st : SD_ST_BAD_NODES;
+    tok = l < nd.T ? a.tokens[nd.first + l] : -1;
+    up = l < nd.T ? a.parents[nd.first + l] : -1;
+    const bool bad = up < -1 || up >= l;
+    if (bad || l == 0) up = -1;
+    if (__any(bad && l < nd.T)) st |= SD_ST_BAD_TREE;
+    if (__any(l > 0 && l < nd.T && (tok < 0 || tok >= a.V))) st |= SD_ST_BAD_DRAFT_ID;
+  }
+  __device__ bool valid() const { return !(st & SD_ST_TREE_INVALID_MASK); }
+  // Enter the current node; false if its row is not needed.
+  __device__ bool enter(uint32_t flags) {
+    if ((int)(threadIdx.x % WAVE) == count) my_path = cur;
+    return !((flags & SD_NO_BONUS) && __ballot(up == cur) == 0);
+  }
+  // Take its row's maximum; false at the walk's end.  Each step goes to a
+  // higher node: at most T of them.
+  __device__ bool step(uint64_t best) {
+    if ((uint32_t)(best >> 32) == 0xFFFFFFFFu) {
+      st |= SD_ST_NONFINITE;
+      return false;
+    }
+    const int win = (int)~(uint32_t)best;
+    if ((int)(threadIdx.x % WAVE) == count) my_tok = win;
+    const uint64_t next = __ballot(up == cur && tok == win);
+    if (next == 0) return false;
+    cur = __builtin_ctzll(next);
+    ++count;
+    return true;
+  }
+  __device__ void write(const VerifyArgs& a, int b) const {
+    const int l = threadIdx.x % WAVE;
+    const bool bad = !valid();
+    if (l < a.max_nodes) {
+      a.path[(int64_t)b * a.max_nodes + l] = bad ? -1 : my_path;
+      a.out_tokens[(int64_t)b * a.max_nodes + l] = bad ? -1 : my_tok;
+    }
+    if (l == 0) {
+      a.accepted[b] = bad ? -1 : count;
+      if (a.status) a.status[b] = st;
+    }
+  }
+};
 
 __global__ __launch_bounds__(WAVE) void k_tree_walk(VerifyArgs a) {
   const int b = blockIdx.x, l = threadIdx.x;
-  const Nodes nd = request_nodes(a.off, b, a.N, a.max_nodes);
-  uint32_t st = nd.T > 0 ? nd.st : SD_ST_BAD_NODES;
-  const int tok = l < nd.T ? a.tokens[nd.first + l] : -1;
-  int up = l < nd.T && l > 0 ? a.parents[nd.first + l] : -1;
-  bool bad_tree = l < nd.T && (l > 0 ? up < -1 || up >= l : a.parents[nd.first] < -1 || a.parents[nd.first] >= 0);
-  if (up < -1 || up >= l) up = -1;
-  if (__any(bad_tree)) st |= SD_ST_BAD_TREE;
-  if (__any(l > 0 && l < nd.T && (tok < 0 || tok >= a.V))) st |= SD_ST_BAD_DRAFT_ID;
-  int cur = 0, count = 0, my_path = -1, my_tok = -1;
-  if (!(st & SD_ST_TREE_INVALID_MASK)) {
-    for (;;) {      // each step goes to a higher node: at most T steps
-      const uint64_t kids = __ballot(up == cur);
-      if (l == count) my_path = cur;
-      if ((a.flags & SD_NO_BONUS) && kids == 0) break;
-      uint64_t best = 0;
-      for (int s = l; s < a.slices; s += WAVE) {
-        const uint64_t k = a.part[(int64_t)(nd.first + cur) * a.slices + s];
-        best = k > best ? k : best;
-      }
-      best = wave_max_u64(best);
-      if ((uint32_t)(best >> 32) == 0xFFFFFFFFu) {
-        st |= SD_ST_NONFINITE;
-        break;
-      }
-      const int win = (int)~(uint32_t)best;
-      if (l == count) my_tok = win;
-      const uint64_t next = __ballot(up == cur && tok == win);
-      if (next == 0) break;
-      cur = __builtin_ctzll(next);
-      ++count;
+  Walk w(a, b);
+  while (w.valid() && w.enter(a.flags)) {
+    uint64_t best = 0;
+    for (int s = l; s < a.slices; s += WAVE) {
+      const uint64_t k = a.part[(int64_t)(w.nd.first + w.cur) * a.slices + s];
+      best = k > best ? k : best;
     }
+    if (!w.step(wave_max_u64(best))) break;
   }
-  const bool bad = st & SD_ST_TREE_INVALID_MASK;
-  if (l < a.max_nodes) {
-    a.path[(int64_t)b * a.max_nodes + l] = bad ? -1 : my_path;
-    a.out_tokens[(int64_t)b * a.max_nodes + l] = bad ? -1 : my_tok;
+  w.write(a, b);
+}
+
+template <int DT>
+__global__ __launch_bounds__(NT_D) void k_tree_descend(VerifyArgs a) {
+  constexpr int E = DT == SD_BF16 ? 8 : 4;
+  __shared__ uint64_t sm[2 * NT_D / WAVE];
+  const int b = blockIdx.x;
+  Walk w(a, b);      // every wave walks along
+  while (w.valid() && w.enter(a.flags)) {
+    const char* row = a.logits + (int64_t)(w.nd.first + w.cur) * a.row_bytes;
+    if (!w.step(row_best<DT, NT_D, UD>(row, 0, a.V / E, a.V, true, sm))) break;
   }
-  if (l == 0) {
-    a.accepted[b] = bad ? -1 : count;
-    if (a.status) a.status[b] = st;
-  }
+  if (threadIdx.x < WAVE) w.write(a, b);
 }
 
 int check(const sd_tree_verify_args_t* p) {
@@ -128,7 +282,7 @@ int check(const sd_tree_verify_args_t* p) {
   if (p->B < 1 || p->N < 1 || p->V < 1 || p->max_nodes < 1 || p->ld < p->V || (p->ld * es) % 16 ||
       (p->flags & ~(uint32_t)SD_NO_BONUS))
     return SD_EINVAL;
-  if (p->max_nodes > SD_MAX_NODES || p->V >= (1 << 30) || p->N > (1 << 24)) return SD_EUNSUPPORTED;
+  if (p->max_nodes > SD_MAX_NODES || p->V >= (1 << 28) || p->N > (1 << 24)) return SD_EUNSUPPORTED;
   return SD_OK;
 }
 
@@ -136,6 +290,16 @@ int check(const sd_tree_verify_args_t* p) {
 // vectors.
 int slice_count(int N, int nvec) {
   return std::max(1, std::min({(2048 + N - 1) / N, (nvec + 511) / 512, 64}));
+}
+
+// Whether to read only the rows that the walks visit.  One workgroup reads a
+// row at about 70 GB/s, a full chip at about 4.5 TB/s, and a step of a walk
+// costs about 2 us beside its bytes: reading all N rows takes longer than a walk
+// of d + 1 rows when N > (d + 1) (64 + 9 MB / row).  Walks are rarely deeper than
+// 16 (a deeper one costs at most four times what reading all rows would).
+bool walk_rows(const sd_tree_verify_args_t* p) {
+  const int64_t row = (int64_t)p->V * (p->dtype == SD_BF16 ? 2 : 4);
+  return p->N * row > std::min(p->max_nodes, 16) * (64 * row + (9 << 20));
 }
 
 }  // namespace
@@ -170,6 +334,13 @@ extern "C" int sd_tree_verify_greedy(const sd_tree_verify_args_t* args, void* wo
   a.part = static_cast<uint64_t*>(workspace);
   a.accepted = out_accepted, a.path = out_path, a.out_tokens = out_tokens, a.status = out_status;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (walk_rows(args)) {
+    if (args->dtype == SD_BF16)
+      hipLaunchKernelGGL(k_tree_descend<SD_BF16>, dim3(a.B), dim3(NT_D), 0, st, a);
+    else
+      hipLaunchKernelGGL(k_tree_descend<SD_F32>, dim3(a.B), dim3(NT_D), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SD_OK : SD_EHIP;
+  }
   if (args->dtype == SD_BF16)
     hipLaunchKernelGGL(k_tree_argmax<SD_BF16>, dim3(a.N, a.slices), dim3(NT_A), 0, st, a);
   else

@@ -249,14 +249,14 @@ def test_evict_leaves_a_request_of_wrong_length_alone():
 
 
 def test_long_caches_against_sorting():
-    """32768 slots to 5000, random and with many equal weights: the survivors
-    against a stable sort on the device."""
+    """32768 and 40000 slots (more than LDS holds) to 5000, random and with many
+    equal weights: the survivors against a stable sort on the device."""
     import torch
     sdv = _sdv()
     g = torch.Generator(device="cuda")
     g.manual_seed(3)
-    B, H, D, page, n, budget = 2, 2, 64, 64, 32768, 5000
-    for equal in (False, True):
+    B, H, D, page, budget = 2, 2, 64, 64, 5000
+    for n, equal in ((32768, False), (32768, True), (40000, False), (40000, True)):
         k = torch.randn((B * n // page, H, page, D), generator=g, device="cuda").to(torch.bfloat16)
         v = -k
         table = torch.randperm(B * n // page, generator=g, device="cuda").to(torch.int32).reshape(B, -1)

@@ -32,7 +32,9 @@ def _agreeing(rng, z, parents, offsets, depth):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("nodes,V", [([1], 1), ([3, 1, 64], 7), ([5, 9, 2], 1000), ([64] * 70, 333), ([16, 33], 20011),
-                                     ([2, 7], 152064), ([8] * 300, 2050), ([1, 4] * 40, 9001)])
+                                     ([2, 7], 152064), ([8] * 300, 2050), ([1, 4] * 40, 9001),
+                                     # enough rows that only the visited ones are read
+                                     ([1] * 300, 20011), ([4, 2, 3, 1] * 150, 30001), ([9] * 260, 20011)])
 def test_walks_match_the_oracle(nodes, V, dtype):
     rng = np.random.default_rng(len(nodes) + V)
     off = np.concatenate([[0], np.cumsum(nodes)]).astype(np.int32)
@@ -53,7 +55,7 @@ def test_walks_match_the_oracle(nodes, V, dtype):
             assert np.array_equal(g.cpu().numpy(), w), name
 
 
-@pytest.mark.parametrize("B", [1, 90])
+@pytest.mark.parametrize("B", [1, 90, 1200])
 def test_a_deep_chain_is_walked_to_its_end(B):
     rng = np.random.default_rng(2)
     T, V = 64, 516
@@ -67,7 +69,7 @@ def test_a_deep_chain_is_walked_to_its_end(B):
     assert np.array_equal(tok.cpu().numpy(), z.argmax(1).reshape(B, T))
 
 
-@pytest.mark.parametrize("copies", [1, 60])
+@pytest.mark.parametrize("copies", [1, 60, 520])
 def test_defects_are_reported_request_by_request(copies):
     import torch
     sdv = _sdv()
@@ -109,7 +111,7 @@ def test_verify_in_a_graph():
     import torch
     sdv = _sdv()
     rng = np.random.default_rng(4)
-    for B in (2, 100):
+    for B in (2, 100, 700):
         T, V = 6, 5000
         parents = np.concatenate([random_tree(rng, T) for _ in range(B)]).astype(np.int32)
         off = (np.arange(B + 1) * T).astype(np.int32)
