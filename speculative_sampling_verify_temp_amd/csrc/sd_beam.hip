@@ -1,10 +1,16 @@
 // Beam selection over a vocabulary and reordering of beam states on gfx950.
 //
-// k_beam_rows    one workgroup per (beam, slice of the vocabulary): the
-//                slice's maximum, its sum of exponentials, and its n_out best
-//                logits in order (larger logit, then lower id);
+// k_beam_rows    one workgroup per (beam, slice of the vocabulary), the slice in
+//                registers: its maximum, its sum of exponentials and its n_out
+//                best logits in order (larger logit, then lower id);
 // k_beam_merge   one workgroup per request: each beam's log-sum-exp from its
-//                slices, the candidates' scores in 64 bits, the n_out best;
+//                slices, the candidates' scores in 64 bits, the n_out best.
+//
+// Both choose the n best of many in the same way: the n-th largest of 64 maxima,
+// of the values of 4 threads each, bounds the n-th largest of all from below, so
+// only the values not below it (about n, 300 at n = 64) are listed and ranked by
+// counting the larger ones.  Where ties make that list overflow the best are
+// taken one by one.
 // k_beam_reorder one thread per 16-byte column of a state row: the column of
 //                every source beam that another beam takes over is read
 //                before any is written, so the rows permute in place.
@@ -18,14 +24,9 @@ using namespace sdt;
 namespace {
 
 constexpr int NT_B = 256;
+constexpr int NV = 8;            // 16-byte vectors of a thread's part of a slice
+constexpr int LIST = 1024;       // places for the values not below the bound
 constexpr int MAXO = SD_MAX_BEAMS;
-
-struct SliceOut {
-  float m;        // maximum, NaN where the slice holds a NaN or +inf
-  float pad;
-  double s;       // sum of exp(z - m)
-  uint64_t best[MAXO];   // ord_key(z) << 32 | ~id, descending; 0: none
-};
 
 struct BeamArgs {
   const char* logits;
@@ -33,7 +34,9 @@ struct BeamArgs {
   const float* scores;
   const uint8_t* ended;
   int B, W, V, n_out, eos, slices, slice_vecs;
-  SliceOut* part;   // [B * W][slices]
+  float* part_m;       // [B * W][slices] maximum, NaN where the slice holds a NaN or +inf
+  double* part_s;      // sum of exp(z - maximum)
+  uint64_t* part_best; // [B * W][slices][n_out]: ord_key(z) << 32 | ~id, descending; 0: none
   float* out_scores;
   int32_t *out_parents, *out_tokens;
   uint8_t* out_ended;
@@ -42,15 +45,6 @@ struct BeamArgs {
 
 __device__ __forceinline__ bool examined(const BeamArgs& a, int bw) {
   return !(a.ended && a.ended[bw]) && a.scores[bw] > -INFINITY;
-}
-
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t x) {
-#pragma unroll
-  for (int o = WAVE / 2; o > 0; o >>= 1) {
-    const uint64_t y = __shfl_xor(x, o);
-    x = y > x ? y : x;
-  }
-  return x;
 }
 
 __device__ __forceinline__ uint64_t block_max_u64(uint64_t x, uint64_t* scratch) {
@@ -62,49 +56,165 @@ __device__ __forceinline__ uint64_t block_max_u64(uint64_t x, uint64_t* scratch)
   return x;
 }
 
-template <int DT>
-__device__ __forceinline__ float logit(const char* row, int i) {
-  if constexpr (DT == SD_BF16) return __uint_as_float((uint32_t)((const uint16_t*)row)[i] << 16);
-  return ((const float*)row)[i];
+__device__ __forceinline__ uint32_t quad_lanes_max(uint32_t x) {
+  x = max(x, (uint32_t)dpp_i32<DPP_XOR1>((int)x));
+  return max(x, (uint32_t)dpp_i32<DPP_XOR2>((int)x));
+}
+__device__ __forceinline__ uint64_t quad_lanes_max(uint64_t x) {
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    const uint64_t y = __shfl_xor(x, o);
+    x = y > x ? y : x;
+  }
+  return x;
 }
 
+// The n-th largest (n <= 64) of the maxima of groups of 4 threads, in every
+// thread; keys: 64 of LDS.  Every wave ranks the 64 by counting.
+template <typename K>
+__device__ __forceinline__ K nth_group_max(K mine, int n, K* keys) {
+  static_assert(NT_B == 4 * WAVE, "64 groups of 4 threads");
+  const int tid = threadIdx.x, l = tid % WAVE;
+  mine = quad_lanes_max(mine);
+  if (tid % 4 == 0) keys[tid / 4] = mine;
+  __syncthreads();
+  const K k = keys[l];
+  int rank = 0;
+#pragma unroll
+  for (int i = 0; i < WAVE; ++i) {
+    const K o = keys[i];
+    rank += o > k || (o == k && i < l);
+  }
+  const int at = __builtin_ctzll(__ballot(rank == n - 1));
+  if constexpr (sizeof(K) == 4) return (K)lane_read((int)k, at);
+  return ((uint64_t)(uint32_t)lane_read((int)(uint32_t)(k >> 32), at) << 32) | (uint32_t)lane_read((int)(uint32_t)k, at);
+}
+
+// Logit e of a 16-byte vector.
 template <int DT>
-__global__ __launch_bounds__(NT_B) void k_beam_rows(BeamArgs a) {
+__device__ __forceinline__ float logit_of(const uint4& w, int e) {
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+  if constexpr (DT == SD_BF16) return __uint_as_float(e & 1 ? q[e / 2] & 0xFFFF0000u : q[e / 2] << 16);
+  return __uint_as_float(q[e]);
+}
+
+// Bound by HBM: a logit is read once, and its exponential costs about 8
+// operations, half of the time its bytes take.
+template <int DT>
+__global__ __launch_bounds__(NT_B, 4) void k_beam_rows(BeamArgs a) {
   constexpr int E = DT == SD_BF16 ? 8 : 4;
   __shared__ float sf[NT_B / WAVE];
   __shared__ double sd[NT_B / WAVE];
-  __shared__ int si[NT_B / WAVE];
   __shared__ uint64_t su[NT_B / WAVE];
+  __shared__ __align__(16) uint32_t keys[WAVE];
+  __shared__ uint64_t list[LIST];
+  __shared__ int listed;
   const int bw = blockIdx.x, sl = blockIdx.y, tid = threadIdx.x;
   if (!examined(a, bw)) return;
-  const char* row = a.logits + bw * a.row_bytes;
-  const int lo = sl * a.slice_vecs * E, hi = min(a.V, lo + a.slice_vecs * E);
-  SliceOut& out = a.part[(int64_t)bw * a.slices + sl];
-  float m = -INFINITY;
-  int bad = 0;
-  for (int i = lo + tid; i < hi; i += NT_B) {
-    const float z = logit<DT>(row, i);
-    bad |= nonfinite(z);
-    m = fmaxf(m, z);
+  const int64_t out = (int64_t)bw * a.slices + sl;
+  const uint4* const row = reinterpret_cast<const uint4*>(a.logits + bw * a.row_bytes);
+  const int nvec = (a.V + E - 1) / E, lo = sl * a.slice_vecs, hi = min(nvec, lo + a.slice_vecs);
+  const int mine = (hi - lo + NT_B - 1) / NT_B;      // vectors a thread takes
+  if (tid == 0) listed = 0;
+  uint4 w[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    w[u] = make_uint4(0, 0, 0, 0);
+    if (u < mine) w[u] = row[min(lo + u * NT_B + tid, hi - 1)];
   }
-  bad = block_or<NT_B>(bad, si);
-  m = block_max<NT_B>(m, sf);
-  double s = 0.0;
-  if (!bad && m > -INFINITY)
-    for (int i = lo + tid; i < hi; i += NT_B) s += (double)expf(logit<DT>(row, i) - m);
-  s = block_sum<NT_B>(s, sd);
-  if (tid == 0) out.m = bad ? __builtin_nanf("") : m, out.s = s;
+  // past the end: -inf, which is no candidate and adds nothing
+  constexpr uint32_t NINF = DT == SD_BF16 ? 0xFF80FF80u : 0xFF800000u;
+  const bool tail = hi == nvec && a.V % E != 0;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int k = lo + u * NT_B + tid;
+    if (u >= mine || k >= hi) {
+      w[u] = make_uint4(NINF, NINF, NINF, NINF);
+    } else if (tail && k == nvec - 1) {
+      uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (k * E + e >= a.V) {
+          if constexpr (DT == SD_BF16)
+            q[e / 2] = e & 1 ? (q[e / 2] & 0xFFFFu) | 0xFF800000u : (q[e / 2] & 0xFFFF0000u) | 0xFF80u;
+          else
+            q[e] = NINF;
+        }
+      w[u] = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+  }
+  Extremes<DT> x;
+  x.clear();
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    x.add(w[u].x);
+    x.add(w[u].y);
+    x.add(w[u].z);
+    x.add(w[u].w);
+  }
+  bool nan = false;
+  const float top = x.value(nan);
+  // a NaN or +inf anywhere makes the maximum +inf
+  const float m = block_max<NT_B>(nan ? INFINITY : top, sf);
+  if (m == INFINITY) {
+    if (tid == 0) a.part_m[out] = __builtin_nanf("");
+    return;
+  }
+  constexpr float C = 1.4426950408889634f;
+  float s = 0.0f;
+  if (m > -INFINITY) {
+    const float g = m * C;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (u < mine) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += fast_exp2(fmaf(logit_of<DT>(w[u], e), C, -g));
+      }
+  }
+  // at most 64 terms of at most 1 in fp32, the rest in 64 bits
+  const double total = block_sum<NT_B>((double)s, sd);
+  if (tid == 0) a.part_m[out] = m, a.part_s[out] = total;
+
+  uint64_t* const best = a.part_best + out * a.n_out;
+  const uint32_t floor = ord_key(-INFINITY);         // not a candidate
+  const uint32_t edge = nth_group_max(ord_key(top), a.n_out, keys);
+  if (ord_key(top) >= edge && top > -INFINITY) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t o = ord_key(logit_of<DT>(w[u], e));
+        if (o >= edge && o > floor) {
+          const int at = atomicAdd(&listed, 1);
+          if (at < LIST) list[at] = ((uint64_t)o << 32) | (uint32_t)~((lo + u * NT_B + tid) * E + e);
+        }
+      }
+  }
+  __syncthreads();
+  const int n = listed;
+  if (n <= LIST) {
+    for (int i = tid; i < n; i += NT_B) {
+      const uint64_t k = list[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += list[j] > k;
+      if (rank < a.n_out) best[rank] = k;
+    }
+    for (int j = n + tid; j < a.n_out; j += NT_B) best[j] = 0;
+    return;
+  }
   uint64_t last = ~0ull;
   for (int j = 0; j < a.n_out; ++j) {
-    uint64_t best = 0;
-    for (int i = lo + tid; !bad && i < hi; i += NT_B) {
-      const float z = logit<DT>(row, i);
-      const uint64_t k = z > -INFINITY ? ((uint64_t)ord_key(z) << 32) | (uint32_t)~i : 0;
-      if (k < last && k > best) best = k;
-    }
-    last = block_max_u64(best, su);
-    if (tid == 0) out.best[j] = last;
-    if (last == 0) last = 1;   // nothing is below: the rest of the list is empty
+    uint64_t b = 0;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t o = ord_key(logit_of<DT>(w[u], e));
+        const uint64_t k = ((uint64_t)o << 32) | (uint32_t)~((lo + u * NT_B + tid) * E + e);
+        if (o > floor && k < last && k > b) b = k;
+      }
+    last = block_max_u64(b, su);
+    if (tid == 0) best[j] = last;
   }
 }
 
@@ -114,75 +224,124 @@ __device__ __forceinline__ uint64_t ord64(double x) {
   return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
+__device__ __forceinline__ double from_ord64(uint64_t o) {
+  return __longlong_as_double((long long)((o >> 63) ? o & ~(1ull << 63) : ~o));
+}
+
 __device__ __forceinline__ float from_ord32(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
 }
 
+// A candidate: its score as a key, and ~(beam << 32 | token), so that the better
+// of two is the larger pair; s = 0: none.
+struct Candidate {
+  uint64_t s, i;
+  __device__ bool over(const Candidate& o) const { return s > o.s || (s == o.s && i > o.i); }
+};
+
 __global__ __launch_bounds__(NT_B) void k_beam_merge(BeamArgs a) {
   __shared__ double lse[MAXO];
+  __shared__ uint8_t kind[MAXO];      // 0: no candidates, 1: its slices', 2: ended
   __shared__ uint32_t st_sh;
-  __shared__ uint64_t su[NT_B / WAVE];
-  const int b = blockIdx.x, tid = threadIdx.x;
-  if (tid == 0) st_sh = 0;
+  __shared__ __align__(16) uint64_t keys[WAVE];
+  __shared__ uint64_t su[NT_B / WAVE], list_s[LIST], list_i[LIST];
+  __shared__ float score[MAXO];
+  __shared__ int listed;
+  const int b = blockIdx.x, tid = threadIdx.x, l = tid % WAVE;
+  if (tid == 0) st_sh = 0, listed = 0;
   __syncthreads();
-  if (tid < a.W) {
-    const int bw = b * a.W + tid;
+  for (int w = tid / WAVE; w < a.W; w += NT_B / WAVE) {
+    const int bw = b * a.W + w;
     const float sc = a.scores[bw];
     uint32_t st = 0;
     double e = 0.0;
+    const int kd = !(sc > -INFINITY) ? 0 : a.ended && a.ended[bw] ? 2 : 1;
     if (sc != sc || sc == INFINITY) st |= SD_ST_BAD_PARAM;
-    else if (examined(a, bw)) {
-      const SliceOut* p = a.part + (int64_t)bw * a.slices;
+    if (kd == 1 && !st) {
+      const float* pm = a.part_m + (int64_t)bw * a.slices;
+      const double* ps = a.part_s + (int64_t)bw * a.slices;
       float m = -INFINITY;
-      for (int s = 0; s < a.slices; ++s) {
-        if (p[s].m != p[s].m) st |= SD_ST_NONFINITE;
-        m = fmaxf(m, p[s].m);
+      bool bad = false;
+      for (int s = l; s < a.slices; s += WAVE) {
+        bad |= pm[s] != pm[s];
+        m = fmaxf(m, pm[s]);
       }
-      if (!(m > -INFINITY)) st |= SD_ST_NONFINITE;
-      double z = 0.0;
-      for (int s = 0; s < a.slices; ++s)
-        if (p[s].s > 0.0) z += p[s].s * exp((double)p[s].m - (double)m);
-      e = (double)m + log(z);
+      m = wave_max(m);
+      if (__any(bad) || !(m > -INFINITY)) st |= SD_ST_NONFINITE;
+      else {
+        double z = 0.0;
+        for (int s = l; s < a.slices; s += WAVE)
+          if (pm[s] > -INFINITY) z += ps[s] * exp((double)pm[s] - (double)m);
+        e = (double)m + log(wave_sum(z));
+      }
     }
-    lse[tid] = e;
-    if (st) atomicOr(&st_sh, st);
+    if (l == 0) {
+      lse[w] = e, kind[w] = (uint8_t)kd, score[w] = sc;
+      if (st) atomicOr(&st_sh, st);
+    }
   }
   __syncthreads();
   const bool bad = st_sh != 0;
-  const int total = bad ? 0 : a.W * a.slices * a.n_out;
-  uint64_t last_s = ~0ull, last_i = 0;   // the candidate chosen before, by score and then by place
-  for (int j = 0; j < a.n_out; ++j) {
-    uint64_t bs = 0, bi = 0;             // score key and ~place of the best below it
-    double bx = -INFINITY;
-    for (int c = tid; c < total; c += NT_B) {
-      const int w = c / (a.slices * a.n_out), r = c % (a.slices * a.n_out), bw = b * a.W + w;
-      double x;
-      int id;
-      if (a.ended && a.ended[bw]) {
-        if (r) continue;
-        x = a.scores[bw], id = a.eos;
-      } else {
-        if (!examined(a, bw)) continue;
-        const uint64_t k = a.part[(int64_t)bw * a.slices + r / a.n_out].best[r % a.n_out];
-        if (k == 0) continue;
+  const int per = a.slices * a.n_out, total = bad ? 0 : a.W * per;
+  auto candidate = [&](int c) {
+    const int w = c / per, r = c % per;
+    Candidate x{0, 0};
+    double sc = -INFINITY;
+    int id = a.eos;
+    if (kind[w] == 2) {
+      if (r == 0) sc = score[w];
+    } else if (kind[w] == 1) {
+      const uint64_t k = a.part_best[(int64_t)b * a.W * per + c];
+      if (k) {
         id = (int)~(uint32_t)k;
-        x = (double)a.scores[bw] + ((double)from_ord32((uint32_t)(k >> 32)) - lse[w]);
+        sc = (double)score[w] + ((double)from_ord32((uint32_t)(k >> 32)) - lse[w]);
       }
-      if (!(x > -INFINITY)) continue;
-      const uint64_t s = ord64(x), i = ~((uint64_t)w << 32 | (uint32_t)id);
-      if (s > last_s || (s == last_s && i >= last_i)) continue;
-      if (s > bs || (s == bs && i > bi)) bs = s, bi = i, bx = x;
     }
-    const uint64_t s = block_max_u64(bs, su);
-    const uint64_t i = block_max_u64(bs == s ? bi : 0, su);
-    last_s = s, last_i = i;
+    if (sc > -INFINITY) x.s = ord64(sc), x.i = ~((uint64_t)w << 32 | (uint32_t)id);
+    return x;
+  };
+  auto put = [&](int j, const Candidate& x) {
     const int o = b * a.n_out + j;
-    if (s == 0 ? tid == 0 : (bs == s && bi == i)) {
-      const int w = s ? (int)(~i >> 32) : -1, id = s ? (int)(uint32_t)~i : -1;
-      a.out_scores[o] = s ? (float)bx : -INFINITY;
-      a.out_parents[o] = w;
-      a.out_tokens[o] = id;
-      if (a.out_ended) a.out_ended[o] = s && ((a.ended && a.ended[b * a.W + w]) || id == a.eos);
+    const int w = x.s ? (int)(~x.i >> 32) : -1, id = x.s ? (int)(uint32_t)~x.i : -1;
+    a.out_scores[o] = x.s ? (float)from_ord64(x.s) : -INFINITY;
+    a.out_parents[o] = w;
+    a.out_tokens[o] = id;
+    if (a.out_ended) a.out_ended[o] = x.s && (kind[w] == 2 || id == a.eos);
+  };
+  uint64_t top = 0;
+  for (int c = tid; c < total; c += NT_B) top = max(top, candidate(c).s);
+  const uint64_t edge = nth_group_max(top, a.n_out, keys);
+  if (top >= edge && top) {
+    for (int c = tid; c < total; c += NT_B) {
+      const Candidate x = candidate(c);
+      if (x.s >= edge && x.s) {
+        const int at = atomicAdd(&listed, 1);
+        if (at < LIST) list_s[at] = x.s, list_i[at] = x.i;
+      }
+    }
+  }
+  __syncthreads();
+  const int n = listed;
+  if (n <= LIST) {
+    for (int i = tid; i < n; i += NT_B) {
+      const Candidate x{list_s[i], list_i[i]};
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += Candidate{list_s[j], list_i[j]}.over(x);
+      if (rank < a.n_out) put(rank, x);
+    }
+    for (int j = n + tid; j < a.n_out; j += NT_B) put(j, Candidate{0, 0});
+  } else {
+    Candidate last{~0ull, ~0ull};
+    for (int j = 0; j < a.n_out; ++j) {
+      Candidate best{0, 0};
+      for (int c = tid; c < total; c += NT_B) {
+        const Candidate x = candidate(c);
+        if (last.over(x) && x.over(best)) best = x;
+      }
+      const uint64_t s = block_max_u64(best.s, su);
+      const uint64_t i = block_max_u64(best.s == s ? best.i : 0, su);
+      last = Candidate{s, i};
+      if (tid == 0) put(j, last);
     }
   }
   if (tid == 0 && a.status) a.status[b] = st_sh;
@@ -197,25 +356,35 @@ struct ReorderArgs {
   int layers, B, W_in, W_out, segs, max_units;
 };
 
+// One 16-byte column of all beams a thread, in registers between its loads and
+// its stores; WM bounds the beams, so that they are registers.
+template <int WM>
 __global__ __launch_bounds__(256) void k_beam_reorder(ReorderArgs a) {
-  __shared__ int par[MAXO];
+  __shared__ int par[WM];
   const int b = blockIdx.y, ls = blockIdx.z, layer = ls / a.segs, seg = ls % a.segs;
-  if (threadIdx.x < a.W_out) {
-    const int p = a.parents[b * a.W_out + threadIdx.x];
-    par[threadIdx.x] = p >= 0 && p < a.W_in ? p : -1;
+  const bool same = a.in == a.out;
+  if ((int)threadIdx.x < WM) {
+    const int w = threadIdx.x, p = w < a.W_out ? a.parents[b * a.W_out + w] : -1;
+    par[w] = p >= 0 && p < a.W_in && !(same && p == w) ? p : -1;     // -1: nothing to move
   }
   __syncthreads();
   const int len = a.lengths ? min(max(a.lengths[b], 0), a.max_units) : a.max_units;
   const int64_t cols = len * a.unit / 16;
-  const bool same = a.in == a.out;
   const char* src = a.in + layer * a.in_layer + b * a.in_request + seg * a.in_seg;
   char* dst = a.out + layer * a.out_layer + b * a.out_request + seg * a.out_seg;
   for (int64_t c = blockIdx.x * 256 + threadIdx.x; c < cols; c += gridDim.x * 256) {
-    uint4 v[MAXO];
-    for (int w = 0; w < a.W_out; ++w)
-      if (par[w] >= 0 && !(same && par[w] == w)) v[w] = *(const uint4*)(src + par[w] * a.in_beam + c * 16);
-    for (int w = 0; w < a.W_out; ++w)
-      if (par[w] >= 0 && !(same && par[w] == w)) *(uint4*)(dst + w * a.out_beam + c * 16) = v[w];
+    uint4 v[WM];
+#pragma unroll
+    for (int w = 0; w < WM; ++w) {
+      const int p = __builtin_amdgcn_readfirstlane(par[w]);
+      v[w] = make_uint4(0, 0, 0, 0);
+      if (p >= 0) v[w] = *(const uint4*)(src + p * a.in_beam + c * 16);
+    }
+#pragma unroll
+    for (int w = 0; w < WM; ++w) {
+      const int p = __builtin_amdgcn_readfirstlane(par[w]);
+      if (p >= 0) *(uint4*)(dst + w * a.out_beam + c * 16) = v[w];
+    }
   }
 }
 
@@ -230,8 +399,29 @@ int check(const sd_beam_select_args_t* p) {
   return SD_OK;
 }
 
-int slice_count(int rows, int nvec) {
-  return std::max(1, std::min({(1024 + rows - 1) / rows, (nvec + 511) / 512, 64}));
+// Vectors of a slice: one per thread until that makes more than about 1024
+// workgroups, at most NV.
+int slice_vectors(int rows, int nvec) {
+  const int64_t per = ((int64_t)rows * nvec / 1024 + NT_B - 1) / NT_B;
+  return NT_B * (int)std::clamp<int64_t>(per, 1, NV);
+}
+
+struct BeamLayout {
+  int slice_vecs, slices;
+  size_t m, s, best, total;    // byte offsets
+};
+
+BeamLayout layout(const sd_beam_select_args_t* p) {
+  const int E = p->dtype == SD_BF16 ? 8 : 4, nvec = (p->V + E - 1) / E, rows = p->B * p->W;
+  BeamLayout L;
+  L.slice_vecs = slice_vectors(rows, nvec);
+  L.slices = (nvec + L.slice_vecs - 1) / L.slice_vecs;
+  const size_t n = (size_t)rows * L.slices;
+  L.best = 0;
+  L.s = n * p->n_out * 8;
+  L.m = L.s + n * 8;
+  L.total = L.m + n * 4;
+  return L;
 }
 
 }  // namespace
@@ -240,8 +430,7 @@ extern "C" int sd_beam_select_workspace_bytes(const sd_beam_select_args_t* args,
   if (!bytes) return SD_EINVAL;
   const int rc = check(args);
   if (rc) return rc;
-  const int E = args->dtype == SD_BF16 ? 8 : 4, rows = args->B * args->W;
-  *bytes = (size_t)rows * slice_count(rows, (args->V + E - 1) / E) * sizeof(SliceOut);
+  *bytes = layout(args).total;
   return SD_OK;
 }
 
@@ -256,15 +445,17 @@ extern "C" int sd_beam_select(const sd_beam_select_args_t* args, void* workspace
       (out_ended && out_ended == args->ended))
     return SD_EINVAL;
   if (!workspace || workspace_bytes < need || (uintptr_t)workspace % 8) return SD_EWORKSPACE;
-  const int E = args->dtype == SD_BF16 ? 8 : 4, nvec = (args->V + E - 1) / E;
+  const BeamLayout L = layout(args);
+  char* const ws = static_cast<char*>(workspace);
   BeamArgs a;
   a.logits = static_cast<const char*>(args->logits);
-  a.row_bytes = args->ld * (16 / E);
+  a.row_bytes = args->ld * (args->dtype == SD_BF16 ? 2 : 4);
   a.scores = args->scores, a.ended = args->ended;
   a.B = args->B, a.W = args->W, a.V = args->V, a.n_out = args->n_out, a.eos = args->eos_id;
-  a.slices = slice_count(a.B * a.W, nvec);
-  a.slice_vecs = (nvec + a.slices - 1) / a.slices;
-  a.part = static_cast<SliceOut*>(workspace);
+  a.slices = L.slices, a.slice_vecs = L.slice_vecs;
+  a.part_m = reinterpret_cast<float*>(ws + L.m);
+  a.part_s = reinterpret_cast<double*>(ws + L.s);
+  a.part_best = reinterpret_cast<uint64_t*>(ws + L.best);
   a.out_scores = out_scores, a.out_parents = out_parents, a.out_tokens = out_tokens;
   a.out_ended = out_ended, a.status = out_status;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -303,6 +494,10 @@ extern "C" int sd_beam_reorder(const sd_beam_reorder_args_t* p, void* stream) {
   a.max_units = p->max_units;
   const int64_t cols = p->max_units * p->unit_bytes / 16;
   const dim3 grid((unsigned)std::min<int64_t>((cols + 255) / 256, 1024), a.B, a.layers * a.segs);
-  hipLaunchKernelGGL(k_beam_reorder, grid, dim3(256), 0, static_cast<hipStream_t>(stream), a);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a.W_out <= 4) hipLaunchKernelGGL(k_beam_reorder<4>, grid, dim3(256), 0, st, a);
+  else if (a.W_out <= 8) hipLaunchKernelGGL(k_beam_reorder<8>, grid, dim3(256), 0, st, a);
+  else if (a.W_out <= 16) hipLaunchKernelGGL(k_beam_reorder<16>, grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(k_beam_reorder<MAXO>, grid, dim3(256), 0, st, a);
   return hipGetLastError() == hipSuccess ? SD_OK : SD_EHIP;
 }

@@ -8,10 +8,7 @@
 //   many rows          k_tree_descend, one workgroup per request, reads only
 //                      the rows that its walk visits, one after another.
 //
-// The scan of a row takes 1.5 operations a logit: packed (bf16) or plain (fp32)
-// integer maxima of the raw bits.  As signed numbers they order the values
-// that are not negative and put a positive NaN above +inf; as unsigned ones they
-// order the negative ones downwards and put a negative NaN above -inf.  A thread
+// The scan of a row takes 1.5 operations a bf16 logit (Extremes).  A thread
 // only keeps which group of its vectors holds its maximum; the token is looked
 // up afterwards by the threads that hold the row's.
 #include <algorithm>
@@ -44,59 +41,6 @@ __device__ __forceinline__ uint64_t arg_key(float z, int id) {
   const uint32_t o = z != z ? 0xFFFFFFFFu : ord_key(z);
   return ((uint64_t)o << 32) | (uint32_t)~id;
 }
-
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t x) {
-#pragma unroll
-  for (int o = WAVE / 2; o > 0; o >>= 1) {
-    const uint64_t y = __shfl_xor(x, o);
-    x = y > x ? y : x;
-  }
-  return x;
-}
-
-template <int DT>
-__device__ __forceinline__ float to_float(const char* row, int i) {
-  if constexpr (DT == SD_BF16) return __uint_as_float((uint32_t)((const uint16_t*)row)[i] << 16);
-  return ((const float*)row)[i];
-}
-
-// Running extremes of raw words: per 16-bit half (bf16) or whole (fp32).
-template <int DT>
-struct Extremes {
-  typedef short s16x2 __attribute__((ext_vector_type(2)));
-  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-  uint32_t smax, umax, umin;
-  __device__ void clear() {
-    constexpr uint32_t NINF = DT == SD_BF16 ? 0xFF80FF80u : 0xFF800000u;
-    smax = umax = umin = NINF;
-  }
-  __device__ void add(uint32_t w) {
-    if constexpr (DT == SD_BF16) {
-      const s16x2 s = __builtin_elementwise_max(__builtin_bit_cast(s16x2, smax), __builtin_bit_cast(s16x2, w));
-      const u16x2 u = __builtin_elementwise_max(__builtin_bit_cast(u16x2, umax), __builtin_bit_cast(u16x2, w));
-      const u16x2 v = __builtin_elementwise_min(__builtin_bit_cast(u16x2, umin), __builtin_bit_cast(u16x2, w));
-      smax = __builtin_bit_cast(uint32_t, s);
-      umax = __builtin_bit_cast(uint32_t, u);
-      umin = __builtin_bit_cast(uint32_t, v);
-    } else {
-      smax = (uint32_t)max((int)smax, (int)w);
-      umax = max(umax, w);
-      umin = min(umin, w);
-    }
-  }
-  // Largest value, and whether a NaN was seen.
-  __device__ float value(bool& nan) const {
-    if constexpr (DT == SD_BF16) {
-      const int s = max((int)(short)(smax & 0xFFFF), (int)(short)(smax >> 16));
-      const uint32_t u = max(umax & 0xFFFFu, umax >> 16), v = min(umin & 0xFFFFu, umin >> 16);
-      nan |= s > 0x7F80 || u > 0xFF80u;
-      return __uint_as_float((s >= 0 ? (uint32_t)s : v) << 16);
-    } else {
-      nan |= (int)smax > 0x7F800000 || umax > 0xFF800000u;
-      return __uint_as_float((int)smax >= 0 ? smax : umin);
-    }
-  }
-};
 
 // Lowest id in the thread's UG vectors of a group at k0 whose logit is z, or -1.
 template <int DT, int NT, int UG>

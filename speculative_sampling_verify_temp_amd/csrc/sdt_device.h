@@ -80,6 +80,64 @@ __device__ __forceinline__ uint16_t from_f32(float x) {
   return u;
 }
 
+// ---- rows of logits ----
+
+template <int DT>
+__device__ __forceinline__ float to_float(const char* row, int i) {
+  if constexpr (DT == SD_BF16) return __uint_as_float((uint32_t)((const uint16_t*)row)[i] << 16);
+  return ((const float*)row)[i];
+}
+
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t x) {
+#pragma unroll
+  for (int o = WAVE / 2; o > 0; o >>= 1) {
+    const uint64_t y = __shfl_xor(x, o);
+    x = y > x ? y : x;
+  }
+  return x;
+}
+
+// Running extremes of raw words, packed 16-bit halves (bf16) or whole (fp32):
+// 3 integer operations a word.  As signed numbers the bits order the values that
+// are not negative and put a positive NaN above +inf; as unsigned ones they order
+// the negative ones downwards and put a negative NaN above -inf.
+template <int DT>
+struct Extremes {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  uint32_t smax, umax, umin;
+  __device__ void clear() {
+    constexpr uint32_t NINF = DT == SD_BF16 ? 0xFF80FF80u : 0xFF800000u;
+    smax = umax = umin = NINF;
+  }
+  __device__ void add(uint32_t w) {
+    if constexpr (DT == SD_BF16) {
+      const s16x2 s = __builtin_elementwise_max(__builtin_bit_cast(s16x2, smax), __builtin_bit_cast(s16x2, w));
+      const u16x2 u = __builtin_elementwise_max(__builtin_bit_cast(u16x2, umax), __builtin_bit_cast(u16x2, w));
+      const u16x2 v = __builtin_elementwise_min(__builtin_bit_cast(u16x2, umin), __builtin_bit_cast(u16x2, w));
+      smax = __builtin_bit_cast(uint32_t, s);
+      umax = __builtin_bit_cast(uint32_t, u);
+      umin = __builtin_bit_cast(uint32_t, v);
+    } else {
+      smax = (uint32_t)max((int)smax, (int)w);
+      umax = max(umax, w);
+      umin = min(umin, w);
+    }
+  }
+  // Largest value, and whether a NaN was seen.
+  __device__ float value(bool& nan) const {
+    if constexpr (DT == SD_BF16) {
+      const int s = max((int)(short)(smax & 0xFFFF), (int)(short)(smax >> 16));
+      const uint32_t u = max(umax & 0xFFFFu, umax >> 16), v = min(umin & 0xFFFFu, umin >> 16);
+      nan |= s > 0x7F80 || u > 0xFF80u;
+      return __uint_as_float((s >= 0 ? (uint32_t)s : v) << 16);
+    } else {
+      nan |= (int)smax > 0x7F800000 || umax > 0xFF800000u;
+      return __uint_as_float((int)smax >= 0 ? smax : umin);
+    }
+  }
+};
+
 // ---- MFMA 16x16x32 ----
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
