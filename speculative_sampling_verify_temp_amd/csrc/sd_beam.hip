@@ -24,7 +24,7 @@ using namespace sdt;
 namespace {
 
 constexpr int NT_B = 256;
-constexpr int NV = 8;            // 16-byte vectors of a thread's part of a slice
+constexpr int NV = 4;            // 16-byte vectors of a thread's part of a slice
 constexpr int LIST = 1024;       // places for the values not below the bound
 constexpr int MAXO = SD_MAX_BEAMS;
 
@@ -101,7 +101,7 @@ __device__ __forceinline__ float logit_of(const uint4& w, int e) {
 // Bound by HBM: a logit is read once, and its exponential costs about 8
 // operations, half of the time its bytes take.
 template <int DT>
-__global__ __launch_bounds__(NT_B, 4) void k_beam_rows(BeamArgs a) {
+__global__ __launch_bounds__(NT_B, 6) void k_beam_rows(BeamArgs a) {
   constexpr int E = DT == SD_BF16 ? 8 : 4;
   __shared__ float sf[NT_B / WAVE];
   __shared__ double sd[NT_B / WAVE];

@@ -16,8 +16,9 @@ are allocated on the current stream; with `stream` given they are kept from
 reuse until that stream is done with them.
 """
 import ctypes
+import struct
 
-from . import (SD_BF16, SD_F32, SD_OK, SD_ST_INVALID_MASK, SdVerifyError, _ptr, _stream, lib)
+from . import SD_BF16, SD_F32, SD_OK, SD_ST_INVALID_MASK, SdVerifyError, lib
 
 SD_F16 = 2
 SD_MAX_NODES = 64
@@ -80,26 +81,47 @@ class SdBeamReorderArgs(ctypes.Structure):
                 ("W_out", _I32), ("segs", _I32), ("max_units", _I32)]
 
 
-def _declare():
-    def entry(name, struct, *rest):
-        f = getattr(lib, name)
-        f.argtypes = [ctypes.POINTER(struct), *rest]
-        f.restype = ctypes.c_int
-
-    size = ctypes.POINTER(_SZ)
-    entry("sd_tree_attention_workspace_bytes", SdTreeAttentionArgs, size)
-    entry("sd_tree_attention", SdTreeAttentionArgs, _P, _SZ, _P, _P, _P, _P)
-    entry("sd_tree_verify_workspace_bytes", SdTreeVerifyArgs, size)
-    entry("sd_tree_verify_greedy", SdTreeVerifyArgs, _P, _SZ, _P, _P, _P, _P, _P)
-    entry("sd_cache_commit", SdCacheCommitArgs, _P, _P, _P)
-    entry("sd_cache_evict_workspace_bytes", SdCacheEvictArgs, size)
-    entry("sd_cache_evict", SdCacheEvictArgs, _P, _SZ, _P, _P, _P)
-    entry("sd_beam_select_workspace_bytes", SdBeamSelectArgs, size)
-    entry("sd_beam_select", SdBeamSelectArgs, _P, _SZ, _P, _P, _P, _P, _P, _P)
-    entry("sd_beam_reorder", SdBeamReorderArgs, _P)
+# The argument structs as bytes: packing them costs a call a tenth of what
+# filling a ctypes.Structure does.  Native alignment is the C compiler's; 0q
+# pads the end to that of an 8-byte field.
+_CACHE = "QQqqqQqQiiiiiii"
+_TREE_ATTENTION = struct.Struct(_CACHE + "QQQqqqqqqQQQiiif0q")
+_TREE_VERIFY = struct.Struct("QqQQQiiiiiI0q")
+_CACHE_COMMIT = struct.Struct(_CACHE + "QQqqqqQQqQiiQqqQiffQQqQQ0q")
+_CACHE_EVICT = struct.Struct(_CACHE + "QQQQqQiii0q")
+_BEAM_SELECT = struct.Struct("QqQQiiiiii0q")
+_BEAM_REORDER = struct.Struct("QQqqqqqqqqQQqiiiiii0q")
 
 
-_declare()
+def _entry(name, *rest):
+    f = lib[name]
+    f.argtypes = [ctypes.c_char_p, *rest]
+    f.restype = ctypes.c_int
+    return f
+
+
+def _size_entry(name):
+    f = _entry(name, ctypes.POINTER(_SZ))
+
+    def size(a):
+        n = _SZ()
+        rc = f(a, n)
+        if rc != SD_OK:
+            raise SdVerifyError(rc, name)
+        return n.value
+    return size
+
+
+_tree_attention = _entry("sd_tree_attention", _P, _SZ, _P, _P, _P, _P)
+_tree_verify = _entry("sd_tree_verify_greedy", _P, _SZ, _P, _P, _P, _P, _P)
+_cache_commit = _entry("sd_cache_commit", _P, _P, _P)
+_cache_evict = _entry("sd_cache_evict", _P, _SZ, _P, _P, _P)
+_beam_select = _entry("sd_beam_select", _P, _SZ, _P, _P, _P, _P, _P, _P)
+_beam_reorder = _entry("sd_beam_reorder", _P)
+_tree_attention_bytes = _size_entry("sd_tree_attention_workspace_bytes")
+_tree_verify_bytes = _size_entry("sd_tree_verify_workspace_bytes")
+_cache_evict_bytes = _size_entry("sd_cache_evict_workspace_bytes")
+_beam_select_bytes = _size_entry("sd_beam_select_workspace_bytes")
 
 
 # ---- argument checks ----
@@ -115,76 +137,86 @@ def _here(first, *rest):
             raise ValueError("all tensors of a call must be on the same GPU")
 
 
+def _plain(t, dtype, name, *shape):
+    """Pointer of a contiguous tensor of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
 def _ints(t, name, *shape):
     import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
-    return t.data_ptr()
+    return _plain(t, torch.int32, name, *shape)
 
 
 def _floats(t, name, *shape):
     import torch
-    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)}")
-    return t.data_ptr()
+    return _plain(t, torch.float32, name, *shape)
 
 
 def _status(status, B):
     return None if status is None else _ints(status, "status", B)
 
 
+def _on(stream):
+    """The stream's handle; for the current one without building a Stream
+    object, which takes longer than the rest of the argument checks."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
+
+
 def _rows(t, name, like, N, H, D):
     """Packed node rows [N][H][D] of the cache's element type: (pointer, strides)."""
-    if t.dtype != like.dtype or tuple(t.shape) != (N, H, D):
+    if t.dtype is not like.dtype or t.shape != (N, H, D):
         raise ValueError(f"{name} must be {like.dtype} of shape {[N, H, D]}")
-    if D > 1 and t.stride(2) != 1:
+    node, head, one = t.stride()
+    if one != 1 and D > 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), node, head
 
 
 def _cache(k, v, table, lens):
+    """The fields of sd_kv_cache_t."""
     import torch
-    if k.dtype == torch.bfloat16:
+    if k.dtype is torch.bfloat16:
         code = SD_BF16
-    elif k.dtype == torch.float16:
+    elif k.dtype is torch.float16:
         code = SD_F16
     else:
         raise TypeError(f"the cache must be bfloat16 or float16 (got {k.dtype})")
-    if k.dim() != 4 or k.shape != v.shape or v.dtype != k.dtype or k.stride() != v.stride():
+    strides = k.stride()
+    if len(strides) != 4 or k.shape != v.shape or v.dtype is not k.dtype or strides != v.stride():
         raise ValueError("k_cache and v_cache must be [pages][H_kv][page_size][D] with the same "
                          "type, shape and strides")
     pages, H, page, D = k.shape
-    ps, hs, ss, es = k.stride()
+    ps, hs, ss, es = strides
     if es != 1 and D > 1:
         raise ValueError("the elements of a cache row must be contiguous")
-    if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+    if table.dtype is not torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError("page_table must be int32 [B][max_pages] with contiguous rows")
     B, cols = table.shape
-    return SdKvCache(k.data_ptr(), v.data_ptr(), ps, hs, ss, table.data_ptr(),
-                     table.stride(0) if B > 1 else max(cols, table.stride(0)),
-                     _ints(lens, "context_lens", B), code, B, H, D, page, pages, cols)
+    return (k.data_ptr(), v.data_ptr(), ps, hs, ss, table.data_ptr(),
+            table.stride(0) if B > 1 else max(cols, table.stride(0)),
+            _ints(lens, "context_lens", B), code, B, H, D, page, pages, cols)
 
 
-def _bytes(name, a):
-    n = _SZ()
-    rc = getattr(lib, name + "_workspace_bytes")(ctypes.byref(a), ctypes.byref(n))
-    if rc != SD_OK:
-        raise SdVerifyError(rc, name)
-    return n.value
-
-
-def _workspace(name, a, given, like, keep):
-    """The given workspace or a new one: (tensor, bytes)."""
+def _workspace(size, a, given, like, keep):
+    """The given workspace or a new one: (pointer, bytes)."""
     import torch
     if given is not None:
         if not given.is_contiguous():
             raise ValueError("the workspace must be contiguous")
         _here(like, given)
-        return given, given.numel() * given.element_size()
-    n = _bytes(name, a)
+        return given.data_ptr(), given.numel() * given.element_size()
+    n = size(a)
     ws = torch.empty(max(16, n), dtype=torch.uint8, device=like.device)
     keep.append(ws)
-    return ws, n
+    return ws.data_ptr(), n
 
 
 def _done(rc, name, stream, keep):
@@ -197,29 +229,38 @@ def _done(rc, name, stream, keep):
 
 # ---- attention of a drafted tree ----
 
-def make_tree_attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens,
-                             node_offsets, max_nodes, parents=None, tree_mask=None, scale=None):
-    """Fill sd_tree_attention_args_t from tensors: q [N][H_q][D], k_new and
-    v_new [N][H_kv][D], node_offsets [B + 1], parents [N] int32 or tree_mask
-    [N] int64 (bit j: node j of the request is seen) or neither (a chain);
-    scale defaults to 1 / sqrt(D)."""
+def _attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets,
+                    max_nodes, parents, tree_mask, scale):
     import torch
     c = _cache(k_cache, v_cache, page_table, context_lens)
+    B, H = c[9:11]
     N, Hq, D = q.shape
-    if c.D != D:
+    if c[11] != D:
         raise ValueError("queries and cache must have the same head size")
     qp, qn, qh = _rows(q, "q", k_cache, N, Hq, D)
-    kp, kn, kh = _rows(k_new, "k_new", k_cache, N, c.H_kv, D)
-    vp, vn, vh = _rows(v_new, "v_new", k_cache, N, c.H_kv, D)
-    mask = None
-    if tree_mask is not None:
-        if tree_mask.dtype != torch.int64 or tuple(tree_mask.shape) != (N,) or not tree_mask.is_contiguous():
-            raise ValueError("tree_mask must be a contiguous int64 tensor of shape [N]")
-        mask = tree_mask.data_ptr()
-    return SdTreeAttentionArgs(c, qp, kp, vp, qn, qh, kn, kh, vn, vh,
-                               _ints(node_offsets, "node_offsets", c.B + 1),
-                               None if parents is None else _ints(parents, "parents", N), mask, N,
-                               max_nodes, Hq, D ** -0.5 if scale is None else scale)
+    kp, kn, kh = _rows(k_new, "k_new", k_cache, N, H, D)
+    vp, vn, vh = _rows(v_new, "v_new", k_cache, N, H, D)
+    return _TREE_ATTENTION.pack(
+        *c, qp, kp, vp, qn, qh, kn, kh, vn, vh, _ints(node_offsets, "node_offsets", B + 1),
+        0 if parents is None else _ints(parents, "parents", N),
+        0 if tree_mask is None else _plain(tree_mask, torch.int64, "tree_mask", N), N, max_nodes,
+        Hq, D ** -0.5 if scale is None else scale)
+
+
+def make_tree_attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens,
+                             node_offsets, max_nodes, parents=None, tree_mask=None, scale=None):
+    """sd_tree_attention_args_t from tensors: q [N][H_q][D], k_new and v_new
+    [N][H_kv][D], node_offsets [B + 1], parents [N] int32 or tree_mask [N]
+    int64 (bit j: node j of the request is seen) or neither (a chain); scale
+    defaults to 1 / sqrt(D)."""
+    return SdTreeAttentionArgs.from_buffer_copy(_attention_args(
+        q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets, max_nodes,
+        parents, tree_mask, scale))
+
+
+def tree_attention_workspace_bytes(args):
+    """Bytes of workspace tree_attention needs for a filled argument struct."""
+    return _tree_attention_bytes(bytes(args))
 
 
 def tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets,
@@ -233,23 +274,23 @@ def tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, 
     import torch
     _here(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets, parents,
           tree_mask, out, lse, status)
-    a = make_tree_attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens,
-                                 node_offsets, max_nodes, parents, tree_mask, scale)
-    N, Hq, D = q.shape
+    a = _attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets,
+                        max_nodes, parents, tree_mask, scale)
+    shape = q.shape
     keep = []
     if out is None:
-        out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
         keep.append(out)
-    elif out.dtype != q.dtype or tuple(out.shape) != (N, Hq, D) or not out.is_contiguous():
-        raise ValueError("out must be contiguous, of q's type and shape")
+    else:
+        _plain(out, q.dtype, "out", *shape)
     if lse is not None:
-        _floats(lse, "lse", N, Hq)
+        _floats(lse, "lse", *shape[:2])
     elif want_lse:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
         keep.append(lse)
-    ws, n = _workspace("sd_tree_attention", a, workspace, q, keep)
-    rc = lib.sd_tree_attention(ctypes.byref(a), ws.data_ptr(), n, out.data_ptr(), _ptr(lse),
-                               _status(status, a.cache.B), _stream(stream))
+    ws, n = _workspace(_tree_attention_bytes, a, workspace, q, keep)
+    rc = _tree_attention(a, ws, n, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                         _status(status, page_table.shape[0]), _on(stream))
     _done(rc, "sd_tree_attention", stream, keep)
     return out, lse
 
@@ -291,10 +332,10 @@ def tree_verify_greedy(logits, tokens, parents, node_offsets, max_nodes, flags=0
     acc, path, tok = o.get("accepted"), o.get("path"), o.get("tokens")
     _here(logits, tokens, parents, node_offsets, status, acc, path, tok)
     ptr, ld, code = _logits(logits, "logits")
-    a = SdTreeVerifyArgs(ptr, ld, _ints(tokens, "tokens", N), _ints(parents, "parents", N),
-                         _ints(node_offsets, "node_offsets", B + 1), code, B, N, V, max_nodes, flags)
+    a = _TREE_VERIFY.pack(ptr, ld, _ints(tokens, "tokens", N), _ints(parents, "parents", N),
+                          _ints(node_offsets, "node_offsets", B + 1), code, B, N, V, max_nodes, flags)
     keep = []
-    ws, n = _workspace("sd_tree_verify", a, workspace, logits, keep)
+    ws, n = _workspace(_tree_verify_bytes, a, workspace, logits, keep)
 
     def output(t, name, *shape):
         if t is None:
@@ -306,9 +347,8 @@ def tree_verify_greedy(logits, tokens, parents, node_offsets, max_nodes, flags=0
 
     acc = output(acc, "accepted", B)
     path, tok = output(path, "path", B, max_nodes), output(tok, "tokens", B, max_nodes)
-    rc = lib.sd_tree_verify_greedy(ctypes.byref(a), ws.data_ptr(), n, acc.data_ptr(),
-                                   path.data_ptr(), tok.data_ptr(), _status(status, B),
-                                   _stream(stream))
+    rc = _tree_verify(a, ws, n, acc.data_ptr(), path.data_ptr(), tok.data_ptr(),
+                      _status(status, B), _on(stream))
     _done(rc, "sd_tree_verify_greedy", stream, keep)
     return acc, path, tok
 
@@ -332,32 +372,28 @@ def cache_commit(k_new, v_new, k_cache, v_cache, page_table, context_lens, node_
     _here(k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets, path, path_lens,
           out_context, q, lse, mass_in, mass_out, positions, seen, status)
     c = _cache(k_cache, v_cache, page_table, context_lens)
-    N, B = k_new.shape[0], c.B
-    kp, kn, kh = _rows(k_new, "k_new", k_cache, N, c.H_kv, c.D)
-    vp, vn, vh = _rows(v_new, "v_new", k_cache, N, c.H_kv, c.D)
-    a = SdCacheCommitArgs(c, kp, vp, kn, kh, vn, vh, _ints(node_offsets, "node_offsets", B + 1),
-                          _ints(path, "path", B, path.shape[-1]), path.shape[-1],
-                          _ints(path_lens, "path_lens", B), N, max_nodes)
-    L = None
+    N = k_new.shape[0]
+    B, H, D = c[9:12]
+    kp, kn, kh = _rows(k_new, "k_new", k_cache, N, H, D)
+    vp, vn, vh = _rows(v_new, "v_new", k_cache, N, H, D)
+    L = 0
+    weights = (0, 0, 0, 0, 0, 0.0, 0.0, 0, 0)
     if mass_out is not None:
-        L = mass_out.shape[-1]
-        a.q, a.q_node, a.q_head = _rows(q, "q", k_cache, N, q.shape[1], c.D)
-        a.H_q = q.shape[1]
-        a.lse = _floats(lse, "lse", N, a.H_q)
-        a.scale = c.D ** -0.5 if scale is None else scale
-        a.decay = decay
-        a.mass_in = _floats(mass_in, "mass_in", B, c.H_kv, L)
-        a.mass_out = _floats(mass_out, "mass_out", B, c.H_kv, L)
-        a.ld_mass = L
+        L, Hq = mass_out.shape[-1], q.shape[1]
+        weights = (*_rows(q, "q", k_cache, N, Hq, D), _floats(lse, "lse", N, Hq), Hq,
+                   D ** -0.5 if scale is None else scale, decay,
+                   _floats(mass_in, "mass_in", B, H, L), _floats(mass_out, "mass_out", B, H, L))
+    places = (0, 0)
     if positions is not None:
         if seen is None:
             raise ValueError("positions need seen")
-        L = positions.shape[-1] if L is None else L
-        a.positions = _ints(positions, "positions", B, c.H_kv, L)
-        a.seen = _ints(seen, "seen", B)
-        a.ld_mass = L
-    rc = lib.sd_cache_commit(ctypes.byref(a), _ints(out_context, "out_context", B),
-                             _status(status, B), _stream(stream))
+        L = L or positions.shape[-1]
+        places = _ints(positions, "positions", B, H, L), _ints(seen, "seen", B)
+    cols = path.shape[-1]
+    a = _CACHE_COMMIT.pack(*c, kp, vp, kn, kh, vn, vh, _ints(node_offsets, "node_offsets", B + 1),
+                           _ints(path, "path", B, cols), cols, _ints(path_lens, "path_lens", B), N,
+                           max_nodes, *weights, L, *places)
+    rc = _cache_commit(a, _ints(out_context, "out_context", B), _status(status, B), _on(stream))
     _done(rc, "sd_cache_commit", stream, ())
     return out_context
 
@@ -373,19 +409,21 @@ def cache_evict(k_cache, v_cache, page_table, context_lens, mass_in, mass_out, p
     _here(k_cache, v_cache, page_table, context_lens, mass_in, mass_out, positions_in,
           positions_out, seen, out_context, status)
     c = _cache(k_cache, v_cache, page_table, context_lens)
-    B, L = c.B, mass_in.shape[-1]
+    B, H = c[9:11]
+    L = mass_in.shape[-1]
     if (positions_in is None) != (positions_out is None):
         raise ValueError("positions_in and positions_out go together")
-    a = SdCacheEvictArgs(c, _floats(mass_in, "mass_in", B, c.H_kv, L),
-                         _floats(mass_out, "mass_out", B, c.H_kv, L),
-                         None if positions_in is None else _ints(positions_in, "positions_in", B, c.H_kv, L),
-                         None if positions_out is None else _ints(positions_out, "positions_out", B, c.H_kv, L),
-                         L, None if seen is None else _ints(seen, "seen", B), budget, recent, sinks)
+    places = (0, 0)
+    if positions_in is not None:
+        places = (_ints(positions_in, "positions_in", B, H, L),
+                  _ints(positions_out, "positions_out", B, H, L))
+    a = _CACHE_EVICT.pack(*c, _floats(mass_in, "mass_in", B, H, L),
+                          _floats(mass_out, "mass_out", B, H, L), *places, L,
+                          0 if seen is None else _ints(seen, "seen", B), budget, recent, sinks)
     keep = []
-    ws, n = _workspace("sd_cache_evict", a, workspace, k_cache, keep)
-    rc = lib.sd_cache_evict(ctypes.byref(a), ws.data_ptr(), n,
-                            _ints(out_context, "out_context", B), _status(status, B),
-                            _stream(stream))
+    ws, n = _workspace(_cache_evict_bytes, a, workspace, k_cache, keep)
+    rc = _cache_evict(a, ws, n, _ints(out_context, "out_context", B), _status(status, B),
+                      _on(stream))
     _done(rc, "sd_cache_evict", stream, keep)
     return out_context
 
@@ -407,14 +445,13 @@ def beam_select(logits, scores, n_out, ended=None, eos_id=-1, out_ended=None, st
     o = out or {}
     sc, par, tok = o.get("scores"), o.get("parents"), o.get("tokens")
     _here(logits, scores, ended, out_ended, status, sc, par, tok)
-    for t, name, shape in ((ended, "ended", (B, W)), (out_ended, "out_ended", (B, n_out))):
-        if t is not None and (t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {list(shape)}")
     ptr, ld, code = _logits(logits, "logits")
-    a = SdBeamSelectArgs(ptr, ld, _floats(scores, "scores", B, W),
-                         None if ended is None else ended.data_ptr(), code, B, W, V, n_out, eos_id)
+    a = _BEAM_SELECT.pack(ptr, ld, _floats(scores, "scores", B, W),
+                          0 if ended is None else _plain(ended, torch.uint8, "ended", B, W), code,
+                          B, W, V, n_out, eos_id)
+    oe = None if out_ended is None else _plain(out_ended, torch.uint8, "out_ended", B, n_out)
     keep = []
-    ws, n = _workspace("sd_beam_select", a, workspace, logits, keep)
+    ws, n = _workspace(_beam_select_bytes, a, workspace, logits, keep)
 
     def output(t, name, dtype, check):
         if t is None:
@@ -426,8 +463,8 @@ def beam_select(logits, scores, n_out, ended=None, eos_id=-1, out_ended=None, st
 
     sc = output(sc, "scores", torch.float32, _floats)
     par, tok = output(par, "parents", torch.int32, _ints), output(tok, "tokens", torch.int32, _ints)
-    rc = lib.sd_beam_select(ctypes.byref(a), ws.data_ptr(), n, sc.data_ptr(), par.data_ptr(),
-                            tok.data_ptr(), _ptr(out_ended), _status(status, B), _stream(stream))
+    rc = _beam_select(a, ws, n, sc.data_ptr(), par.data_ptr(), tok.data_ptr(), oe,
+                      _status(status, B), _on(stream))
     _done(rc, "sd_beam_select", stream, keep)
     return sc, par, tok
 
@@ -441,27 +478,29 @@ def beam_reorder(state, parents, lengths=None, out=None, stream=None):
         raise ValueError("state must be [layers][B][W][segs][units][..]")
     dst = state if out is None else out
     _here(state, dst, parents, lengths)
-    layers, B, W, segs, units = state.shape[:5]
+    shape = state.shape
+    layers, B, W, segs, units = shape[:5]
     if parents.dim() != 2 or parents.shape[0] != B:
         raise ValueError("parents must be [B][W_out]")
     W_out = parents.shape[1]
-    if dst.dtype != state.dtype or tuple(dst.shape) != (layers, B, W_out, segs, *state.shape[4:]):
+    if dst.dtype is not state.dtype or dst.shape != (layers, B, W_out, segs, *shape[4:]):
         raise ValueError("out must have state's type and shape, with W_out beams")
-    es, unit = state.element_size(), 1
-    for n in state.shape[5:]:
+    es = state.element_size()
+    unit = es
+    for n in shape[5:]:
         unit *= n
+    strides = []
     for t in (state, dst):
-        want = unit * es
-        for n, s in zip((*t.shape[5:], 1), t.stride()[4:]):
-            if s * es != want:
+        s = t.stride()
+        want = unit
+        for n, step in zip((*shape[5:], 1), s[4:]):
+            if step * es != want:
                 raise ValueError("the units of a state row must be contiguous")
             want //= max(1, n)
-    if out is not None and out is not state and out.data_ptr() == state.data_ptr() and out.stride() != state.stride():
-        raise ValueError("out must not overlap state")
-    a = SdBeamReorderArgs(state.data_ptr(), dst.data_ptr(), *(s * es for s in state.stride()[:4]),
-                          *(s * es for s in dst.stride()[:4]), _ints(parents, "parents", B, W_out),
-                          None if lengths is None else _ints(lengths, "lengths", B), unit * es,
-                          layers, B, W, W_out, segs, units)
-    rc = lib.sd_beam_reorder(ctypes.byref(a), _stream(stream))
-    _done(rc, "sd_beam_reorder", stream, ())
+        strides += [step * es for step in s[:4]]
+    a = _BEAM_REORDER.pack(state.data_ptr(), dst.data_ptr(), *strides,
+                           _ints(parents, "parents", B, W_out),
+                           0 if lengths is None else _ints(lengths, "lengths", B), unit, layers, B,
+                           W, W_out, segs, units)
+    _done(_beam_reorder(a, _on(stream)), "sd_beam_reorder", stream, ())
     return dst

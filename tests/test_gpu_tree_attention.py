@@ -147,7 +147,7 @@ def test_same_bits_on_every_call_and_stream_and_in_a_graph():
     torch.cuda.synchronize()
     assert torch.equal(a, b) and torch.equal(la, lb)
     args = sdv.make_tree_attention_args(**c.attention_args(), max_nodes=64, scale=c.scale)
-    ws = torch.empty(max(16, sdv.tree._bytes("sd_tree_attention", args)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(sdv.tree_attention_workspace_bytes(args), dtype=torch.uint8, device="cuda")
     out, lse = torch.zeros_like(a), torch.zeros_like(la)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):

@@ -56,6 +56,27 @@ def test_struct_layouts_match_the_header(cls, name, tmp_path):
     assert got == [ctypes.sizeof(A)] + [getattr(A, f).offset for f in fields]
 
 
+@pytest.mark.parametrize("cls,packed", [
+    ("SdTreeAttentionArgs", "_TREE_ATTENTION"), ("SdTreeVerifyArgs", "_TREE_VERIFY"),
+    ("SdCacheCommitArgs", "_CACHE_COMMIT"), ("SdCacheEvictArgs", "_CACHE_EVICT"),
+    ("SdBeamSelectArgs", "_BEAM_SELECT"), ("SdBeamReorderArgs", "_BEAM_REORDER")])
+def test_packed_arguments_are_the_structs(cls, packed):
+    """The binding packs argument structs as bytes: every value lands in its
+    field."""
+    T = _tree()
+    A, S = getattr(T, cls), getattr(T, packed)
+    fields = []
+    for name, kind in A._fields_:
+        if kind is T.SdKvCache:
+            fields += [("cache", f[0]) for f in kind._fields_]
+        else:
+            fields.append((None, name))
+    assert S.size == ctypes.sizeof(A)
+    a = A.from_buffer_copy(S.pack(*range(1, len(fields) + 1)))
+    got = [getattr(a.cache if outer else a, name) for outer, name in fields]
+    assert got == list(range(1, len(fields) + 1))
+
+
 def _cache():
     return _tree().SdKvCache(0x100000, 0x200000, 4 * 16 * 128, 16 * 128, 128, 0x300000, 10, 0x310000,
                              1, 2, 4, 128, 16, 20, 10)
