@@ -35,72 +35,82 @@ struct AttnArgs {
   const int32_t* off;
   const int32_t* parents;
   const uint64_t* mask;
-  int N, max_nodes, Hq, G;
-  float scale;
+  int N, max_nodes, Hq, G, mts_max;
+  bool whole;       // no row tile's keys are split
+  float scale, inv_G;
   float* part;      // partial results, two slots a run
   char* out;
   float* lse;
   uint32_t* status;
 };
 
-// The nodes that node i of the request sees, as bits.
-__device__ __forceinline__ uint64_t sees(const AttnArgs& a, const Nodes& nd, int i) {
-  const uint64_t own = nd.T == 64 ? ~0ull : (1ull << nd.T) - 1;
-  if (a.mask) return a.mask[nd.first + i] & own;
-  if (!a.parents) return (2ull << i) - 1;
-  uint64_t m = 0;
-  for (int j = i; j >= 0;) {
-    m |= 1ull << j;
-    const int p = a.parents[nd.first + j];
-    j = p < j ? p : -1;      // p < -1 ends the walk too
+// ---- the unit list ----
+
+// What the lanes of a wave hold of up to 64 requests, one each: slots in use,
+// nodes, row tiles, key tiles (the tree's is the last) and units, for all KV
+// heads, up to and including the lane's own.
+struct Requests {
+  int ctx, first, T, mts, nt, incl;
+  uint32_t st;
+};
+
+template <int RT, int KT>
+__device__ __forceinline__ Requests requests(const AttnArgs& a, int b) {
+  Requests r{0, 0, 0, 0, 0, 0, 0};
+  if (b < a.c.B) {
+    const Nodes nd = request_nodes(a.off, b, a.N, a.max_nodes);
+    r.ctx = request_ctx(a.c, b, r.st);
+    r.first = nd.first, r.T = nd.T;
+    r.mts = (nd.T * a.G + RT - 1) / RT;
+    r.nt = (r.ctx + KT - 1) / KT + 1;
+  }
+  r.incl = wave_incl_scan_int(r.mts * r.nt * a.c.H);
+  return r;
+}
+
+__device__ __forceinline__ int lane_units(const Requests& r) { return lane_read(r.incl, WAVE - 1); }
+
+// All units; r: the first 64 requests.
+template <int RT, int KT>
+__device__ __forceinline__ int total_units(const AttnArgs& a, const Requests& r) {
+  int u = lane_units(r);
+  for (int b0 = WAVE; b0 < a.c.B; b0 += WAVE) u += lane_units(requests<RT, KT>(a, b0 + (int)threadIdx.x % WAVE));
+  return u;
+}
+
+__device__ __forceinline__ int run_length(int units, int runs) { return (int)(((unsigned)units + runs - 1) / (unsigned)runs); }
+
+// r / G for a packed row (exact: r < 2^11, G <= 32).
+__device__ __forceinline__ int row_node(const AttnArgs& a, int r) { return (int)(((float)r + 0.5f) * a.inv_G); }
+
+// Lane j: the nodes that node j of the request sees, as bits.  Ancestors by
+// pointer doubling: six steps reach the root of any tree of 64 nodes.
+__device__ __forceinline__ uint64_t seen_by_lane(const AttnArgs& a, int first, int T) {
+  const int j = threadIdx.x % WAVE;
+  const bool in = j < T;
+  if (a.mask) return in ? a.mask[first + j] & (T == 64 ? ~0ull : (1ull << T) - 1) : 0;
+  if (!a.parents) return (2ull << j) - 1;
+  int up = in ? a.parents[first + j] : -1;
+  if (up < -1 || up >= j) up = -1;
+  uint64_t m = 1ull << j;
+#pragma unroll
+  for (int s = 0; s < 6; ++s) {
+    const int from = max(up, 0);
+    const uint64_t mu = __shfl(m, from);
+    const int uu = __shfl(up, from);
+    if (up >= 0) m |= mu, up = uu;
   }
   return m;
 }
 
-// ---- the unit list ----
-
-// Row tiles and key tiles of request b, and its units (all KV heads).
-struct Extent {
-  int rows, mts, nt;
-  double units;
-};
-
-template <int RT, int KT>
-__device__ __forceinline__ Extent request_extent(const AttnArgs& a, int b) {
-  Extent e{0, 0, 0, 0.0};
-  if (b >= a.c.B) return e;
-  const Nodes nd = request_nodes(a.off, b, a.N, a.max_nodes);
-  uint32_t st = 0;
-  const int ctx = request_ctx(a.c, b, st);
-  e.rows = nd.T * a.G;
-  e.mts = (e.rows + RT - 1) / RT;
-  e.nt = (ctx + KT - 1) / KT + 1;
-  e.units = (double)e.mts * e.nt * a.c.H;     // exact: below 2^53
-  return e;
-}
-
-// All units, by every wave alike.
-template <int RT, int KT>
-__device__ __forceinline__ double total_units(const AttnArgs& a) {
-  double u = 0.0;
-  for (int b0 = 0; b0 < a.c.B; b0 += WAVE)
-    u += wave_sum(request_extent<RT, KT>(a, b0 + threadIdx.x % WAVE).units);
-  return u;
-}
-
-__device__ __forceinline__ int64_t run_length(double units, int runs) {
-  return ((int64_t)units + runs - 1) / runs;
-}
-
 // Any of the 8 elements infinite or not a number.
 template <int DT>
-__device__ __forceinline__ bool any_nonfinite(const uint4& w) {
+__device__ __forceinline__ bool any_nonfinite(const u32x4& w) {
   constexpr uint32_t E = DT == SD_BF16 ? 0x7F80u : 0x7C00u;
   bool bad = false;
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    bad |= (u[i] & E) == E || ((u[i] >> 16) & E) == E;
+    bad |= (w[i] & E) == E || ((w[i] >> 16) & E) == E;
   return bad;
 }
 
@@ -124,7 +134,8 @@ struct Shape {
   static constexpr int CPR = D / 8;              // 16-byte chunks of a row
   static constexpr int NCH = KEYS * CPR / (WAVE * RG);
   static constexpr int TILE = KEYS * D * 2;      // bytes of a group's K (or V) tile
-  static constexpr int JOIN = (KG - 1) * RT * (D + 2) * 4;
+  static constexpr int JR = D + 4;               // floats of a row in the join of the key groups
+  static constexpr int JOIN = (KG - 1) * RT * JR * 4;
   static constexpr int LDS = 2 * KG * TILE > JOIN ? 2 * KG * TILE : JOIN;
   static constexpr int SLOT = RT * (D + 2);      // floats of a partial result
   static_assert(KT >= SD_MAX_NODES && KEYS <= 64, "the tree is one tile");
@@ -141,62 +152,78 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
   char* const ldv = ldk + S::TILE;
   const float c = a.scale * 1.4426950408889634f;
 
-  // Workgroups of one XCD take neighbouring runs: row tiles of one KV head
-  // find each other's keys in its L2.
-  const int runs = gridDim.x, per_xcd = runs / 8;
-  const int run = runs % 8 ? (int)blockIdx.x : (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
-  const int64_t total = (int64_t)total_units<S::RT, S::KT>(a);
-  const int64_t per = run_length((double)total, runs);
-  int64_t u0 = run * per, u1 = min(total, u0 + per);
-  if (u0 >= u1) return;
-
-  // the request that holds unit u0
-  int b = 0;
-  int64_t before = 0;
-  for (int b0 = 0;; b0 += WAVE) {
-    const double incl = wave_incl_scan(request_extent<S::RT, S::KT>(a, b0 + l).units);
-    const uint64_t over = __ballot((double)(u0 - before) < incl);
-    if (over) {
-      const int f = __builtin_ctzll(over);
-      b = b0 + f;
-      if (f) before += (int64_t)lane_read(incl, f - 1);
-      break;
-    }
-    before += (int64_t)lane_read(incl, WAVE - 1);
+  Requests rq = requests<S::RT, S::KT>(a, l);
+  int run, u0, u1;
+  if (a.whole) {
+    // one workgroup per (request, KV head, row tile): nothing is split
+    run = 0, u0 = 0, u1 = 0;
+  } else {
+    // Workgroups of one XCD take neighbouring runs: row tiles of one KV head
+    // find each other's keys in its L2.
+    const int runs = gridDim.x, total = total_units<S::RT, S::KT>(a, rq), per = run_length(total, runs);
+    run = (int)(blockIdx.x % 8) * (runs / 8) + (int)(blockIdx.x / 8);      // runs is a multiple of 8
+    if ((int64_t)run * per >= total) return;
+    u0 = run * per, u1 = min(total, u0 + per);
   }
-  b = __builtin_amdgcn_readfirstlane(b);
-  int64_t in = u0 - before;      // units of request b before ours
 
-  for (; u0 < u1; ++b, in = 0) {
-    const Extent e = request_extent<S::RT, S::KT>(a, b);
-    const int64_t mine = (int64_t)e.units - in;
-    if (mine <= 0) continue;
-    const Nodes nd = request_nodes(a.off, b, a.N, a.max_nodes);
-    uint32_t st = 0;
-    const int ctx = request_ctx(a.c, b, st);
-    const int32_t* tab = table_row(a.c, b);
-    const int64_t stop = min(u1, u0 + mine);
+  // the request (lane f of this 64) that holds unit u0, and its units before
+  int b0 = 0, f, in;
+  if (a.whole) {
+    const int b = blockIdx.x / (a.c.H * a.mts_max), seg = blockIdx.x % (a.c.H * a.mts_max);
+    b0 = b & ~(WAVE - 1), f = b & (WAVE - 1);
+    if (b0) rq = requests<S::RT, S::KT>(a, b0 + l);
+    const int mts = lane_read(rq.mts, f), nt = lane_read(rq.nt, f);
+    if (seg % a.mts_max >= mts) return;
+    in = (seg / a.mts_max * mts + seg % a.mts_max) * nt;
+    u1 = nt;
+  } else {
+    int left = u0;
+    while (left >= lane_units(rq)) {
+      left -= lane_units(rq);
+      b0 += WAVE;
+      rq = requests<S::RT, S::KT>(a, b0 + l);
+    }
+    f = __builtin_ctzll(__ballot(left < rq.incl));
+    in = left - (f ? lane_read(rq.incl, f - 1) : 0);
+  }
+
+  while (u0 < u1) {
+    const int units = lane_read(rq.incl, f) - (f ? lane_read(rq.incl, f - 1) : 0);
+    const int ctx = lane_read(rq.ctx, f), first = lane_read(rq.first, f), T = lane_read(rq.T, f);
+    const int mts = lane_read(rq.mts, f), nt = lane_read(rq.nt, f);
+    const uint32_t st = (uint32_t)lane_read((int)rq.st, f);
+    const int32_t* const tab = table_row(a.c, b0 + f);
+    const int rows = T * a.G;
+    const int stop = u0 + min(u1 - u0, units - in);
     while (u0 < stop) {
-      const int seg = (int)(in / e.nt), t0 = (int)(in % e.nt);
-      const int h = seg / e.mts, mt = seg % e.mts;
-      const int t1 = (int)min((int64_t)e.nt, t0 + (stop - u0));
+      const int seg = in / nt, t0 = in - seg * nt;
+      const int h = seg / mts, mt = seg - h * mts;
+      const int t1 = min(nt, t0 + (stop - u0));
       const int row0 = mt * S::RT + rg * 16 * MT;
+
+      // Lane l of a wave looks key l of its group's tile up; the page of the
+      // tile after the next one is always on its way.
+      auto page_of = [&](int t) {
+        const int s = t * S::KT + kg * S::KEYS + l;
+        return t < nt - 1 && l < S::KEYS && s < ctx ? tab[s >> a.c.page_shift] : -1;
+      };
+      const int page0 = page_of(t0);
+      int page = page_of(t0 + 1);
 
       // this wave's queries, as the B operand: lane (n, g4) holds columns
       // 32 ks + 8 g4 .. + 7 of row n
       s16x8 q[MT][KS];
-      uint64_t vis[MT];
+      int node[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int r = row0 + 16 * m + n;
-        const bool on = r < e.rows;
-        const int node = on ? r / a.G : 0, head = h * a.G + (on ? r % a.G : 0);
-        const char* qp = a.q + (int64_t)(nd.first + node) * a.q_node + head * a.q_head;
+        const bool on = r < rows;
+        node[m] = on ? row_node(a, r) : 0;
+        const int head = h * a.G + (on ? r - node[m] * a.G : 0);
+        const char* qp = a.q + (int64_t)(first + node[m]) * a.q_node + head * a.q_head;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
+        for (int ks = 0; ks < KS; ++ks)
           q[m][ks] = on ? *(const s16x8*)(qp + (ks * 32 + g4 * 8) * 2) : s16x8{};
-        }
-        vis[m] = on && !st && t1 == e.nt ? sees(a, nd, node) : 0;
       }
       f32x4 o[MT][DTS];
       float mx[MT], sum[MT];
@@ -208,64 +235,86 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
       }
       if (tid == 0) odd_value = 0;
 
-      // Lane l of a wave looks key l of its group's tile up; the page of the
-      // tile after the next one is always on its way.
-      auto page_of = [&](int t) {
-        const int s = t * S::KT + kg * S::KEYS + l;
-        return t < e.nt - 1 && l < S::KEYS && s < ctx ? tab[s >> a.c.page_shift] : -1;
-      };
-      uint4 rk[S::NCH], rv[S::NCH];
-      uint64_t ok = 0;
+      // Loads are unconditional: a key that is not there reads the pool's first
+      // row (or the tree's last) and is masked, its value zeroed on the way to
+      // LDS.
+      u32x4 rk[S::NCH], rv[S::NCH];
+      uint64_t ok = 0;                 // keys of the loaded tile that are there
       auto load = [&](int t, int page) {
-        if (t == e.nt - 1) {
-          const int left = nd.T - kg * S::KEYS;
-          ok = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0;
+        uint64_t kp[S::NCH], vp[S::NCH];      // (as numbers: pointers that meet lose their address space)
+        if (t < nt - 1) {
+          const bool there = (unsigned)page < (unsigned)a.c.num_pages;
+          ok = __ballot(there);
+          const int s = t * S::KT + kg * S::KEYS + l;
+          const int64_t at = there ? page * a.c.page_stride + h * a.c.head_stride + (s & a.c.page_mask) * a.c.slot_stride : 0;
+#pragma unroll
+          for (int i = 0; i < S::NCH; ++i) {
+            const int lin = (i * RG + rg) * WAVE + l, col = lin % S::CPR;
+            const int64_t x = __shfl(at, lin / S::CPR) + col * 16;
+            kp[i] = (uint64_t)a.c.k + x;
+            vp[i] = (uint64_t)a.c.v + x;
+          }
         } else {
-          ok = __ballot((unsigned)page < (unsigned)a.c.num_pages);
+          // (opaque to the compiler, which would otherwise keep these addresses
+          // in 40 registers throughout the loop)
+          int from = first;
+          asm volatile("" : "+s"(from));
+          const int left = T - kg * S::KEYS;
+          ok = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0;
+#pragma unroll
+          for (int i = 0; i < S::NCH; ++i) {
+            const int lin = (i * RG + rg) * WAVE + l, col = lin % S::CPR;
+            const int64_t r = from + min(kg * S::KEYS + lin / S::CPR, T - 1);
+            kp[i] = (uint64_t)a.kn + r * a.k_node + h * a.k_head + col * 16;
+            vp[i] = (uint64_t)a.vn + r * a.v_node + h * a.v_head + col * 16;
+          }
         }
-        const int s = t * S::KT + kg * S::KEYS + l;
-        const int64_t at = page * a.c.page_stride + h * a.c.head_stride + (s & a.c.page_mask) * a.c.slot_stride;
+        // (one set of loads for both: two would have to meet in copies, which
+        // wait for them)
 #pragma unroll
         for (int i = 0; i < S::NCH; ++i) {
-          const int lin = (i * RG + rg) * WAVE + l, row = lin / S::CPR, col = lin % S::CPR;
-          rk[i] = rv[i] = make_uint4(0, 0, 0, 0);
-          const char *kp, *vp;
-          if (t == e.nt - 1) {
-            const int64_t r = nd.first + kg * S::KEYS + row;
-            kp = a.kn + r * a.k_node + h * a.k_head;
-            vp = a.vn + r * a.v_node + h * a.v_head;
-          } else {
-            const int64_t x = __shfl(at, row);
-            kp = a.c.k + x;
-            vp = a.c.v + x;
-          }
-          if (ok >> row & 1) {
-            rk[i] = *(const uint4*)(kp + col * 16);
-            rv[i] = *(const uint4*)(vp + col * 16);
-          }
+          rk[i] = *(const global_u32x4*)kp[i];
+          rv[i] = *(const global_u32x4*)vp[i];
         }
       };
 
-      load(t0, page_of(t0));
-      int page = page_of(t0 + 1);
+      load(t0, page0);
+      uint64_t vis[MT];
+      if (t1 == nt) {
+        const uint64_t seen = st ? 0 : seen_by_lane(a, first, T);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) vis[m] = __shfl(seen, node[m]);
+      } else {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) vis[m] = 0;
+      }
       for (int t = t0; t < t1; ++t) {
         if (RG > 1 || t == t0) __syncthreads();      // the tile before has been read
-        const bool tree = t == e.nt - 1;
+        const bool tree = t == nt - 1;
+        const uint64_t valid = ok;
+        constexpr uint64_t FULL = S::KEYS == 64 ? ~0ull : (1ull << (S::KEYS % 64)) - 1;
+        if (tree || (valid & FULL) != FULL) {
+#pragma unroll
+          for (int i = 0; i < S::NCH; ++i) {
+            const int row = ((i * RG + rg) * WAVE + l) / S::CPR;
+            if (!(valid >> row & 1)) {
+              rv[i] = u32x4{0, 0, 0, 0};
+            } else if (tree && any_nonfinite<DT>(rv[i])) {
+              // 0 x infinity in the product would reach rows that do not see
+              // this node: such values are added at the end instead
+              odd_value = 1;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) rv[i][j] = finite_or_zero<DT>(rv[i][j]);
+            }
+          }
+        }
 #pragma unroll
         for (int i = 0; i < S::NCH; ++i) {
           const int lin = (i * RG + rg) * WAVE + l, row = lin / S::CPR, col = lin % S::CPR;
           const int at = row * (D * 2) + ((col ^ swz<D>(row)) * 16);
-          if (tree && any_nonfinite<DT>(rv[i])) {
-            // 0 x infinity in the product would reach rows that do not see
-            // this node: such values are added at the end instead
-            odd_value = 1;
-            rv[i] = make_uint4(finite_or_zero<DT>(rv[i].x), finite_or_zero<DT>(rv[i].y),
-                               finite_or_zero<DT>(rv[i].z), finite_or_zero<DT>(rv[i].w));
-          }
-          *(uint4*)(ldk + at) = rk[i];
-          *(uint4*)(ldv + at) = rv[i];
+          *(u32x4*)(ldk + at) = rk[i];
+          *(u32x4*)(ldv + at) = rv[i];
         }
-        const uint64_t valid = ok;
         if (RG > 1) __syncthreads();
         else __builtin_amdgcn_wave_barrier();
         if (t + 1 < t1) {
@@ -274,20 +323,43 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
         }
 #pragma unroll
         for (int ns = 0; ns < NS; ++ns) {
-          // S^T: lane (n, g4) gets keys 16 s + 4 g4 + r of row n
-          f32x4 x[2][MT];
+          // S^T: lane (n, g4) gets keys 16 s + 4 g4 + r of row n.  All reads of a
+          // step are issued ahead of the products that use them.
+          s16x8 kf[2][KS];
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const int row = ns * 32 + s * 16 + n;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) x[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-              const s16x8 k = *(const s16x8*)(ldk + row * (D * 2) + (((ks * 4 + g4) ^ swz<D>(row)) * 16));
-#pragma unroll
-              for (int m = 0; m < MT; ++m) x[s][m] = mfma<DT>(k, q[m][ks], x[s][m]);
+              const int row = ns * 32 + s * 16 + n;
+              kf[s][ks] = *(const s16x8*)(ldk + row * (D * 2) + (((ks * 4 + g4) ^ swz<D>(row)) * 16));
             }
-          }
+          __builtin_amdgcn_sched_barrier(0);
+          f32x4 x[2][MT];
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              x[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+              for (int ks = 0; ks < KS; ++ks) x[s][m] = mfma<DT>(kf[s][ks], q[m][ks], x[s][m]);
+            }
+          // V^T of 16 columns by 32 keys, keys in the weights' order; the first
+          // half of the columns is on its way during the softmax
+          auto value = [&](int d) {
+            s16x8 v;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const int row = ns * 32 + s * 16 + g4 * 4 + (n >> 2);
+              const int at = row * (D * 2) + (((d * 2 + ((n & 3) >> 1)) ^ swz<D>(row)) * 16) + (n & 1) * 8;
+              const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(ldv + at));
+              v[s * 4] = y[0], v[s * 4 + 1] = y[1], v[s * 4 + 2] = y[2], v[s * 4 + 3] = y[3];
+            }
+            return v;
+          };
+          s16x8 vf[DTS / 2];
+#pragma unroll
+          for (int d = 0; d < DTS / 2; ++d) vf[d] = value(d);
+          __builtin_amdgcn_sched_barrier(0);
           const uint32_t some = (uint32_t)(valid >> (ns * 32));
           s16x8 p[MT];
 #pragma unroll
@@ -333,19 +405,12 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
                 p[m][s * 4 + r] = (short)from_f32<DT>(y);
               }
           }
-          // O^T: V^T of 16 columns by 32 keys, keys in the weights' order
+          // O^T
 #pragma unroll
           for (int d = 0; d < DTS; ++d) {
-            s16x8 v;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const int row = ns * 32 + s * 16 + g4 * 4 + (n >> 2);
-              const int at = row * (D * 2) + (((d * 2 + ((n & 3) >> 1)) ^ swz<D>(row)) * 16) + (n & 1) * 8;
-              const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(ldv + at));
-              v[s * 4] = y[0], v[s * 4 + 1] = y[1], v[s * 4 + 2] = y[2], v[s * 4 + 3] = y[3];
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) o[m][d] = mfma<DT>(v, p[m], o[m][d]);
+            for (int m = 0; m < MT; ++m) o[m][d] = mfma<DT>(vf[d % (DTS / 2)], p[m], o[m][d]);
+            if (d < DTS / 2) vf[d] = value(d + DTS / 2);
           }
         }
         if (RG == 1) __builtin_amdgcn_wave_barrier();
@@ -358,43 +423,39 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
         float* const sh = (float*)lds;
         __syncthreads();
         if (kg > 0) {
-          float* const z = sh + ((kg - 1) * RG + rg) * 16 * MT * (D + 2);
+          float* const z = sh + ((kg - 1) * RG + rg) * 16 * MT * S::JR;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            float* const zr = z + (16 * m + n) * (D + 2);
+            float* const zr = z + (16 * m + n) * S::JR;
 #pragma unroll
-            for (int d = 0; d < DTS; ++d)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) zr[d * 16 + g4 * 4 + r] = o[m][d][r];
+            for (int d = 0; d < DTS; ++d) *(f32x4*)(zr + d * 16 + g4 * 4) = o[m][d];
             if (g4 == 0) zr[D] = mx[m], zr[D + 1] = sum[m];
           }
         }
         __syncthreads();
         if (kg == 0) {
           for (int k2 = 1; k2 < KG; ++k2) {
-            const float* const z = sh + ((k2 - 1) * RG + rg) * 16 * MT * (D + 2);
+            const float* const z = sh + ((k2 - 1) * RG + rg) * 16 * MT * S::JR;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              const float* const zr = z + (16 * m + n) * (D + 2);
+              const float* const zr = z + (16 * m + n) * S::JR;
               const float m2 = zr[D], mn = fmaxf(mx[m], m2), ms = mn > -INFINITY ? mn : 0.0f;
               const float f1 = fast_exp2(mx[m] - ms), f2 = fast_exp2(m2 - ms);
               mx[m] = mn;
               sum[m] = sum[m] * f1 + zr[D + 1] * f2;
 #pragma unroll
-              for (int d = 0; d < DTS; ++d)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[m][d][r] = o[m][d][r] * f1 + zr[d * 16 + g4 * 4 + r] * f2;
+              for (int d = 0; d < DTS; ++d) o[m][d] = o[m][d] * f1 + *(const f32x4*)(zr + d * 16 + g4 * 4) * f2;
             }
           }
         }
       }
       if (RG > 1 && KG == 1) __syncthreads();      // odd_value
       if (kg == 0) {
-        if (t1 == e.nt && odd_value) {
+        if (t1 == nt && odd_value) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
-            for (int j = 0; j < nd.T; ++j) {
-              const uint16_t* v = (const uint16_t*)(a.vn + (int64_t)(nd.first + j) * a.v_node + h * a.v_head);
+            for (int j = 0; j < T; ++j) {
+              const uint16_t* v = (const uint16_t*)(a.vn + (int64_t)(first + j) * a.v_node + h * a.v_head);
 #pragma unroll
               for (int d = 0; d < DTS; ++d)
 #pragma unroll
@@ -404,16 +465,16 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
                 }
             }
         }
-        const bool whole = t0 == 0 && t1 == e.nt;
+        const bool whole = t0 == 0 && t1 == nt;
         float* const part = a.part + (int64_t)(run * 2 + (t0 == 0)) * S::SLOT;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const int lr = rg * 16 * MT + 16 * m + n, r = mt * S::RT + lr;
-          if (r >= e.rows) continue;
+          if (r >= rows) continue;
           if (whole) {
             const bool none = sum[m] == 0.0f;
             const float inv = none ? 0.0f : 1.0f / sum[m];
-            const int64_t at = (int64_t)(nd.first + r / a.G) * a.Hq + h * a.G + r % a.G;
+            const int64_t at = (int64_t)(first + node[m]) * a.Hq + h * a.G + (r - node[m] * a.G);
             char* const out = a.out + at * (D * 2);
 #pragma unroll
             for (int d = 0; d < DTS; ++d) {
@@ -440,42 +501,62 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
       u0 += t1 - t0;
       in += t1 - t0;
     }
+    in = 0;
+    if (++f == WAVE && u0 < u1) {
+      f = 0, b0 += WAVE;
+      rq = requests<S::RT, S::KT>(a, b0 + l);
+    }
   }
 }
 
 // Rows whose key tiles went to several runs: their parts in the order of the
-// runs.  grid (4-column groups of a row tile / 256, H * row tiles, B).
+// runs, four at a time.  grid (4-column groups of a row tile / 256, H * row
+// tiles, B).
 template <int DT, typename S>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int runs, int mts_max) {
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int runs) {
   constexpr int D = S::D, GPR = D / 4;
-  const int b = blockIdx.z, h = blockIdx.y / mts_max, mt = blockIdx.y % mts_max, l = threadIdx.x % WAVE;
-  const Extent e = request_extent<S::RT, S::KT>(a, b);
-  if (mt >= e.mts) return;
-  const int lin = blockIdx.x * 256 + threadIdx.x, lr = lin / GPR, col = lin % GPR;
-  const int64_t per = run_length(total_units<S::RT, S::KT>(a), runs);
-  double before = 0.0;
-  for (int b0 = 0; b0 < b; b0 += WAVE)
-    before += wave_sum(b0 + l < b ? request_extent<S::RT, S::KT>(a, b0 + l).units : 0.0);
-  const int64_t s = (int64_t)before + (int64_t)(h * e.mts + mt) * e.nt;
-  const int64_t w0 = s / per, w1 = (s + e.nt - 1) / per;
-  const int r = mt * S::RT + lr;
-  if (w0 == w1 || lr >= S::RT || r >= e.rows) return;
-  auto part = [&](int64_t w) { return a.part + (w * 2 + (w == w0)) * S::SLOT; };
-  float m = -INFINITY;
-  for (int64_t w = w0; w <= w1; ++w) m = fmaxf(m, part(w)[S::RT * D + lr]);
-  const float ms = m > -INFINITY ? m : 0.0f;
-  float sum = 0.0f;
-  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t w = w0; w <= w1; ++w) {
-    const float* z = part(w);
-    const float f = fast_exp2(z[S::RT * D + lr] - ms);
-    sum += z[S::RT * D + S::RT + lr] * f;
-    o += *(const f32x4*)(z + lr * D + col * 4) * f;
+  const int b = blockIdx.z, h = blockIdx.y / a.mts_max, mt = blockIdx.y % a.mts_max, l = threadIdx.x % WAVE;
+  Requests rq = requests<S::RT, S::KT>(a, l);
+  const int per = run_length(total_units<S::RT, S::KT>(a, rq), runs);
+  int before = 0;
+  for (int b0 = 0; b0 + WAVE <= b; b0 += WAVE) {
+    before += lane_units(rq);
+    rq = requests<S::RT, S::KT>(a, b0 + WAVE + l);
   }
-  const Nodes nd = request_nodes(a.off, b, a.N, a.max_nodes);
+  const int f = b % WAVE, nt = lane_read(rq.nt, f), mts = lane_read(rq.mts, f);
+  if (mt >= mts) return;
+  if (f) before += lane_read(rq.incl, f - 1);
+  const int s = before + (h * mts + mt) * nt;
+  const int w0 = (int)((unsigned)s / (unsigned)per), w1 = (int)((unsigned)(s + nt - 1) / (unsigned)per);
+  const int lin = blockIdx.x * 256 + threadIdx.x, lr = lin / GPR, col = lin % GPR, r = mt * S::RT + lr;
+  if (w0 == w1 || r >= lane_read(rq.T, f) * a.G) return;
+  float m = -INFINITY, sum = 0.0f;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int w = w0; w <= w1; w += 4) {
+    float pm[4], ps[4];
+    f32x4 po[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int wi = min(w + i, w1);
+      const float* z = a.part + (int64_t)(wi * 2 + (wi == w0)) * S::SLOT;
+      pm[i] = z[S::RT * D + lr];
+      ps[i] = z[S::RT * D + S::RT + lr];
+      po[i] = *(const f32x4*)(z + lr * D + col * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (w + i > w1) break;
+      const float mn = fmaxf(m, pm[i]), ms = mn > -INFINITY ? mn : 0.0f;
+      const float f1 = fast_exp2(m - ms), f2 = fast_exp2(pm[i] - ms);
+      m = mn;
+      sum = sum * f1 + ps[i] * f2;
+      o = o * f1 + po[i] * f2;
+    }
+  }
   const bool none = sum == 0.0f;
   const float inv = none ? 0.0f : 1.0f / sum;
-  const int64_t at = (int64_t)(nd.first + r / a.G) * a.Hq + h * a.G + r % a.G;
+  const int node = row_node(a, r);
+  const int64_t at = (int64_t)(lane_read(rq.first, f) + node) * a.Hq + h * a.G + (r - node * a.G);
   uint32_t u[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -533,6 +614,7 @@ AttnArgs device_args(const sd_tree_attention_args_t* p) {
   a.max_nodes = p->max_nodes;
   a.Hq = p->H_q;
   a.G = p->H_q / p->cache.H_kv;
+  a.inv_G = 1.0f / (float)a.G;
   a.scale = p->scale;
   return a;
 }
@@ -554,16 +636,24 @@ constexpr int run_count() {
   return S::NT == 512 ? 256 : 512;
 }
 
+// Where a table holds no more than this many key tiles, splitting them and
+// joining the parts in a second launch costs more than it saves.
+constexpr int WHOLE_TILES = 8;
+
 template <int DT, int D>
 int launch(AttnArgs a, int rows, hipStream_t st) {
   return with_shape<D>(rows, [&](auto s) {
     using S = decltype(s);
     constexpr int runs = run_count<S>();
-    hipLaunchKernelGGL((k_attn_tiles<DT, S>), dim3(runs), dim3(S::NT), 0, st, a);
+    a.mts_max = (rows + S::RT - 1) / S::RT;
+    const int64_t segments = (int64_t)a.c.B * a.c.H * a.mts_max, tiles = (a.c.cap + S::KT - 1) / S::KT + 1;
+    if (segments * tiles > 0x7FFFFFFF) return SD_EUNSUPPORTED;
+    a.whole = tiles <= WHOLE_TILES;
+    hipLaunchKernelGGL((k_attn_tiles<DT, S>), dim3(a.whole ? (unsigned)segments : (unsigned)runs), dim3(S::NT), 0, st, a);
     if (hipGetLastError() != hipSuccess) return SD_EHIP;
-    const int mts = (rows + S::RT - 1) / S::RT;
-    const dim3 grid(S::RT * (D / 4) / 256, a.c.H * mts, a.c.B);
-    hipLaunchKernelGGL((k_attn_join<DT, S>), grid, dim3(256), 0, st, a, runs, mts);
+    if (a.whole) return SD_OK;
+    const dim3 grid(S::RT * (D / 4) / 256, a.c.H * a.mts_max, a.c.B);
+    hipLaunchKernelGGL((k_attn_join<DT, S>), grid, dim3(256), 0, st, a, runs);
     return hipGetLastError() == hipSuccess ? SD_OK : SD_EHIP;
   });
 }
