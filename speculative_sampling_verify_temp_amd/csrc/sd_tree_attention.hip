@@ -21,6 +21,8 @@
 //                through registers into swizzled LDS rows, the next tile's
 //                loads in flight behind the products.
 // k_attn_join    one thread per 4 output columns of a split row.
+#include <type_traits>
+
 #include "sdt_device.h"
 
 using namespace sdv;
@@ -143,14 +145,16 @@ struct Shape {
 
 template <int DT, typename S>
 __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
-  constexpr int D = S::D, MT = S::MT, RG = S::RG, KG = S::KG, NS = S::NS, KS = D / 32, DTS = D / 16;
+  constexpr int D = S::D, MT = S::MT, RG = S::RG, KG = S::KG, NS = S::NS, KS = D / 32, DTS = D / 16, VA = 4;      // VA: V operands read ahead
   __shared__ __align__(16) char lds[S::LDS];
   __shared__ int odd_value;      // a tree value is infinite or not a number
   const int tid = threadIdx.x, l = tid % WAVE, w = tid / WAVE, n = l & 15, g4 = l >> 4;
   const int rg = w % RG, kg = w / RG;
   char* const ldk = lds + kg * 2 * S::TILE;
   char* const ldv = ldk + S::TILE;
-  const float c = a.scale * 1.4426950408889634f;
+  // scores in base 2; a negative scale is in the queries' signs, and one of zero
+  // stays above it so that a masked score times it is still -inf
+  const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
 
   Requests rq = requests<S::RT, S::KT>(a, l);
   int run, u0, u1;
@@ -212,6 +216,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
 
       // this wave's queries, as the B operand: lane (n, g4) holds columns
       // 32 ks + 8 g4 .. + 7 of row n
+      const s16x8 sign = s16x8{} + (short)(a.scale < 0.0f ? 0x8000 : 0);
       s16x8 q[MT][KS];
       int node[MT];
 #pragma unroll
@@ -223,7 +228,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
         const char* qp = a.q + (int64_t)(first + node[m]) * a.q_node + head * a.q_head;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-          q[m][ks] = on ? *(const s16x8*)(qp + (ks * 32 + g4 * 8) * 2) : s16x8{};
+          q[m][ks] = on ? *(const s16x8*)(qp + (ks * 32 + g4 * 8) * 2) ^ sign : s16x8{};
       }
       f32x4 o[MT][DTS];
       float mx[MT], sum[MT];
@@ -288,6 +293,109 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) vis[m] = 0;
       }
+      // One tile in LDS against this wave's rows.  MASKED: bit j of on[m] says
+      // whether row m sees the group's key j.
+      auto tile = [&](auto masked, const uint64_t (&on)[MT]) {
+        constexpr bool MASKED = decltype(masked)::value;
+        // S^T: lane (n, g4) gets keys 16 s + 4 g4 + r of row n; the reads of 16
+        // keys are issued ahead of the products of the 16 before
+        auto keys = [&](int s, s16x8 (&kf)[KS]) {
+          const int row = s * 16 + n;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            kf[ks] = *(const s16x8*)(ldk + row * (D * 2) + (((ks * 4 + g4) ^ swz<D>(row)) * 16));
+        };
+        // V^T of 16 columns by 32 keys, keys in the weights' order
+        auto values = [&](int i) {
+          const int ns = i / DTS, d = i % DTS;
+          s16x8 v;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int row = ns * 32 + s * 16 + g4 * 4 + (n >> 2);
+            const int at = row * (D * 2) + (((d * 2 + ((n & 3) >> 1)) ^ swz<D>(row)) * 16) + (n & 1) * 8;
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(ldv + at));
+            v[s * 4] = y[0], v[s * 4 + 1] = y[1], v[s * 4 + 2] = y[2], v[s * 4 + 3] = y[3];
+          }
+          return v;
+        };
+        f32x4 x[2 * NS][MT];
+        s16x8 kf[2][KS], vf[VA];
+        keys(0, kf[0]);
+#pragma unroll
+        for (int s = 0; s < 2 * NS; ++s) {
+          if (s + 1 < 2 * NS) {
+            keys(s + 1, kf[(s + 1) & 1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < VA; ++i) vf[i] = values(i);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            x[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) x[s][m] = mfma<DT>(kf[s & 1][ks], q[m][ks], x[s][m]);
+          }
+        }
+        float ms[MT];
+        bool grown = false;
+        float top[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          top[m] = -INFINITY;
+          const uint64_t mine = on[m] >> (g4 * 4);      // bit 16 s + r: this lane's
+#pragma unroll
+          for (int s = 0; s < 2 * NS; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if constexpr (MASKED)
+                x[s][m][r] = (mine >> (s * 16 + r) & 1) ? x[s][m][r] : -INFINITY;
+              top[m] = fmaxf(top[m], x[s][m][r]);
+            }
+          top[m] = quad_max(top[m]) * c;
+          // the sums are rescaled only when a maximum grows by more than 2^8:
+          // until then weights up to 2^8 are as exact as those below 1
+          grown |= top[m] > mx[m] + 8.0f;
+        }
+        if (__any(grown)) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const float mn = fmaxf(mx[m], top[m]);
+            const float f = mn > -INFINITY ? fast_exp2(mx[m] - mn) : 1.0f;
+            mx[m] = mn;
+            sum[m] *= f;
+#pragma unroll
+            for (int d = 0; d < DTS; ++d) o[m][d] *= f;
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) ms[m] = mx[m] > -INFINITY ? mx[m] : 0.0f;
+#pragma unroll
+        for (int ns = 0; ns < NS; ++ns) {
+          s16x8 p[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float y = fast_exp2(fmaf(x[ns * 2 + s][m][r], c, -ms[m]));
+                sum[m] += y;
+                // the weights enter the product in the element type: half a
+                // step each, and the sum keeps their fp32 values
+                p[m][s * 4 + r] = (short)from_f32<DT>(y);
+              }
+          // O^T
+#pragma unroll
+          for (int d = 0; d < DTS; ++d) {
+            const int i = ns * DTS + d;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) o[m][d] = mfma<DT>(vf[i % VA], p[m], o[m][d]);
+            if (i + VA < NS * DTS) vf[i % VA] = values(i + VA);
+          }
+        }
+      };
+
       for (int t = t0; t < t1; ++t) {
         if (RG > 1 || t == t0) __syncthreads();      // the tile before has been read
         const bool tree = t == nt - 1;
@@ -321,97 +429,13 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
           load(t + 1, page);
           page = page_of(t + 2);
         }
+        if (!tree && (valid & FULL) == FULL) {
+          tile(std::false_type{}, vis);
+        } else {
+          uint64_t on[MT];
 #pragma unroll
-        for (int ns = 0; ns < NS; ++ns) {
-          // S^T: lane (n, g4) gets keys 16 s + 4 g4 + r of row n.  All reads of a
-          // step are issued ahead of the products that use them.
-          s16x8 kf[2][KS];
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              const int row = ns * 32 + s * 16 + n;
-              kf[s][ks] = *(const s16x8*)(ldk + row * (D * 2) + (((ks * 4 + g4) ^ swz<D>(row)) * 16));
-            }
-          __builtin_amdgcn_sched_barrier(0);
-          f32x4 x[2][MT];
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              x[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-              for (int ks = 0; ks < KS; ++ks) x[s][m] = mfma<DT>(kf[s][ks], q[m][ks], x[s][m]);
-            }
-          // V^T of 16 columns by 32 keys, keys in the weights' order; the first
-          // half of the columns is on its way during the softmax
-          auto value = [&](int d) {
-            s16x8 v;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const int row = ns * 32 + s * 16 + g4 * 4 + (n >> 2);
-              const int at = row * (D * 2) + (((d * 2 + ((n & 3) >> 1)) ^ swz<D>(row)) * 16) + (n & 1) * 8;
-              const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(ldv + at));
-              v[s * 4] = y[0], v[s * 4 + 1] = y[1], v[s * 4 + 2] = y[2], v[s * 4 + 3] = y[3];
-            }
-            return v;
-          };
-          s16x8 vf[DTS / 2];
-#pragma unroll
-          for (int d = 0; d < DTS / 2; ++d) vf[d] = value(d);
-          __builtin_amdgcn_sched_barrier(0);
-          const uint32_t some = (uint32_t)(valid >> (ns * 32));
-          s16x8 p[MT];
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            float top = -INFINITY;
-            const uint32_t on = tree ? some & (uint32_t)(vis[m] >> (kg * S::KEYS + ns * 32)) : some;
-            if (tree || some != 0xFFFFFFFFu) {
-#pragma unroll
-              for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  x[s][m][r] = (on >> (s * 16 + g4 * 4 + r) & 1) ? x[s][m][r] * c : -INFINITY;
-            } else {
-#pragma unroll
-              for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[s][m][r] *= c;
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) top = fmaxf(top, x[s][m][r]);
-            top = quad_max(top);
-            // the sums are rescaled only when a maximum grows by more than
-            // 2^8: until then weights up to 2^8 are as exact as those below 1
-            if (__any(top > mx[m] + 8.0f)) {
-              const float mn = fmaxf(mx[m], top);
-              const float f = mn > -INFINITY ? fast_exp2(mx[m] - mn) : 1.0f;
-              mx[m] = mn;
-              sum[m] *= f;
-#pragma unroll
-              for (int d = 0; d < DTS; ++d) o[m][d] *= f;
-            }
-            const float ms = mx[m] > -INFINITY ? mx[m] : 0.0f;
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float y = fast_exp2(x[s][m][r] - ms);
-                sum[m] += y;
-                // the weights enter the product in the element type: half a
-                // step each, and the sum keeps their fp32 values
-                p[m][s * 4 + r] = (short)from_f32<DT>(y);
-              }
-          }
-          // O^T
-#pragma unroll
-          for (int d = 0; d < DTS; ++d) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) o[m][d] = mfma<DT>(vf[d % (DTS / 2)], p[m], o[m][d]);
-            if (d < DTS / 2) vf[d] = value(d + DTS / 2);
-          }
+          for (int m = 0; m < MT; ++m) on[m] = tree ? valid & vis[m] >> (kg * S::KEYS) : valid;
+          tile(std::true_type{}, on);
         }
         if (RG == 1) __builtin_amdgcn_wave_barrier();
       }
