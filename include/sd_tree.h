@@ -117,8 +117,9 @@ typedef struct sd_tree_attention_args {
   float           scale;         /* finite                                      */
 } sd_tree_attention_args_t;
 
-/* Workspace bytes (depends on B, H_kv, H_q, D, max_nodes and the table's
- * size only). */
+/* Workspace bytes (depends on H_q / H_kv, D, max_nodes and the table's size
+ * only; 0 for short tables, then workspace may be NULL).  SD_EUNSUPPORTED where
+ * B * H_kv * (packed rows / 16) * (slots of a table / 64) could pass 2^31. */
 int sd_tree_attention_workspace_bytes(const sd_tree_attention_args_t *args, size_t *bytes);
 
 int sd_tree_attention(const sd_tree_attention_args_t *args, void *workspace,

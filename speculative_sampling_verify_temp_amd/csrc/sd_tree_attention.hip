@@ -664,15 +664,33 @@ constexpr int run_count() {
 // joining the parts in a second launch costs more than it saves.
 constexpr int WHOLE_TILES = 8;
 
+// How a call is cut up.
+struct Plan {
+  int mts_max;                // row tiles of a KV head
+  int64_t segments, tiles;    // (request, KV head, row tile)s, and key tiles of one
+  bool fits, whole;
+};
+
+template <typename S>
+Plan plan(const sd_kv_cache_t& c, int rows) {
+  Plan p;
+  p.mts_max = (rows + S::RT - 1) / S::RT;
+  p.segments = (int64_t)c.B * c.H_kv * p.mts_max;
+  p.tiles = ((int64_t)c.max_pages * c.page_size + S::KT - 1) / S::KT + 1;
+  p.fits = p.segments <= 0x7FFFFFFF / p.tiles;      // units are counted in 32 bits
+  p.whole = p.tiles <= WHOLE_TILES;
+  return p;
+}
+
 template <int DT, int D>
-int launch(AttnArgs a, int rows, hipStream_t st) {
+int launch(AttnArgs a, const sd_kv_cache_t& c, int rows, hipStream_t st) {
   return with_shape<D>(rows, [&](auto s) {
     using S = decltype(s);
     constexpr int runs = run_count<S>();
-    a.mts_max = (rows + S::RT - 1) / S::RT;
-    const int64_t segments = (int64_t)a.c.B * a.c.H * a.mts_max, tiles = (a.c.cap + S::KT - 1) / S::KT + 1;
-    if (segments * tiles > 0x7FFFFFFF) return SD_EUNSUPPORTED;
-    a.whole = tiles <= WHOLE_TILES;
+    const Plan p = plan<S>(c, rows);
+    const int64_t segments = p.segments;
+    a.mts_max = p.mts_max;
+    a.whole = p.whole;
     hipLaunchKernelGGL((k_attn_tiles<DT, S>), dim3(a.whole ? (unsigned)segments : (unsigned)runs), dim3(S::NT), 0, st, a);
     if (hipGetLastError() != hipSuccess) return SD_EHIP;
     if (a.whole) return SD_OK;
@@ -689,12 +707,13 @@ extern "C" int sd_tree_attention_workspace_bytes(const sd_tree_attention_args_t*
   const int rc = check(args);
   if (rc) return rc;
   const int rows = args->max_nodes * (args->H_q / args->cache.H_kv);
-  auto size = [](auto s) {
+  auto size = [&](auto s) {
     using S = decltype(s);
-    return (size_t)run_count<S>() * 2 * S::SLOT * sizeof(float);
+    const Plan p = plan<S>(args->cache, rows);
+    *bytes = p.whole ? 0 : (size_t)run_count<S>() * 2 * S::SLOT * sizeof(float);
+    return p.fits ? SD_OK : SD_EUNSUPPORTED;
   };
-  *bytes = args->cache.D == 64 ? with_shape<64>(rows, size) : with_shape<128>(rows, size);
-  return SD_OK;
+  return args->cache.D == 64 ? with_shape<64>(rows, size) : with_shape<128>(rows, size);
 }
 
 extern "C" int sd_tree_attention(const sd_tree_attention_args_t* args, void* workspace,
@@ -704,7 +723,7 @@ extern "C" int sd_tree_attention(const sd_tree_attention_args_t* args, void* wor
   int rc = sd_tree_attention_workspace_bytes(args, &need);
   if (rc) return rc;
   if (!out || !aligned16(out)) return SD_EINVAL;
-  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return SD_EWORKSPACE;
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return SD_EWORKSPACE;
   AttnArgs a = device_args(args);
   a.out = static_cast<char*>(out);
   a.lse = out_lse;
@@ -713,9 +732,9 @@ extern "C" int sd_tree_attention(const sd_tree_attention_args_t* args, void* wor
   a.part = static_cast<float*>(workspace);
   const int rows = a.max_nodes * a.G, D = args->cache.D;
   if (args->cache.dtype == SD_BF16)
-    rc = D == 64 ? launch<SD_BF16, 64>(a, rows, st) : launch<SD_BF16, 128>(a, rows, st);
+    rc = D == 64 ? launch<SD_BF16, 64>(a, args->cache, rows, st) : launch<SD_BF16, 128>(a, args->cache, rows, st);
   else
-    rc = D == 64 ? launch<SD_F16, 64>(a, rows, st) : launch<SD_F16, 128>(a, rows, st);
+    rc = D == 64 ? launch<SD_F16, 64>(a, args->cache, rows, st) : launch<SD_F16, 128>(a, args->cache, rows, st);
   if (rc) return rc;
   if (out_status) {
     hipLaunchKernelGGL(k_tree_status, dim3(a.c.B), dim3(WAVE), 0, st, a);

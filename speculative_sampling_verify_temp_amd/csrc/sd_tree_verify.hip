@@ -5,8 +5,8 @@
 //   few rows in all    k_tree_argmax finds the maximum of every row, a
 //                      workgroup per (row, slice of the vocabulary), and
 //                      k_tree_walk, one wave per request, follows the tree;
-//   many rows          k_tree_descend, one workgroup per request, reads only
-//                      the rows that its walk visits, one after another.
+//   many rows          k_tree_descend reads only the rows that the walks visit,
+//                      one after another, each by a team of workgroups.
 //
 // The scan of a row takes 1.5 operations a bf16 logit (Extremes).  A thread
 // only keeps which group of its vectors holds its maximum; the token is looked
@@ -21,8 +21,10 @@ using namespace sdt;
 namespace {
 
 constexpr int NT_A = 256;    // threads of a (row, slice)
-constexpr int NT_D = 1024;   // threads of a walk that reads its own rows
-constexpr int UD = 19;       // vectors a thread of such a walk loads at once: 155648 bf16 logits
+constexpr int NT_D = 512;    // threads of a workgroup of a team
+constexpr int UD = 8;        // vectors a thread of a team loads at once
+
+struct Team;
 
 struct VerifyArgs {
   const char* logits;
@@ -31,7 +33,8 @@ struct VerifyArgs {
   int B, N, V, max_nodes;
   uint32_t flags;
   int slices, slice_vecs;   // 16-byte vectors of a slice
-  uint64_t* part;           // [N][slices]
+  uint64_t* part;           // [N][slices] ([B][slices] where walks read their rows)
+  Team* team;               // [B], there
   int32_t *accepted, *path, *out_tokens;
   uint32_t* status;
 };
@@ -205,17 +208,131 @@ __global__ __launch_bounds__(WAVE) void k_tree_walk(VerifyArgs a) {
   w.write(a, b);
 }
 
+// ---- walks that read their own rows ----
+//
+// One workgroup reads a row from HBM at about 30 GB/s, so a team of `slices` of
+// them shares each row of a request's walk.  They meet through tickets: ticket
+// k of a request is slice k % slices of its row number k / slices.  A workgroup
+// takes the next ticket, waits until that row is known, leaves its slice's
+// maximum, and the last one of a row to do so takes the step and makes the
+// next row known.  A ticket is only waited for by later ones, and whoever holds
+// an earlier one is running, so every wait ends however few workgroups of a
+// team the chip holds at a time.
+
+//
+// What the team shares is only touched by relaxed agent-scope atomics, which
+// act where all of the chip's caches meet; a wait for the ones before stands
+// where order matters.  (Acquire and release operations would also write back
+// and invalidate whole L2 caches: 14 us a step instead of 6.)
+
+struct Team {
+  uint32_t ticket, left, row, pad;          // row: depth << 8 | node, or DONE
+  uint64_t visited[SD_MAX_NODES];           // by depth: node << 32 | its row's best token
+};
+constexpr uint32_t DONE = 0xFFFFFFFFu;
+
+template <typename T>
+__device__ __forceinline__ T shared_load(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ void shared_store(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint32_t shared_add(uint32_t* p) {
+  return __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// All memory operations of this wave before are done, and none after begun.
+__device__ __forceinline__ void settle() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0);
+  asm volatile("" ::: "memory");
+}
+
+// Results of a walk that has ended, by one wave; the entries of lane l.
+__device__ __forceinline__ void finish(const VerifyArgs& a, int b, uint32_t st, int accepted, int path, int tok) {
+  const int l = threadIdx.x % WAVE;
+  const bool bad = st & SD_ST_TREE_INVALID_MASK;
+  if (l < a.max_nodes) {
+    a.path[(int64_t)b * a.max_nodes + l] = bad ? -1 : path;
+    a.out_tokens[(int64_t)b * a.max_nodes + l] = bad ? -1 : tok;
+  }
+  if (l == 0) {
+    a.accepted[b] = bad ? -1 : accepted;
+    if (a.status) a.status[b] = st;
+  }
+}
+
+// Requests as their walks begin, one wave each.
+__global__ __launch_bounds__(WAVE) void k_tree_begin(VerifyArgs a) {
+  const int b = blockIdx.x, l = threadIdx.x;
+  Walk w(a, b);
+  const bool go = w.valid() && w.enter(a.flags);
+  if (!go) finish(a, b, w.st, 0, w.my_path, -1);
+  if (l == 0) {
+    Team& t = a.team[b];
+    t.ticket = t.left = 0;
+    t.row = go ? 0 : DONE;
+  }
+}
+
 template <int DT>
 __global__ __launch_bounds__(NT_D) void k_tree_descend(VerifyArgs a) {
   constexpr int E = DT == SD_BF16 ? 8 : 4;
   __shared__ uint64_t sm[2 * NT_D / WAVE];
-  const int b = blockIdx.x;
-  Walk w(a, b);      // every wave walks along
-  while (w.valid() && w.enter(a.flags)) {
-    const char* row = a.logits + (int64_t)(w.nd.first + w.cur) * a.row_bytes;
-    if (!w.step(row_best<DT, NT_D, UD>(row, 0, a.V / E, a.V, true, sm))) break;
+  __shared__ uint32_t ticket_sh, row_sh, last_sh;
+  const int b = blockIdx.y, tid = threadIdx.x, l = tid % WAVE;
+  Team& team = a.team[b];
+  uint64_t* const part = a.part + (int64_t)b * a.slices;
+  uint32_t next = tid == 0 ? shared_add(&team.ticket) : 0;
+  Walk w(a, b);
+  for (;;) {
+    if (tid == 0) {
+      const uint32_t depth = next / (uint32_t)a.slices;
+      uint32_t r;
+      for (;;) {
+        r = shared_load(&team.row);
+        if (r == DONE || (r >> 8) >= depth) break;
+        __builtin_amdgcn_s_sleep(1);
+      }
+      ticket_sh = next, row_sh = r;
+    }
+    __syncthreads();
+    if (row_sh == DONE) return;
+    const int sl = (int)(ticket_sh % (uint32_t)a.slices), depth = (int)(row_sh >> 8), cur = (int)(row_sh & 255u);
+    if (tid == 0) next = shared_add(&team.ticket);      // on its way while the row is read
+    const int lo = sl * a.slice_vecs, hi = min(a.V / E, lo + a.slice_vecs);
+    const char* row = a.logits + (int64_t)(w.nd.first + cur) * a.row_bytes;
+    const uint64_t mine = row_best<DT, NT_D, UD>(row, lo, hi, a.V, sl == a.slices - 1, sm);
+    if (tid == 0) {
+      shared_store(&part[sl], mine);
+      settle();
+      last_sh = shared_add(&team.left) == (uint32_t)((depth + 1) * a.slices - 1);
+    }
+    __syncthreads();
+    if (last_sh && tid < WAVE) {
+      settle();
+      uint64_t best = 0;
+      for (int s = l; s < a.slices; s += WAVE) {
+        const uint64_t k = shared_load(&part[s]);
+        best = k > best ? k : best;
+      }
+      best = wave_max_u64(best);
+      if (l == 0) shared_store(&team.visited[depth], (uint64_t)cur << 32 | (uint32_t)~(uint32_t)best);
+      w.cur = cur, w.count = depth;
+      const bool on = w.step(best);
+      const bool more = on && w.enter(a.flags);
+      settle();
+      if (!more) {
+        // (a node entered last without its row has no entry there)
+        const int rows = on ? w.count : depth + 1;
+        const uint64_t v = l < rows ? shared_load(&team.visited[l]) : 0;
+        finish(a, b, w.st, w.count, l < rows ? (int)(v >> 32) : l == w.count ? w.cur : -1, l < rows ? (int)(uint32_t)v : -1);
+      }
+      if (l == 0) shared_store(&team.row, more ? (uint32_t)w.count << 8 | (uint32_t)w.cur : DONE);
+    }
+    __syncthreads();
   }
-  if (threadIdx.x < WAVE) w.write(a, b);
 }
 
 int check(const sd_tree_verify_args_t* p) {
@@ -226,24 +343,39 @@ int check(const sd_tree_verify_args_t* p) {
   if (p->B < 1 || p->N < 1 || p->V < 1 || p->max_nodes < 1 || p->ld < p->V || (p->ld * es) % 16 ||
       (p->flags & ~(uint32_t)SD_NO_BONUS))
     return SD_EINVAL;
-  if (p->max_nodes > SD_MAX_NODES || p->V >= (1 << 28) || p->N > (1 << 24)) return SD_EUNSUPPORTED;
+  if (p->max_nodes > SD_MAX_NODES || p->V >= (1 << 28) || p->N > (1 << 24) || p->B > 65535) return SD_EUNSUPPORTED;
   return SD_OK;
 }
 
-// Vocabulary slices of a row: enough workgroups for the chip, none below 512
-// vectors.
-int slice_count(int N, int nvec) {
-  return std::max(1, std::min({(2048 + N - 1) / N, (nvec + 511) / 512, 64}));
-}
-
-// Whether to read only the rows that the walks visit.  One workgroup reads a
-// row at about 70 GB/s, a full chip at about 4.5 TB/s, and a step of a walk
-// costs about 2 us beside its bytes: reading all N rows takes longer than a walk
-// of d + 1 rows when N > (d + 1) (64 + 9 MB / row).  Walks are rarely deeper than
-// 16 (a deeper one costs at most four times what reading all rows would).
+// Whether to read only the rows that the walks visit.  A step of that takes
+// about 5.5 us (64 requests, 152064 bf16 logits); reading every row, at about
+// 4.5 TB/s, is the shorter way where it takes no longer than half of the steps of
+// a walk of max_nodes, or of 16, which walks are rarely longer than: 12 MB a step.
+// (64 trees of 64 nodes: 215 us for all rows, 41 us for walks of up to 7.)
 bool walk_rows(const sd_tree_verify_args_t* p) {
   const int64_t row = (int64_t)p->V * (p->dtype == SD_BF16 ? 2 : 4);
-  return p->N * row > std::min(p->max_nodes, 16) * (64 * row + (9 << 20));
+  return p->N * row > std::min(p->max_nodes, 16) * (int64_t)(12 << 20);
+}
+
+// Workgroups a row is shared by, and the 16-byte vectors of each.
+struct Slices {
+  int count, vecs;
+  bool walk;
+};
+
+Slices slices_of(const sd_tree_verify_args_t* p) {
+  const int E = p->dtype == SD_BF16 ? 8 : 4, nvec = (p->V + E - 1) / E;
+  Slices s;
+  s.walk = walk_rows(p);
+  // all rows: about 2048 workgroups; walks: about two a CU.  None below 512 vectors.
+  const int rows = s.walk ? p->B : p->N, want = s.walk ? 512 : 2048;
+  s.count = std::max(1, std::min({(want + rows - 1) / rows, (nvec + 511) / 512, 64}));
+  s.vecs = (nvec + s.count - 1) / s.count;
+  return s;
+}
+
+size_t parts_bytes(const sd_tree_verify_args_t* p, const Slices& s) {
+  return ((size_t)(s.walk ? p->B : p->N) * s.count * 8 + 63) & ~(size_t)63;
 }
 
 }  // namespace
@@ -252,8 +384,8 @@ extern "C" int sd_tree_verify_workspace_bytes(const sd_tree_verify_args_t* args,
   if (!bytes) return SD_EINVAL;
   const int rc = check(args);
   if (rc) return rc;
-  const int E = args->dtype == SD_BF16 ? 8 : 4;
-  *bytes = (size_t)args->N * slice_count(args->N, (args->V + E - 1) / E) * 8;
+  const Slices s = slices_of(args);
+  *bytes = parts_bytes(args, s) + (s.walk ? (size_t)args->B * sizeof(Team) : 0);
   return SD_OK;
 }
 
@@ -266,23 +398,25 @@ extern "C" int sd_tree_verify_greedy(const sd_tree_verify_args_t* args, void* wo
   if (rc) return rc;
   if (!out_accepted || !out_path || !out_tokens) return SD_EINVAL;
   if (!workspace || workspace_bytes < need || (uintptr_t)workspace % 8) return SD_EWORKSPACE;
-  const int E = args->dtype == SD_BF16 ? 8 : 4, nvec = (args->V + E - 1) / E;
+  const Slices s = slices_of(args);
   VerifyArgs a;
   a.logits = static_cast<const char*>(args->logits);
-  a.row_bytes = args->ld * (16 / E);
+  a.row_bytes = args->ld * (args->dtype == SD_BF16 ? 2 : 4);
   a.tokens = args->tokens, a.parents = args->parents, a.off = args->node_offsets;
   a.B = args->B, a.N = args->N, a.V = args->V, a.max_nodes = args->max_nodes;
   a.flags = args->flags;
-  a.slices = slice_count(a.N, nvec);
-  a.slice_vecs = (nvec + a.slices - 1) / a.slices;
+  a.slices = s.count, a.slice_vecs = s.vecs;
   a.part = static_cast<uint64_t*>(workspace);
+  a.team = reinterpret_cast<Team*>(static_cast<char*>(workspace) + parts_bytes(args, s));
   a.accepted = out_accepted, a.path = out_path, a.out_tokens = out_tokens, a.status = out_status;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (walk_rows(args)) {
+  if (s.walk) {
+    hipLaunchKernelGGL(k_tree_begin, dim3(a.B), dim3(WAVE), 0, st, a);
+    if (hipGetLastError() != hipSuccess) return SD_EHIP;
     if (args->dtype == SD_BF16)
-      hipLaunchKernelGGL(k_tree_descend<SD_BF16>, dim3(a.B), dim3(NT_D), 0, st, a);
+      hipLaunchKernelGGL(k_tree_descend<SD_BF16>, dim3(a.slices, a.B), dim3(NT_D), 0, st, a);
     else
-      hipLaunchKernelGGL(k_tree_descend<SD_F32>, dim3(a.B), dim3(NT_D), 0, st, a);
+      hipLaunchKernelGGL(k_tree_descend<SD_F32>, dim3(a.slices, a.B), dim3(NT_D), 0, st, a);
     return hipGetLastError() == hipSuccess ? SD_OK : SD_EHIP;
   }
   if (args->dtype == SD_BF16)

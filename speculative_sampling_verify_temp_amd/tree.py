@@ -206,7 +206,7 @@ def _cache(k, v, table, lens):
 
 
 def _workspace(size, a, given, like, keep):
-    """The given workspace or a new one: (pointer, bytes)."""
+    """The given workspace or a new one, if one is needed: (pointer, bytes)."""
     import torch
     if given is not None:
         if not given.is_contiguous():
@@ -214,7 +214,9 @@ def _workspace(size, a, given, like, keep):
         _here(like, given)
         return given.data_ptr(), given.numel() * given.element_size()
     n = size(a)
-    ws = torch.empty(max(16, n), dtype=torch.uint8, device=like.device)
+    if n == 0:
+        return None, 0
+    ws = torch.empty(n, dtype=torch.uint8, device=like.device)
     keep.append(ws)
     return ws.data_ptr(), n
 
@@ -279,7 +281,7 @@ def tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, 
     shape = q.shape
     keep = []
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty(shape)
         keep.append(out)
     else:
         _plain(out, q.dtype, "out", *shape)

@@ -47,6 +47,27 @@ def test_chains_and_trees_match_the_oracle(case, dtype):
     c.check_attention(*_run(c, parents=dev(parents)), c.reference(parents=parents))
 
 
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 14)])
+def test_many_requests(D, Hq):
+    """More requests than a wave has lanes, some without nodes or slots, in a
+    table with room for long contexts."""
+    rng = np.random.default_rng(D)
+    lens = rng.integers(0, 90, 150).tolist()
+    lens[70], lens[149] = 700, 1100
+    nodes = rng.integers(0, 4, 150).tolist()
+    c = Cached(41, lens, nodes, Hq, 2, D, 16, "bf16")
+    c.check_attention(*_run(c), c.reference())
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.07, 0.3])
+def test_other_scales(scale):
+    """Scales of zero (a plain mean) and below."""
+    for D in (64, 128):
+        c = Cached(42, [100, 0, 600], [3, 2, 30], 8, 2, D, 16, "f16")
+        c.scale = scale
+        c.check_attention(*_run(c), c.reference())
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_masks_and_what_hides_behind_them(D):
     """Arbitrary masks: rows that see nothing, bits past the tree, and nodes
@@ -147,7 +168,7 @@ def test_same_bits_on_every_call_and_stream_and_in_a_graph():
     torch.cuda.synchronize()
     assert torch.equal(a, b) and torch.equal(la, lb)
     args = sdv.make_tree_attention_args(**c.attention_args(), max_nodes=64, scale=c.scale)
-    ws = torch.empty(sdv.tree_attention_workspace_bytes(args), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(16, sdv.tree_attention_workspace_bytes(args)), dtype=torch.uint8, device="cuda")
     out, lse = torch.zeros_like(a), torch.zeros_like(la)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):

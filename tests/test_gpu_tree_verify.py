@@ -34,7 +34,7 @@ def _agreeing(rng, z, parents, offsets, depth):
 @pytest.mark.parametrize("nodes,V", [([1], 1), ([3, 1, 64], 7), ([5, 9, 2], 1000), ([64] * 70, 333), ([16, 33], 20011),
                                      ([2, 7], 152064), ([8] * 300, 2050), ([1, 4] * 40, 9001),
                                      # enough rows that only the visited ones are read
-                                     ([1] * 300, 20011), ([4, 2, 3, 1] * 150, 30001), ([9] * 260, 20011)])
+                                     ([1] * 330, 20011), ([4, 2, 3, 1] * 150, 30001), ([9] * 330, 20011)])
 def test_walks_match_the_oracle(nodes, V, dtype):
     rng = np.random.default_rng(len(nodes) + V)
     off = np.concatenate([[0], np.cumsum(nodes)]).astype(np.int32)
@@ -55,7 +55,44 @@ def test_walks_match_the_oracle(nodes, V, dtype):
             assert np.array_equal(g.cpu().numpy(), w), name
 
 
-@pytest.mark.parametrize("B", [1, 90, 1200])
+@pytest.mark.parametrize("B,T,V,dtype", [(48, 16, 152064, "bf16"), (64, 30, 152063, "bf16"), (9, 64, 151936, "f32"),
+                                         (700, 5, 40000, "f32")])
+def test_large_batches_against_every_row(B, T, V, dtype):
+    """Batches whose walks read their own rows, against the argmax of every row
+    on the device."""
+    import torch
+    sdv = _sdv()
+    rng = np.random.default_rng(B)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    z = torch.randn((B * T, -(-V // 8) * 8), generator=g, device="cuda").to(torch_dtype(dtype))[:, :V] * 3
+    z = torch.nn.functional.pad(z, (0, -V % 8), value=float("nan"))[:, :V]      # rows padded with NaN
+    best = torch.where(z == z.amax(1, keepdim=True), torch.arange(V, device="cuda", dtype=torch.int32), V).amin(1)
+    best = best.cpu().numpy()
+    off = (np.arange(B + 1) * T).astype(np.int32)
+    parents = np.concatenate([random_tree(rng, T) for _ in range(B)]).astype(np.int32)
+    tokens = rng.integers(0, V, B * T).astype(np.int32)
+    for i in range(B * T):                      # most nodes continue their parent's best token
+        if parents[i] >= 0 and rng.random() < 0.7:
+            tokens[i] = best[i // T * T + parents[i]]
+    acc, path, tok = sdv.tree_verify_greedy(z, dev(tokens), dev(parents), dev(off), T)
+    a, p = np.zeros(B, np.int32), np.full((B, T), -1, np.int32)
+    for b in range(B):
+        cur, n = 0, 0
+        while True:
+            p[b, n] = cur
+            kids = [c for c in range(cur + 1, T) if parents[b * T + c] == cur and tokens[b * T + c] == best[b * T + cur]]
+            if not kids:
+                break
+            cur, n = kids[0], n + 1
+        a[b] = n
+    assert np.array_equal(acc.cpu().numpy(), a) and np.array_equal(path.cpu().numpy(), p)
+    want = np.where(p >= 0, best[np.arange(B)[:, None] * T + np.maximum(p, 0)], -1)
+    assert np.array_equal(tok.cpu().numpy(), want)
+    assert a.max() >= 3 or T < 6
+
+
+@pytest.mark.parametrize("B", [1, 90, 1600])
 def test_a_deep_chain_is_walked_to_its_end(B):
     rng = np.random.default_rng(2)
     T, V = 64, 516
@@ -69,7 +106,7 @@ def test_a_deep_chain_is_walked_to_its_end(B):
     assert np.array_equal(tok.cpu().numpy(), z.argmax(1).reshape(B, T))
 
 
-@pytest.mark.parametrize("copies", [1, 60, 520])
+@pytest.mark.parametrize("copies", [1, 60, 700])
 def test_defects_are_reported_request_by_request(copies):
     import torch
     sdv = _sdv()

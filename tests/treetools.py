@@ -84,8 +84,9 @@ class Cached:
         """Bound of a score's error: products of 8- or 11-bit numbers are exact
         in fp32, so D additions and the scaling, each off by 2^-24 of the sum
         of magnitudes; the exponent's argument in base 2 adds two more."""
-        mag = self.scale * self.D * np.abs(self.q).max() * max(np.abs(self.k).max(), np.abs(self.kn).max())
-        top = self.scale * np.linalg.norm(self.q, axis=-1).max() * \
+        scale = abs(self.scale)
+        mag = scale * self.D * np.abs(self.q).max() * max(np.abs(self.k).max(), np.abs(self.kn).max())
+        top = scale * np.linalg.norm(self.q, axis=-1).max() * \
             max(np.linalg.norm(self.k, axis=-1).max(), np.linalg.norm(self.kn, axis=-1).max())
         return (self.D + 4) * 2.0 ** -24 * min(mag, 4 * top)
 
