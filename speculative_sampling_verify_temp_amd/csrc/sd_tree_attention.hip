@@ -139,7 +139,7 @@ struct Shape {
   static constexpr int JR = D + 4;               // floats of a row in the join of the key groups
   static constexpr int JOIN = (KG - 1) * RT * JR * 4;
   static constexpr int LDS = 2 * KG * TILE > JOIN ? 2 * KG * TILE : JOIN;
-  static constexpr int SLOT = RT * (D + 2);      // floats of a partial result
+  static constexpr int SLOT = RT * (D + 3);      // floats of a partial result
   static_assert(KT >= SD_MAX_NODES && KEYS <= 64, "the tree is one tile");
 };
 
@@ -231,10 +231,14 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
           q[m][ks] = on ? *(const s16x8*)(qp + (ks * 32 + g4 * 8) * 2) ^ sign : s16x8{};
       }
       f32x4 o[MT][DTS];
+      // sum: of the weights, for the log-sum-exp; norm (any of its 4 equal
+      // entries): of the weights as the product sees them, which it is divided by
+      f32x4 norm[MT];
       float mx[MT], sum[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         mx[m] = -INFINITY, sum[m] = 0.0f;
+        norm[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int d = 0; d < DTS; ++d) o[m][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       }
@@ -364,6 +368,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
             const float f = mn > -INFINITY ? fast_exp2(mx[m] - mn) : 1.0f;
             mx[m] = mn;
             sum[m] *= f;
+            norm[m] *= f;
 #pragma unroll
             for (int d = 0; d < DTS; ++d) o[m][d] *= f;
           }
@@ -381,10 +386,14 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
               for (int r = 0; r < 4; ++r) {
                 const float y = fast_exp2(fmaf(x[ns * 2 + s][m][r], c, -ms[m]));
                 sum[m] += y;
-                // the weights enter the product in the element type: half a
-                // step each, and the sum keeps their fp32 values
+                // the weights enter the product in the element type, half a
+                // step off each; dividing by the sum of the rounded ones takes
+                // the rounding of a weight that dominates out again
                 p[m][s * 4 + r] = (short)from_f32<DT>(y);
               }
+          const s16x8 ones = s16x8{} + (short)(DT == SD_BF16 ? 0x3F80 : 0x3C00);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) norm[m] = mfma<DT>(ones, p[m], norm[m]);
           // O^T
 #pragma unroll
           for (int d = 0; d < DTS; ++d) {
@@ -453,7 +462,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
             float* const zr = z + (16 * m + n) * S::JR;
 #pragma unroll
             for (int d = 0; d < DTS; ++d) *(f32x4*)(zr + d * 16 + g4 * 4) = o[m][d];
-            if (g4 == 0) zr[D] = mx[m], zr[D + 1] = sum[m];
+            if (g4 == 0) zr[D] = mx[m], zr[D + 1] = sum[m], zr[D + 2] = norm[m][0];
           }
         }
         __syncthreads();
@@ -467,6 +476,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
               const float f1 = fast_exp2(mx[m] - ms), f2 = fast_exp2(m2 - ms);
               mx[m] = mn;
               sum[m] = sum[m] * f1 + zr[D + 1] * f2;
+              norm[m][0] = norm[m][0] * f1 + zr[D + 2] * f2;
 #pragma unroll
               for (int d = 0; d < DTS; ++d) o[m][d] = o[m][d] * f1 + *(const f32x4*)(zr + d * 16 + g4 * 4) * f2;
             }
@@ -497,7 +507,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
           if (r >= rows) continue;
           if (whole) {
             const bool none = sum[m] == 0.0f;
-            const float inv = none ? 0.0f : 1.0f / sum[m];
+            const float inv = none ? 0.0f : 1.0f / norm[m][0];
             const int64_t at = (int64_t)(first + node[m]) * a.Hq + h * a.G + (r - node[m] * a.G);
             char* const out = a.out + at * (D * 2);
 #pragma unroll
@@ -517,6 +527,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
             if (g4 == 0) {
               part[S::RT * D + lr] = mx[m];
               part[S::RT * D + S::RT + lr] = sum[m];
+              part[S::RT * D + 2 * S::RT + lr] = norm[m][0];
             }
           }
         }
@@ -554,10 +565,10 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int runs) {
   const int w0 = (int)((unsigned)s / (unsigned)per), w1 = (int)((unsigned)(s + nt - 1) / (unsigned)per);
   const int lin = blockIdx.x * 256 + threadIdx.x, lr = lin / GPR, col = lin % GPR, r = mt * S::RT + lr;
   if (w0 == w1 || r >= lane_read(rq.T, f) * a.G) return;
-  float m = -INFINITY, sum = 0.0f;
+  float m = -INFINITY, sum = 0.0f, norm = 0.0f;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int w = w0; w <= w1; w += 4) {
-    float pm[4], ps[4];
+    float pm[4], ps[4], pn[4];
     f32x4 po[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -565,6 +576,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int runs) {
       const float* z = a.part + (int64_t)(wi * 2 + (wi == w0)) * S::SLOT;
       pm[i] = z[S::RT * D + lr];
       ps[i] = z[S::RT * D + S::RT + lr];
+      pn[i] = z[S::RT * D + 2 * S::RT + lr];
       po[i] = *(const f32x4*)(z + lr * D + col * 4);
     }
 #pragma unroll
@@ -574,11 +586,12 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int runs) {
       const float f1 = fast_exp2(m - ms), f2 = fast_exp2(pm[i] - ms);
       m = mn;
       sum = sum * f1 + ps[i] * f2;
+      norm = norm * f1 + pn[i] * f2;
       o = o * f1 + po[i] * f2;
     }
   }
   const bool none = sum == 0.0f;
-  const float inv = none ? 0.0f : 1.0f / sum;
+  const float inv = none ? 0.0f : 1.0f / norm;
   const int node = row_node(a, r);
   const int64_t at = (int64_t)(lane_read(rq.first, f) + node) * a.Hq + h * a.G + (r - node * a.G);
   uint32_t u[2];
