@@ -72,15 +72,31 @@ __device__ __forceinline__ Requests requests(const AttnArgs& a, int b) {
 
 __device__ __forceinline__ int lane_units(const Requests& r) { return lane_read(r.incl, WAVE - 1); }
 
-// All units; r: the first 64 requests.
-template <int RT, int KT>
-__device__ __forceinline__ int total_units(const AttnArgs& a, const Requests& r) {
-  int u = lane_units(r);
-  for (int b0 = WAVE; b0 < a.c.B; b0 += WAVE) u += lane_units(requests<RT, KT>(a, b0 + (int)threadIdx.x % WAVE));
-  return u;
+__device__ __forceinline__ int wave_max_int(int x) {
+  x = max(x, dpp_i32<DPP_XOR1>(x));
+  x = max(x, dpp_i32<DPP_XOR2>(x));
+  x = max(x, dpp_i32<DPP_ROW_HALF_MIRROR>(x));
+  x = max(x, dpp_i32<DPP_ROW_MIRROR>(x));
+  return max(max(lane_read(x, 0), lane_read(x, 16)), max(lane_read(x, 32), lane_read(x, 48)));
 }
 
-__device__ __forceinline__ int run_length(int units, int runs) { return (int)(((unsigned)units + runs - 1) / (unsigned)runs); }
+// All units, and the units of a run: equal shares, but no row tile in more than
+// about 32 parts, which the join would take longer to add up than their runs
+// save.  r: the first 64 requests.
+struct Cut {
+  int total, per;
+};
+
+template <int RT, int KT>
+__device__ __forceinline__ Cut cut_units(const AttnArgs& a, const Requests& r, int runs) {
+  int total = lane_units(r), nt = r.nt;
+  for (int b0 = WAVE; b0 < a.c.B; b0 += WAVE) {
+    const Requests q = requests<RT, KT>(a, b0 + (int)threadIdx.x % WAVE);
+    total += lane_units(q);
+    nt = max(nt, q.nt);
+  }
+  return Cut{total, max((int)(((unsigned)total + runs - 1) / (unsigned)runs), (wave_max_int(nt) + 31) / 32)};
+}
 
 // r / G for a packed row (exact: r < 2^11, G <= 32).
 __device__ __forceinline__ int row_node(const AttnArgs& a, int r) { return (int)(((float)r + 0.5f) * a.inv_G); }
@@ -164,7 +180,8 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
   } else {
     // Workgroups of one XCD take neighbouring runs: row tiles of one KV head
     // find each other's keys in its L2.
-    const int runs = gridDim.x, total = total_units<S::RT, S::KT>(a, rq), per = run_length(total, runs);
+    const int runs = gridDim.x;
+    const auto [total, per] = cut_units<S::RT, S::KT>(a, rq, runs);
     run = (int)(blockIdx.x % 8) * (runs / 8) + (int)(blockIdx.x / 8);      // runs is a multiple of 8
     if ((int64_t)run * per >= total) return;
     u0 = run * per, u1 = min(total, u0 + per);
@@ -545,14 +562,14 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
 }
 
 // Rows whose key tiles went to several runs: their parts in the order of the
-// runs, four at a time.  grid (4-column groups of a row tile / 256, H * row
+// runs, JN at a time.  grid (4-column groups of a row tile / 256, H * row
 // tiles, B).
 template <int DT, typename S>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int runs) {
-  constexpr int D = S::D, GPR = D / 4;
+  constexpr int D = S::D, GPR = D / 4, JN = 8;
   const int b = blockIdx.z, h = blockIdx.y / a.mts_max, mt = blockIdx.y % a.mts_max, l = threadIdx.x % WAVE;
   Requests rq = requests<S::RT, S::KT>(a, l);
-  const int per = run_length(total_units<S::RT, S::KT>(a, rq), runs);
+  const int per = cut_units<S::RT, S::KT>(a, rq, runs).per;
   int before = 0;
   for (int b0 = 0; b0 + WAVE <= b; b0 += WAVE) {
     before += lane_units(rq);
@@ -567,11 +584,11 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int runs) {
   if (w0 == w1 || r >= lane_read(rq.T, f) * a.G) return;
   float m = -INFINITY, sum = 0.0f, norm = 0.0f;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int w = w0; w <= w1; w += 4) {
-    float pm[4], ps[4], pn[4];
-    f32x4 po[4];
+  for (int w = w0; w <= w1; w += JN) {
+    float pm[JN], ps[JN], pn[JN];
+    f32x4 po[JN];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < JN; ++i) {
       const int wi = min(w + i, w1);
       const float* z = a.part + (int64_t)(wi * 2 + (wi == w0)) * S::SLOT;
       pm[i] = z[S::RT * D + lr];
@@ -580,7 +597,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int runs) {
       po[i] = *(const f32x4*)(z + lr * D + col * 4);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < JN; ++i) {
       if (w + i > w1) break;
       const float mn = fmaxf(m, pm[i]), ms = mn > -INFINITY ? mn : 0.0f;
       const float f1 = fast_exp2(m - ms), f2 = fast_exp2(pm[i] - ms);
@@ -661,9 +678,9 @@ AttnArgs device_args(const sd_tree_attention_args_t* p) {
 template <int D, typename F>
 auto with_shape(int rows, F&& f) {
   if (rows <= 16) return f(Shape<D, 1, 1, 4, 1>{});
-  if (rows <= 32) return f(Shape<D, 2, 1, 4, 1>{});
-  if (rows <= 64) return f(Shape<D, 2, 2, 2, 1>{});
-  if (rows <= 128) return f(Shape<D, 2, 4, 1, 2>{});
+  if (rows <= 32) return f(Shape<D, 1, 2, 2, 1>{});
+  if (rows <= 64) return f(Shape<D, 1, 4, 1, 2>{});
+  if (rows <= 128) return f(Shape<D, 1, 8, 1, 2>{});
   return f(Shape<D, 2, 8, 1, 2>{});
 }
 
