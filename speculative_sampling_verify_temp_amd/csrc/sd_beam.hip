@@ -7,7 +7,7 @@
 //                slices, the candidates' scores in 64 bits, the n_out best.
 //
 // Both choose the n best of many in the same way: the n-th largest of 64 maxima,
-// of the values of 4 threads each, bounds the n-th largest of all from below, so
+// each of a 64th of the threads, bounds the n-th largest of all from below, so
 // only the values not below it (about n, 300 at n = 64) are listed and ranked by
 // counting the larger ones.  Where ties make that list overflow the best are
 // taken one by one.
@@ -24,6 +24,7 @@ using namespace sdt;
 namespace {
 
 constexpr int NT_B = 256;
+constexpr int NT_M = 1024;       // threads of a merge
 constexpr int NV = 4;            // 16-byte vectors of a thread's part of a slice
 constexpr int LIST = 1024;       // places for the values not below the bound
 constexpr int MAXO = SD_MAX_BEAMS;
@@ -47,47 +48,40 @@ __device__ __forceinline__ bool examined(const BeamArgs& a, int bw) {
   return !(a.ended && a.ended[bw]) && a.scores[bw] > -INFINITY;
 }
 
+template <int NT>
 __device__ __forceinline__ uint64_t block_max_u64(uint64_t x, uint64_t* scratch) {
   x = wave_max_u64(x);
   __syncthreads();
   if (threadIdx.x % WAVE == 0) scratch[threadIdx.x / WAVE] = x;
   __syncthreads();
-  for (int w = 0; w < NT_B / WAVE; ++w) x = scratch[w] > x ? scratch[w] : x;
+  for (int w = 0; w < NT / WAVE; ++w) x = scratch[w] > x ? scratch[w] : x;
   return x;
 }
 
-__device__ __forceinline__ uint32_t quad_lanes_max(uint32_t x) {
-  x = max(x, (uint32_t)dpp_i32<DPP_XOR1>((int)x));
-  return max(x, (uint32_t)dpp_i32<DPP_XOR2>((int)x));
-}
-__device__ __forceinline__ uint64_t quad_lanes_max(uint64_t x) {
+template <int LANES, typename K>
+__device__ __forceinline__ K lanes_max(K x) {
 #pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    const uint64_t y = __shfl_xor(x, o);
+  for (int o = 1; o < LANES; o <<= 1) {
+    const K y = __shfl_xor(x, o);
     x = y > x ? y : x;
   }
   return x;
 }
 
-// The n-th largest (n <= 64) of the maxima of groups of 4 threads, in every
-// thread; keys: 64 of LDS.  Every wave ranks the 64 by counting.
-template <typename K>
-__device__ __forceinline__ K nth_group_max(K mine, int n, K* keys) {
-  static_assert(NT_B == 4 * WAVE, "64 groups of 4 threads");
-  const int tid = threadIdx.x, l = tid % WAVE;
-  mine = quad_lanes_max(mine);
-  if (tid % 4 == 0) keys[tid / 4] = mine;
-  __syncthreads();
-  const K k = keys[l];
-  int rank = 0;
+// The n-th largest (n <= 64) of the 64 keys in LDS, in every thread: bit by bit
+// from the top, the largest value that n of a wave's 64 lanes reach.  Bits below
+// LOW are the same in all keys of one sign: n lanes that reach a value with them
+// clear are enough of a bound.
+template <int LOW, typename K>
+__device__ __forceinline__ K nth_of_64(const K* keys, int n) {
+  const K k = keys[threadIdx.x % WAVE];
+  K edge = 0;
 #pragma unroll
-  for (int i = 0; i < WAVE; ++i) {
-    const K o = keys[i];
-    rank += o > k || (o == k && i < l);
+  for (int bit = (int)sizeof(K) * 8 - 1; bit >= LOW; --bit) {
+    const K c = edge | (K)1 << bit;
+    if (__popcll(__ballot(k >= c)) >= n) edge = c;
   }
-  const int at = __builtin_ctzll(__ballot(rank == n - 1));
-  if constexpr (sizeof(K) == 4) return (K)lane_read((int)k, at);
-  return ((uint64_t)(uint32_t)lane_read((int)(uint32_t)(k >> 32), at) << 32) | (uint32_t)lane_read((int)(uint32_t)k, at);
+  return edge;
 }
 
 // Logit e of a 16-byte vector.
@@ -143,27 +137,26 @@ __global__ __launch_bounds__(NT_B, 6) void k_beam_rows(BeamArgs a) {
       w[u] = make_uint4(q[0], q[1], q[2], q[3]);
     }
   }
-  Extremes<DT> x;
-  x.clear();
+  bool nan = false;
+  float vtop[NV], top = -INFINITY;
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
+    Extremes<DT> x;
+    x.clear();
     x.add(w[u].x);
     x.add(w[u].y);
     x.add(w[u].z);
     x.add(w[u].w);
+    vtop[u] = x.value(nan);
+    top = fmaxf(top, vtop[u]);
   }
-  bool nan = false;
-  const float top = x.value(nan);
-  // a NaN or +inf anywhere makes the maximum +inf
-  const float m = block_max<NT_B>(nan ? INFINITY : top, sf);
-  if (m == INFINITY) {
-    if (tid == 0) a.part_m[out] = __builtin_nanf("");
-    return;
-  }
+  if (nan) top = INFINITY;           // reported like one
+  // exponentials against the thread's own maximum: at most 32 terms of at most
+  // 1 in fp32; the threads' sums meet in 64 bits
   constexpr float C = 1.4426950408889634f;
   float s = 0.0f;
-  if (m > -INFINITY) {
-    const float g = m * C;
+  if (top > -INFINITY && top < INFINITY) {
+    const float g = top * C;
 #pragma unroll
     for (int u = 0; u < NV; ++u)
       if (u < mine) {
@@ -171,26 +164,41 @@ __global__ __launch_bounds__(NT_B, 6) void k_beam_rows(BeamArgs a) {
         for (int e = 0; e < E; ++e) s += fast_exp2(fmaf(logit_of<DT>(w[u], e), C, -g));
       }
   }
-  // at most 64 terms of at most 1 in fp32, the rest in 64 bits
-  const double total = block_sum<NT_B>((double)s, sd);
-  if (tid == 0) a.part_m[out] = m, a.part_s[out] = total;
-
-  uint64_t* const best = a.part_best + out * a.n_out;
-  const uint32_t floor = ord_key(-INFINITY);         // not a candidate
-  const uint32_t edge = nth_group_max(ord_key(top), a.n_out, keys);
-  if (ord_key(top) >= edge && top > -INFINITY) {
+  const uint32_t o = ord_key(top), group = lanes_max<4>(o);
+  const float wtop = wave_max(top);
+  if (tid % 4 == 0) keys[tid / 4] = group;
+  if (tid % WAVE == 0) sf[tid / WAVE] = wtop;
+  __syncthreads();
+  float m = sf[0];
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
+  for (int i = 1; i < NT_B / WAVE; ++i) m = fmaxf(m, sf[i]);
+  if (m == INFINITY) {
+    if (tid == 0) a.part_m[out] = __builtin_nanf("");
+    return;
+  }
+  const uint32_t floor = ord_key(-INFINITY);         // not a candidate
+  const uint32_t edge = nth_of_64<DT == SD_BF16 ? 16 : 0>(keys, a.n_out);
+  const double part = wave_sum(top > -INFINITY ? (double)s * (double)fast_exp2((top - m) * C) : 0.0);
+  if (tid % WAVE == 0) sd[tid / WAVE] = part;
+  uint64_t* const best = a.part_best + out * a.n_out;
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+    if (ord_key(vtop[u]) >= edge && vtop[u] > -INFINITY) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const uint32_t o = ord_key(logit_of<DT>(w[u], e));
-        if (o >= edge && o > floor) {
+        const uint32_t k = ord_key(logit_of<DT>(w[u], e));
+        if (k >= edge && k > floor) {
           const int at = atomicAdd(&listed, 1);
-          if (at < LIST) list[at] = ((uint64_t)o << 32) | (uint32_t)~((lo + u * NT_B + tid) * E + e);
+          if (at < LIST) list[at] = ((uint64_t)k << 32) | (uint32_t)~((lo + u * NT_B + tid) * E + e);
         }
       }
-  }
+    }
   __syncthreads();
+  if (tid == 0) {
+    double total = 0.0;
+    for (int i = 0; i < NT_B / WAVE; ++i) total += sd[i];
+    a.part_m[out] = m, a.part_s[out] = total;
+  }
   const int n = listed;
   if (n <= LIST) {
     for (int i = tid; i < n; i += NT_B) {
@@ -213,7 +221,7 @@ __global__ __launch_bounds__(NT_B, 6) void k_beam_rows(BeamArgs a) {
         const uint64_t k = ((uint64_t)o << 32) | (uint32_t)~((lo + u * NT_B + tid) * E + e);
         if (o > floor && k < last && k > b) b = k;
       }
-    last = block_max_u64(b, su);
+    last = block_max_u64<NT_B>(b, su);
     if (tid == 0) best[j] = last;
   }
 }
@@ -239,18 +247,18 @@ struct Candidate {
   __device__ bool over(const Candidate& o) const { return s > o.s || (s == o.s && i > o.i); }
 };
 
-__global__ __launch_bounds__(NT_B) void k_beam_merge(BeamArgs a) {
+__global__ __launch_bounds__(NT_M) void k_beam_merge(BeamArgs a) {
   __shared__ double lse[MAXO];
   __shared__ uint8_t kind[MAXO];      // 0: no candidates, 1: its slices', 2: ended
   __shared__ uint32_t st_sh;
   __shared__ __align__(16) uint64_t keys[WAVE];
-  __shared__ uint64_t su[NT_B / WAVE], list_s[LIST], list_i[LIST];
+  __shared__ uint64_t su[NT_M / WAVE], list_s[LIST], list_i[LIST];
   __shared__ float score[MAXO];
   __shared__ int listed;
   const int b = blockIdx.x, tid = threadIdx.x, l = tid % WAVE;
   if (tid == 0) st_sh = 0, listed = 0;
   __syncthreads();
-  for (int w = tid / WAVE; w < a.W; w += NT_B / WAVE) {
+  for (int w = tid / WAVE; w < a.W; w += NT_M / WAVE) {
     const int bw = b * a.W + w;
     const float sc = a.scores[bw];
     uint32_t st = 0;
@@ -309,10 +317,13 @@ __global__ __launch_bounds__(NT_B) void k_beam_merge(BeamArgs a) {
     if (a.out_ended) a.out_ended[o] = x.s && (kind[w] == 2 || id == a.eos);
   };
   uint64_t top = 0;
-  for (int c = tid; c < total; c += NT_B) top = max(top, candidate(c).s);
-  const uint64_t edge = nth_group_max(top, a.n_out, keys);
+  for (int c = tid; c < total; c += NT_M) top = max(top, candidate(c).s);
+  const uint64_t group = lanes_max<NT_M / WAVE>(top);
+  if (tid % (NT_M / WAVE) == 0) keys[tid / (NT_M / WAVE)] = group;
+  __syncthreads();
+  const uint64_t edge = nth_of_64<0>(keys, a.n_out);
   if (top >= edge && top) {
-    for (int c = tid; c < total; c += NT_B) {
+    for (int c = tid; c < total; c += NT_M) {
       const Candidate x = candidate(c);
       if (x.s >= edge && x.s) {
         const int at = atomicAdd(&listed, 1);
@@ -323,23 +334,23 @@ __global__ __launch_bounds__(NT_B) void k_beam_merge(BeamArgs a) {
   __syncthreads();
   const int n = listed;
   if (n <= LIST) {
-    for (int i = tid; i < n; i += NT_B) {
+    for (int i = tid; i < n; i += NT_M) {
       const Candidate x{list_s[i], list_i[i]};
       int rank = 0;
       for (int j = 0; j < n; ++j) rank += Candidate{list_s[j], list_i[j]}.over(x);
       if (rank < a.n_out) put(rank, x);
     }
-    for (int j = n + tid; j < a.n_out; j += NT_B) put(j, Candidate{0, 0});
+    for (int j = n + tid; j < a.n_out; j += NT_M) put(j, Candidate{0, 0});
   } else {
     Candidate last{~0ull, ~0ull};
     for (int j = 0; j < a.n_out; ++j) {
       Candidate best{0, 0};
-      for (int c = tid; c < total; c += NT_B) {
+      for (int c = tid; c < total; c += NT_M) {
         const Candidate x = candidate(c);
         if (last.over(x) && x.over(best)) best = x;
       }
-      const uint64_t s = block_max_u64(best.s, su);
-      const uint64_t i = block_max_u64(best.s == s ? best.i : 0, su);
+      const uint64_t s = block_max_u64<NT_M>(best.s, su);
+      const uint64_t i = block_max_u64<NT_M>(best.s == s ? best.i : 0, su);
       last = Candidate{s, i};
       if (tid == 0) put(j, last);
     }
@@ -463,7 +474,7 @@ extern "C" int sd_beam_select(const sd_beam_select_args_t* args, void* workspace
   if (args->dtype == SD_BF16) hipLaunchKernelGGL(k_beam_rows<SD_BF16>, grid, dim3(NT_B), 0, st, a);
   else hipLaunchKernelGGL(k_beam_rows<SD_F32>, grid, dim3(NT_B), 0, st, a);
   if (hipGetLastError() != hipSuccess) return SD_EHIP;
-  hipLaunchKernelGGL(k_beam_merge, dim3(a.B), dim3(NT_B), 0, st, a);
+  hipLaunchKernelGGL(k_beam_merge, dim3(a.B), dim3(NT_M), 0, st, a);
   return hipGetLastError() == hipSuccess ? SD_OK : SD_EHIP;
 }
 

@@ -161,7 +161,7 @@ struct Shape {
 
 template <int DT, typename S>
 __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
-  constexpr int D = S::D, MT = S::MT, RG = S::RG, KG = S::KG, NS = S::NS, KS = D / 32, DTS = D / 16, VA = 4;      // VA: V operands read ahead
+  constexpr int D = S::D, MT = S::MT, RG = S::RG, KG = S::KG, NS = S::NS, KS = D / 32, DTS = D / 16, VA = 2;      // VA: V operands read ahead
   __shared__ __align__(16) char lds[S::LDS];
   __shared__ int odd_value;      // a tree value is infinite or not a number
   const int tid = threadIdx.x, l = tid % WAVE, w = tid / WAVE, n = l & 15, g4 = l >> 4;
