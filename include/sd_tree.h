@@ -96,8 +96,9 @@ typedef struct sd_kv_cache {
  * out = softmax(scores) . v, rounded once to the element type; out_lse (may
  * be NULL) = log sum exp(scores).  A row that sees nothing gets zeros and
  * -inf.  Keys and values that a row does not see never reach its result,
- * whatever they hold.  Rows of an invalid request get zeros and -inf.
- * Rows of packed nodes that belong to no request are left as they were.
+ * whatever they hold.  Rows of a request of wrong length get zeros and -inf;
+ * rows of one whose node offsets are wrong, and rows of packed nodes that belong
+ * to no request, are left as they were.
  * out [N][H_q][D] and out_lse [N][H_q] are contiguous.
  * ------------------------------------------------------------------------ */
 typedef struct sd_tree_attention_args {

@@ -11,11 +11,12 @@ check and marshal arguments.
 
 The cache is a pair of tensors [pages][H_kv][page_size][D] (any strides with
 contiguous rows, the same for both), with a page table [B][max_pages] and the
-slots in use [B], both int32.  Outputs and workspaces that are not passed in
-are allocated on the current stream; with `stream` given they are kept from
-reuse until that stream is done with them.
+slots in use [B], both int32.  With `stream` given, outputs and workspaces that
+are not passed in are allocated on that stream too, as in a
+`with torch.cuda.stream(stream)` block.
 """
 import ctypes
+import functools
 import struct
 
 from . import SD_BF16, SD_F32, SD_OK, SD_ST_INVALID_MASK, SdVerifyError, lib
@@ -158,12 +159,22 @@ def _status(status, B):
     return None if status is None else _ints(status, "status", B)
 
 
-def _on(stream):
-    """The stream's handle; for the current one without building a Stream
-    object, which takes longer than the rest of the argument checks."""
+def _streamed(f):
+    """f with a `stream` keyword: the call, and what it allocates, on it."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+def _stream():
+    """The current stream's handle, without building a Stream object, which
+    takes longer than the rest of the argument checks."""
     import torch
-    if stream is not None:
-        return stream.cuda_stream
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is None:
         return torch.cuda.current_stream().cuda_stream
@@ -205,28 +216,24 @@ def _cache(k, v, table, lens):
             _ints(lens, "context_lens", B), code, B, H, D, page, pages, cols)
 
 
-def _workspace(size, a, given, like, keep):
-    """The given workspace or a new one, if one is needed: (pointer, bytes)."""
+def _workspace(size, a, given, like):
+    """The given workspace or a new one, if one is needed: (tensor, pointer, bytes)."""
     import torch
     if given is not None:
         if not given.is_contiguous():
             raise ValueError("the workspace must be contiguous")
         _here(like, given)
-        return given.data_ptr(), given.numel() * given.element_size()
+        return given, given.data_ptr(), given.numel() * given.element_size()
     n = size(a)
     if n == 0:
-        return None, 0
+        return None, None, 0
     ws = torch.empty(n, dtype=torch.uint8, device=like.device)
-    keep.append(ws)
-    return ws.data_ptr(), n
+    return ws, ws.data_ptr(), n
 
 
-def _done(rc, name, stream, keep):
+def _done(rc, name):
     if rc != SD_OK:
         raise SdVerifyError(rc, name)
-    if stream is not None:
-        for t in keep:
-            t.record_stream(stream)
 
 
 # ---- attention of a drafted tree ----
@@ -265,9 +272,10 @@ def tree_attention_workspace_bytes(args):
     return _tree_attention_bytes(bytes(args))
 
 
+@_streamed
 def tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets,
                    max_nodes, parents=None, tree_mask=None, scale=None, want_lse=False, out=None,
-                   lse=None, status=None, workspace=None, stream=None):
+                   lse=None, status=None, workspace=None):
     """Attention of the packed nodes of B drafted trees over the paged cache
     and each other; returns (out [N][H_q][D], lse [N][H_q] or None).
 
@@ -279,21 +287,18 @@ def tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, 
     a = _attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets,
                         max_nodes, parents, tree_mask, scale)
     shape = q.shape
-    keep = []
     if out is None:
         out = q.new_empty(shape)
-        keep.append(out)
     else:
         _plain(out, q.dtype, "out", *shape)
     if lse is not None:
         _floats(lse, "lse", *shape[:2])
     elif want_lse:
         lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
-        keep.append(lse)
-    ws, n = _workspace(_tree_attention_bytes, a, workspace, q, keep)
-    rc = _tree_attention(a, ws, n, out.data_ptr(), None if lse is None else lse.data_ptr(),
-                         _status(status, page_table.shape[0]), _on(stream))
-    _done(rc, "sd_tree_attention", stream, keep)
+    ws, wp, n = _workspace(_tree_attention_bytes, a, workspace, q)
+    rc = _tree_attention(a, wp, n, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                         _status(status, page_table.shape[0]), _stream())
+    _done(rc, "sd_tree_attention")
     return out, lse
 
 
@@ -315,11 +320,12 @@ def _logits(t, name):
     if t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * ld:
         raise ValueError(f"{name} must have its rows back to back")
     rows = t.numel() // max(1, V)
-    return t.data_ptr(), (ld if rows > 1 else max(ld, -(-V // 8) * 8)), code
+    return t.data_ptr(), (ld if rows > 1 else max(ld, V)), code
 
 
+@_streamed
 def tree_verify_greedy(logits, tokens, parents, node_offsets, max_nodes, flags=0, status=None,
-                       out=None, workspace=None, stream=None):
+                       out=None, workspace=None):
     """Greedy verify of B drafted trees: logits [N][V], tokens and parents
     [N], node_offsets [B + 1].  Returns (accepted [B], path [B][max_nodes],
     tokens [B][max_nodes]).
@@ -336,30 +342,29 @@ def tree_verify_greedy(logits, tokens, parents, node_offsets, max_nodes, flags=0
     ptr, ld, code = _logits(logits, "logits")
     a = _TREE_VERIFY.pack(ptr, ld, _ints(tokens, "tokens", N), _ints(parents, "parents", N),
                           _ints(node_offsets, "node_offsets", B + 1), code, B, N, V, max_nodes, flags)
-    keep = []
-    ws, n = _workspace(_tree_verify_bytes, a, workspace, logits, keep)
+    ws, wp, n = _workspace(_tree_verify_bytes, a, workspace, logits)
 
     def output(t, name, *shape):
         if t is None:
             t = torch.empty(shape, dtype=torch.int32, device=logits.device)
-            keep.append(t)
         else:
             _ints(t, name, *shape)
         return t
 
     acc = output(acc, "accepted", B)
     path, tok = output(path, "path", B, max_nodes), output(tok, "tokens", B, max_nodes)
-    rc = _tree_verify(a, ws, n, acc.data_ptr(), path.data_ptr(), tok.data_ptr(),
-                      _status(status, B), _on(stream))
-    _done(rc, "sd_tree_verify_greedy", stream, keep)
+    rc = _tree_verify(a, wp, n, acc.data_ptr(), path.data_ptr(), tok.data_ptr(),
+                      _status(status, B), _stream())
+    _done(rc, "sd_tree_verify_greedy")
     return acc, path, tok
 
 
 # ---- append to and eviction from the cache ----
 
+@_streamed
 def cache_commit(k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets, max_nodes,
                  path, path_lens, out_context, q=None, lse=None, scale=None, mass_in=None,
-                 mass_out=None, decay=1.0, positions=None, seen=None, status=None, stream=None):
+                 mass_out=None, decay=1.0, positions=None, seen=None, status=None):
     """Append the nodes path[b][: path_lens[b]] to the cache; out_context [B]
     receives the new lengths.
 
@@ -395,14 +400,15 @@ def cache_commit(k_new, v_new, k_cache, v_cache, page_table, context_lens, node_
     a = _CACHE_COMMIT.pack(*c, kp, vp, kn, kh, vn, vh, _ints(node_offsets, "node_offsets", B + 1),
                            _ints(path, "path", B, cols), cols, _ints(path_lens, "path_lens", B), N,
                            max_nodes, *weights, L, *places)
-    rc = _cache_commit(a, _ints(out_context, "out_context", B), _status(status, B), _on(stream))
-    _done(rc, "sd_cache_commit", stream, ())
+    rc = _cache_commit(a, _ints(out_context, "out_context", B), _status(status, B), _stream())
+    _done(rc, "sd_cache_commit")
     return out_context
 
 
+@_streamed
 def cache_evict(k_cache, v_cache, page_table, context_lens, mass_in, mass_out, positions_in,
                 positions_out, seen, out_context, budget, recent=0, sinks=0, status=None,
-                workspace=None, stream=None):
+                workspace=None):
     """Cut every request's cache to its `budget` slots of the largest mass,
     keeping positions below `sinks` and the last `recent` ones; out_context
     [B] receives the new lengths.  mass_* [B][H_kv][L] float32 and positions_*
@@ -422,18 +428,18 @@ def cache_evict(k_cache, v_cache, page_table, context_lens, mass_in, mass_out, p
     a = _CACHE_EVICT.pack(*c, _floats(mass_in, "mass_in", B, H, L),
                           _floats(mass_out, "mass_out", B, H, L), *places, L,
                           0 if seen is None else _ints(seen, "seen", B), budget, recent, sinks)
-    keep = []
-    ws, n = _workspace(_cache_evict_bytes, a, workspace, k_cache, keep)
-    rc = _cache_evict(a, ws, n, _ints(out_context, "out_context", B), _status(status, B),
-                      _on(stream))
-    _done(rc, "sd_cache_evict", stream, keep)
+    ws, wp, n = _workspace(_cache_evict_bytes, a, workspace, k_cache)
+    rc = _cache_evict(a, wp, n, _ints(out_context, "out_context", B), _status(status, B),
+                      _stream())
+    _done(rc, "sd_cache_evict")
     return out_context
 
 
 # ---- a beam step ----
 
+@_streamed
 def beam_select(logits, scores, n_out, ended=None, eos_id=-1, out_ended=None, status=None,
-                out=None, workspace=None, stream=None):
+                out=None, workspace=None):
     """The n_out best continuations over the beams of each request: logits
     [B][W][V] (float32 or bfloat16), scores [B][W] float32, ended [B][W] uint8
     or None.  Returns (scores [B][n_out], parents [B][n_out], tokens
@@ -452,26 +458,25 @@ def beam_select(logits, scores, n_out, ended=None, eos_id=-1, out_ended=None, st
                           0 if ended is None else _plain(ended, torch.uint8, "ended", B, W), code,
                           B, W, V, n_out, eos_id)
     oe = None if out_ended is None else _plain(out_ended, torch.uint8, "out_ended", B, n_out)
-    keep = []
-    ws, n = _workspace(_beam_select_bytes, a, workspace, logits, keep)
+    ws, wp, n = _workspace(_beam_select_bytes, a, workspace, logits)
 
     def output(t, name, dtype, check):
         if t is None:
             t = torch.empty((B, n_out), dtype=dtype, device=logits.device)
-            keep.append(t)
         else:
             check(t, name, B, n_out)
         return t
 
     sc = output(sc, "scores", torch.float32, _floats)
     par, tok = output(par, "parents", torch.int32, _ints), output(tok, "tokens", torch.int32, _ints)
-    rc = _beam_select(a, ws, n, sc.data_ptr(), par.data_ptr(), tok.data_ptr(), oe,
-                      _status(status, B), _on(stream))
-    _done(rc, "sd_beam_select", stream, keep)
+    rc = _beam_select(a, wp, n, sc.data_ptr(), par.data_ptr(), tok.data_ptr(), oe,
+                      _status(status, B), _stream())
+    _done(rc, "sd_beam_select")
     return sc, par, tok
 
 
-def beam_reorder(state, parents, lengths=None, out=None, stream=None):
+@_streamed
+def beam_reorder(state, parents, lengths=None, out=None):
     """Move beam states to the beams that continue them: state
     [layers][B][W][segs][units][..] (the trailing part of a unit contiguous,
     a multiple of 16 bytes), parents [B][W_out] int32, lengths [B] int32 units
@@ -504,5 +509,5 @@ def beam_reorder(state, parents, lengths=None, out=None, stream=None):
                            _ints(parents, "parents", B, W_out),
                            0 if lengths is None else _ints(lengths, "lengths", B), unit, layers, B,
                            W, W_out, segs, units)
-    _done(_beam_reorder(a, _on(stream)), "sd_beam_reorder", stream, ())
+    _done(_beam_reorder(a, _stream()), "sd_beam_reorder")
     return dst
