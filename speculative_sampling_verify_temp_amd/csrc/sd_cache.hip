@@ -276,7 +276,8 @@ __global__ __launch_bounds__(NT_E) void k_evict_select(EvictArgs a) {
   // slots a thread loads at once, and steps of 64 slots a wave of the last
   // passes takes at once: more of them only where contexts are long
   constexpr int UE = LCAP > 4096 ? 16 : 4, UP = LCAP > 4096 ? 8 : 4;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, l = tid % WAVE, w = tid / WAVE;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, l = tid % WAVE;
+  const int w = __builtin_amdgcn_readfirstlane(tid / WAVE);
   uint32_t st = 0;
   const int n = request_ctx(a.c, b, st);
   const int bh = b * a.c.H + h;
@@ -348,52 +349,64 @@ __global__ __launch_bounds__(NT_E) void k_evict_select(EvictArgs a) {
     for (int i = 0; i < w; ++i) s += counts[which][i];
     return s;
   };
+  auto first = [](int k) { return k >= WAVE ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1; };   // lanes 0 .. k - 1
   int eq = 0;
   if (equal != want) {
-    for (int t0 = lo; t0 < hi; t0 += WAVE) eq += __popcll(__ballot(t0 + l < hi && key(min(t0 + l, n - 1)) == cut));
+    for (int t0 = lo; t0 < hi; t0 += WAVE) eq += __popcll(__ballot(key(min(t0 + l, n - 1)) == cut) & first(hi - t0));
     if (l == 0) counts[0][w] = eq;
     __syncthreads();
     eq = before(0);
   }
-  // first the waves' counts of freed and displaced slots, then the lists
-  const uint64_t below = (1ull << l) - 1;
+  // first the waves' counts of freed and displaced slots, then the lists; a
+  // step's 64 slots are masks in scalar registers
   int holes = 0, late = 0;
   for (int pass = 0; pass < 2; ++pass) {
     int e = eq, hp = holes, lp = late;
     const bool copy = pass && a.mass_out != a.mass_in, copy_pos = pass && a.pos_in && a.pos_out != a.pos_in;
     for (int t1 = lo; t1 < hi; t1 += WAVE * UP) {
       uint32_t k[UP];
-      float m[UP];
-      int p[UP];
+      float m[UP] = {};
+      int p[UP] = {};
+      if (held) {
 #pragma unroll
-      for (int u = 0; u < UP; ++u) {
-        const int t = min(t1 + u * WAVE + l, n - 1);
-        k[u] = key(t);
-        m[u] = copy && t1 < a.budget ? a.mass_in[row + t] : 0.0f;
-        p[u] = copy_pos && t1 < a.budget ? a.pos_in[row + t] : 0;
+        for (int u = 0; u < UP; ++u) k[u] = keys[min(t1 + u * WAVE + l, n - 1)];
+      } else {
+#pragma unroll
+        for (int u = 0; u < UP; ++u) k[u] = evict_key(a, row, min(t1 + u * WAVE + l, n - 1), recent_from);
+      }
+      if (copy && t1 < a.budget) {
+#pragma unroll
+        for (int u = 0; u < UP; ++u) m[u] = a.mass_in[row + min(t1 + u * WAVE + l, n - 1)];
+      }
+      if (copy_pos && t1 < a.budget) {
+#pragma unroll
+        for (int u = 0; u < UP; ++u) p[u] = a.pos_in[row + min(t1 + u * WAVE + l, n - 1)];
       }
 #pragma unroll
       for (int u = 0; u < UP; ++u) {
-        const int t = t1 + u * WAVE + l;
-        const bool in = t < hi;
-        bool keep = in && k[u] >= cut;
-        if (equal != want) {
-          const uint64_t same = __ballot(in && k[u] == cut);
-          if (k[u] == cut) keep = in && e + __popcll(same & below) < want;
+        const int t0 = t1 + u * WAVE, t = t0 + l;
+        const uint64_t in = first(hi - t0), low = first(a.budget - t0);
+        uint64_t keep = __ballot(k[u] >= cut) & in;
+        if (equal != want) {      // of the slots at the cut, the first `want` of the row
+          const uint64_t same = __ballot(k[u] == cut) & in;
+          const uint64_t early = __ballot(e + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
+                                          __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0)) < want);
+          keep &= ~same | early;
           e += __popcll(same);
         }
-        const bool move = keep && t >= a.budget, hole = in && !keep && t < a.budget;
-        const uint64_t mh = __ballot(hole), ml = __ballot(move);
+        const uint64_t hole = ~keep & in & low, move = keep & ~low;
         if (pass) {
-          if (hole) a.holes[(int64_t)bh * a.moves + hp + __popcll(mh & below)] = t;
-          if (move) a.late[(int64_t)bh * a.moves + lp + __popcll(ml & below)] = t;
-          if (keep && !move) {
+          const int hat = hp + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(hole >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hole, 0));
+          const int lat = lp + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(move >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)move, 0));
+          if (hole >> l & 1) a.holes[(int64_t)bh * a.moves + hat] = t;
+          if (move >> l & 1) a.late[(int64_t)bh * a.moves + lat] = t;
+          if ((keep & low) >> l & 1) {
             if (copy) a.mass_out[row + t] = m[u];
             if (copy_pos) a.pos_out[row + t] = p[u];
           }
         }
-        hp += __popcll(mh);
-        lp += __popcll(ml);
+        hp += __popcll(hole);
+        lp += __popcll(move);
       }
     }
     if (pass == 0) {
