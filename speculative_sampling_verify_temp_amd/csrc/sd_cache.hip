@@ -103,8 +103,9 @@ __device__ void append(const CommitArgs& a, const Branch& r, int b, int h) {
 // MFMA operands straight from the cache and meets the branch's query rows, 16
 // at a time from LDS: S = Q . K^T, so a lane holds 4 rows of one key and the
 // sum over the rows is in its own registers but for two lane swaps at the end.
-// The keys are read once (bound by HBM up to about 150 rows); row blocks past
-// the first are staged again for every tile.
+// The keys are read once; row blocks past the first are staged again for every
+// tile.  Bound by HBM up to about 150 rows: 361 MB of keys and weights in 87 us
+// (4.1 TB/s) for 32 requests of 5k to 16k slots, 4 KV heads and up to 42 rows.
 template <int DT, int D>
 __global__ __launch_bounds__(NT_C, 2) void k_commit(CommitArgs a, int chunk) {
   constexpr int KS = D / 32, CPR = D / 8;
@@ -263,9 +264,11 @@ __device__ __forceinline__ void find_digit(const int* hist, int want, int* scrat
 
 // One workgroup per (KV head, request).  The rank keys of up to LCAP slots are
 // kept in LDS, so mass and positions are read once; longer contexts compute
-// them again in each of the 5 to 6 passes.  Bound by what one CU reads (about
-// 30 GB/s) and by LDS atomics: four copies of the histogram keep the lanes of a
-// quad apart.
+// them again in each of the 5 or 6 passes.  Bound by what one CU reads (about
+// 30 GB/s) and by the latencies of the passes over LDS.  Digits are 11 bits wide,
+// as masses share few exponents, and two copies of the histogram keep
+// neighbouring lanes apart.  39 us for 64 heads of 20k to 32k slots; 10 us for
+// 2053 slots.
 template <int LCAP>
 __global__ __launch_bounds__(NT_E) void k_evict_select(EvictArgs a) {
   __shared__ uint32_t keys[LCAP];
@@ -421,7 +424,8 @@ __global__ __launch_bounds__(NT_E) void k_evict_select(EvictArgs a) {
 
 // Rows of up to MV moves a round: their addresses once into LDS, then all
 // loads of a round before its stores.  Bound by HBM: each moved row is read and
-// written once.
+// written once, 370 MB in 72 us (5.1 TB/s) for 64 heads that keep 8192 of 20k to
+// 32k slots.
 template <int D>
 __global__ __launch_bounds__(256) void k_evict_move(EvictArgs a) {
   constexpr int LPR = D / 8, RPI = 256 / LPR, IT = MV / RPI;

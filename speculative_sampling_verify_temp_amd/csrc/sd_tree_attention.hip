@@ -20,7 +20,15 @@
 //                out of LDS transposed (ds_read_b64_tr_b16).  Keys are staged
 //                through registers into swizzled LDS rows, the next tile's
 //                loads in flight behind the products.
-// k_attn_join    one thread per 4 output columns of a split row.
+//                Up to about 130 rows a KV head it is bound by HBM (3.2 TB/s
+//                over 32 chains of 9 nodes, 3.8 TB/s over longer contexts: a
+//                run's start and end take as long as 3 of its tiles), past
+//                that by the issue of softmax and products, which overlap
+//                little: 16 trees of 64 nodes over 16k to 32k slots take 460
+//                us, 670 TFLOP/s, with the matrix cores busy 36 %, the vector
+//                ALU 44 % and LDS 34 % of the time.
+// k_attn_join    one thread per 4 output columns of a split row; latency, 6 to
+//                12 us.
 #include <type_traits>
 
 #include "sdt_device.h"
@@ -674,7 +682,10 @@ AttnArgs device_args(const sd_tree_attention_args_t* p) {
 }
 
 // The shape for `rows` packed rows a KV head: fewer rows leave more waves to
-// the keys.  f(Shape{}) is called with the one taken.
+// the keys.  16 rows a wave need no register spills and win up to 128 rows (63
+// rows 49 us against 64 for 32 a wave, 28 rows 52 against 90, 112 rows 61 against
+// 78); past that 32 a wave halve the LDS reads (448 rows 460 us against 600).
+// f(Shape{}) is called with the one taken.
 template <int D, typename F>
 auto with_shape(int rows, F&& f) {
   if (rows <= 16) return f(Shape<D, 1, 1, 4, 1>{});
@@ -691,7 +702,8 @@ constexpr int run_count() {
 }
 
 // Where a table holds no more than this many key tiles, splitting them and
-// joining the parts in a second launch costs more than it saves.
+// joining the parts in a second launch costs more than it saves (517 slots of
+// one request: 9 us in one launch, 6 + 5 us and a launch's host time in two).
 constexpr int WHOLE_TILES = 8;
 
 // How a call is cut up.

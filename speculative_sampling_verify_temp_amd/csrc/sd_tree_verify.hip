@@ -2,7 +2,8 @@
 //
 // Bound by the bytes of logits read.  Which rows the walk visits is known one
 // row at a time, so there are two ways (rule at walk_rows):
-//   few rows in all    k_tree_argmax finds the maximum of every row, a
+//   few rows in all    (one tree of 16 rows of 151936 fp32 logits: 4.6 + 4.3
+//                      us, latency) k_tree_argmax finds the maximum of every row, a
 //                      workgroup per (row, slice of the vocabulary), and
 //                      k_tree_walk, one wave per request, follows the tree;
 //   many rows          k_tree_descend reads only the rows that the walks visit,

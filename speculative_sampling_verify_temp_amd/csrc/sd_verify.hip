@@ -3156,7 +3156,7 @@ const char* sd_strerror(int code) {
     case SD_EINVAL: return "invalid argument";
     case SD_EWORKSPACE: return "workspace missing or too small";
     case SD_EHIP: return "HIP runtime error";
-    case SD_EUNSUPPORTED: return "unsupported size (K_max or V beyond this build's limits)";
+    case SD_EUNSUPPORTED: return "unsupported size (beyond this build's limits)";
     case SD_ESCRATCH: return "call needs more workspace than the built-in scratch array holds";
     default: return "unknown error code";
   }

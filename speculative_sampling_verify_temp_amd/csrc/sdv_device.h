@@ -1,6 +1,6 @@
 // Device helpers of the verify step for gfx950 (wave64): logit loads, the
 // penalized key, the orderable key, fixed-point masses, Philox4x32-10 and
-// block reductions.  Included by sd_verify.hip only.
+// block reductions.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
