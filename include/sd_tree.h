@@ -80,7 +80,7 @@ typedef struct sd_kv_cache {
   int32_t        D;              /* head size: 64 or 128                        */
   int32_t        page_size;      /* a power of two, <= SD_MAX_PAGE_SIZE         */
   int32_t        num_pages;      /* pages of the pool                           */
-  int32_t        max_pages;      /* table entries of a request; at most 2^31 - 1
+  int32_t        max_pages;      /* table entries of a request; at most 2^30
                                     slots                                       */
 } sd_kv_cache_t;
 

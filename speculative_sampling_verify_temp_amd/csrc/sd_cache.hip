@@ -431,7 +431,7 @@ __global__ __launch_bounds__(256) void k_evict_move(EvictArgs a) {
   constexpr int LPR = D / 8, RPI = 256 / LPR, IT = MV / RPI;
   __shared__ int64_t from[MV], to[MV];
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int bh = b * a.c.H + h, n = a.count[bh];
+  const int bh = b * a.c.H + h, n = min(a.count[bh], a.moves);
   const int64_t row = (int64_t)bh * a.ld, list = (int64_t)bh * a.moves;
   const int32_t* tab = table_row(a.c, b);
   const int d = (tid % LPR) * 16;
@@ -439,7 +439,8 @@ __global__ __launch_bounds__(256) void k_evict_move(EvictArgs a) {
     if (tid < MV) {
       int64_t s = -1, t = -1;
       if (i0 + tid < n) {
-        const int src = a.late[list + i0 + tid], dst = a.holes[list + i0 + tid];
+        const int src = min(max(a.late[list + i0 + tid], 0), a.c.cap - 1);
+        const int dst = min(max(a.holes[list + i0 + tid], 0), a.c.cap - 1);
         s = slot_offset(a.c, tab, src, h);
         t = slot_offset(a.c, tab, dst, h);
         a.mass_out[row + dst] = a.mass_in[row + src];

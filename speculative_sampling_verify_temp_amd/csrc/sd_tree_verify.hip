@@ -218,7 +218,9 @@ __global__ __launch_bounds__(WAVE) void k_tree_walk(VerifyArgs a) {
 // maximum, and the last one of a row to do so takes the step and makes the
 // next row known.  A ticket is only waited for by later ones, and whoever holds
 // an earlier one is running, so every wait ends however few workgroups of a
-// team the chip holds at a time.
+// team the chip holds at a time.  (Calls that overlap on one workspace, which
+// the interface forbids, could take each other's tickets: waits are bounded, and
+// such a request keeps the -1 that its results begin with.)
 
 //
 // What the team shares is only touched by relaxed agent-scope atomics, which
@@ -231,6 +233,7 @@ struct Team {
   uint64_t visited[SD_MAX_NODES];           // by depth: node << 32 | its row's best token
 };
 constexpr uint32_t DONE = 0xFFFFFFFFu;
+constexpr int MAX_POLLS = 1 << 21;          // about two seconds; a wait takes microseconds
 
 template <typename T>
 __device__ __forceinline__ T shared_load(const T* p) {
@@ -269,7 +272,7 @@ __global__ __launch_bounds__(WAVE) void k_tree_begin(VerifyArgs a) {
   const int b = blockIdx.x, l = threadIdx.x;
   Walk w(a, b);
   const bool go = w.valid() && w.enter(a.flags);
-  if (!go) finish(a, b, w.st, 0, w.my_path, -1);
+  finish(a, b, w.st, go ? -1 : 0, go ? -1 : w.my_path, -1);
   if (l == 0) {
     Team& t = a.team[b];
     t.ticket = t.left = 0;
@@ -290,17 +293,18 @@ __global__ __launch_bounds__(NT_D) void k_tree_descend(VerifyArgs a) {
   for (;;) {
     if (tid == 0) {
       const uint32_t depth = next / (uint32_t)a.slices;
-      uint32_t r;
-      for (;;) {
+      uint32_t r = DONE;
+      for (int i = 0; i < MAX_POLLS; ++i) {
         r = shared_load(&team.row);
         if (r == DONE || (r >> 8) >= depth) break;
+        r = DONE;
         __builtin_amdgcn_s_sleep(1);
       }
       ticket_sh = next, row_sh = r;
     }
     __syncthreads();
     if (row_sh == DONE) return;
-    const int sl = (int)(ticket_sh % (uint32_t)a.slices), depth = (int)(row_sh >> 8), cur = (int)(row_sh & 255u);
+    const int sl = (int)(ticket_sh % (uint32_t)a.slices), depth = (int)(row_sh >> 8) & 63, cur = min((int)(row_sh & 63u), w.nd.T - 1);
     if (tid == 0) next = shared_add(&team.ticket);      // on its way while the row is read
     const int lo = sl * a.slice_vecs, hi = min(a.V / E, lo + a.slice_vecs);
     const char* row = a.logits + (int64_t)(w.nd.first + cur) * a.row_bytes;

@@ -195,7 +195,7 @@ inline int check_cache(const sd_kv_cache_t& c) {
     return SD_EINVAL;
   if (c.D != 64 && c.D != 128) return SD_EUNSUPPORTED;
   if ((c.page_size & (c.page_size - 1)) || c.page_size > SD_MAX_PAGE_SIZE) return SD_EUNSUPPORTED;
-  if ((int64_t)c.max_pages * c.page_size > 0x7FFFFFFF - 4096) return SD_EUNSUPPORTED;
+  if ((int64_t)c.max_pages * c.page_size > (1 << 30)) return SD_EUNSUPPORTED;
   if (c.B > 65535 || c.H_kv > 65535) return SD_EUNSUPPORTED;
   return SD_OK;
 }

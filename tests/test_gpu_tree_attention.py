@@ -31,6 +31,8 @@ CASES = [
     ([130, 700, 64], [16, 31, 64], 7, 1, 128, 256),
     ([2500], [2], 4, 4, 128, 16),
     ([90] * 11, [1, 2, 3, 4, 5, 6, 7, 8, 16, 17, 9], 6, 2, 64, 16),
+    ([150, 600], [64, 5], 32, 1, 64, 16),
+    ([700], [64], 32, 1, 128, 16),
 ]
 
 
@@ -182,6 +184,39 @@ def test_same_bits_on_every_call_and_stream_and_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, lwant)
+
+
+def test_interleaved_caches_and_wide_tables():
+    """Keys and values of a page side by side in one tensor, padded rows, a
+    table that is a part of a wider one, and a query shared by all heads."""
+    import torch
+    c = Cached(17, [300, 20, 77], [5, 9, 2], 8, 2, 64, 16, "bf16")
+    pool = c.k.shape[0]
+    kv = torch.full((pool, 2, 2, 16, 72), float("nan"), dtype=torch.bfloat16, device="cuda")
+    kv[:, 0, :, :, :64], kv[:, 1, :, :, :64] = c.d["k_cache"], c.d["v_cache"]
+    c.d["k_cache"], c.d["v_cache"] = kv[:, 0, :, :, :64], kv[:, 1, :, :, :64]
+    wide = torch.full((3, c.table.shape[1] + 5), -7, dtype=torch.int32, device="cuda")
+    wide[:, 2:2 + c.table.shape[1]] = c.d["page_table"]
+    c.d["page_table"] = wide[:, 2:2 + c.table.shape[1]]
+    c.check_attention(*_run(c), c.reference())
+    c.d["q"] = c.d["q"][:, :1].expand(-1, 8, -1)
+    c.q = np.repeat(c.q[:, :1], 8, 1)
+    c.check_attention(*_run(c), c.reference())
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with workspaces of their own."""
+    import torch
+    a, b = Cached(18, [3000, 500], [9, 64], 28, 4, 128, 16, "bf16"), Cached(19, [2500], [64], 8, 2, 64, 16, "f16")
+    wa, wb = _run(a), _run(b)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got.append((_run(a, stream=s), _run(b, stream=t)))
+    torch.cuda.synchronize()
+    for ga, gb in got:
+        assert all(torch.equal(x, y) for x, y in zip((*ga, *gb), (*wa, *wb)))
 
 
 def test_a_pool_past_four_gigabytes():

@@ -86,6 +86,7 @@ CASES = [
     ([63, 64, 65, 15, 127], [9, 9, 9, 9, 9], [1, 2, 9, 3, 4], 28, 4, 128, 16),
     ([300, 20], [64, 64], [64, 33], 7, 1, 128, 32),
     ([1200, 0, 31], [16, 5, 1], [5, 5, 1], 32, 1, 64, 8),
+    ([400, 90], [64, 64], [64, 20], 32, 1, 128, 16),
 ]
 
 
@@ -101,6 +102,69 @@ def test_commit_matches_the_oracle(case, dtype):
     print(f"commit {CASES[case]} {dtype}", flush=True)
     mass, kw = _commit(c, paths, decay, L, case, in_place=in_place)
     _check_commit(c, paths, decay, mass, kw, in_place)
+
+
+def test_a_branch_may_name_a_node_twice():
+    c = Cached(223, [40, 3], [4, 4], 4, 2, 64, 16, "bf16", room=8)
+    L = c.table.shape[1] * 16
+    mass, kw = _commit(c, [[0, 2, 2], [3, 1]], 1.0, L, 1, in_place=True)
+    _check_commit(c, [[0, 2, 2], [3, 1]], 1.0, mass, kw, True)
+
+
+def test_commit_and_evict_in_a_graph():
+    """A commit and an eviction captured once and replayed on states that the
+    program changes in between."""
+    import torch
+    sdv = _sdv()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    B, H, Hq, D, page, n, T, budget = 3, 2, 8, 64, 16, 300, 4, 200
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    cols = 20
+    k, v = rnd(B * cols, H, page, D), rnd(B * cols, H, page, D)
+    table = torch.randperm(B * cols, generator=g, device="cuda").to(torch.int32).reshape(B, cols)
+    q, kn, vn = rnd(B * T, Hq, D), rnd(B * T, H, D), rnd(B * T, H, D)
+    lse = torch.full((B * T, Hq), 6.0, device="cuda")
+    off = torch.arange(B + 1, device="cuda", dtype=torch.int32) * T
+    ctx = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    path = torch.tensor([[0, 1, 3, -1]] * B, dtype=torch.int32, device="cuda")
+    plen = torch.tensor([3, 1, 0], dtype=torch.int32, device="cuda")
+    mass = torch.rand((B, H, cols * page), generator=g, device="cuda")
+    pos = torch.arange(cols * page, dtype=torch.int32, device="cuda").repeat(B, H, 1)
+    seen = ctx.clone()
+    mid, out = torch.zeros_like(ctx), torch.zeros_like(ctx)
+    m2, p2 = mass.clone(), pos.clone()
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+
+    def step():
+        sdv.cache_commit(kn, vn, k, v, table, ctx, off, T, path, plen, mid, q=q, lse=lse, mass_in=mass, mass_out=m2,
+                         positions=p2, seen=seen)
+        sdv.cache_evict(k, v, table, mid, m2, m2, p2, p2, seen, out, budget, 20, 4, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        for x in (k, v, q, kn, vn):
+            x.copy_(rnd(*x.shape))
+        mass.copy_(torch.rand(mass.shape, generator=g, device="cuda"))
+        plen.copy_(torch.tensor([i % 4, 1, 2], dtype=torch.int32))
+        state = [x.clone() for x in (k, v)]
+        m2.copy_(mass)
+        p2.copy_(pos)
+        step()
+        want = [x.clone() for x in (k, v, m2, p2, mid, out)]
+        for x, y in zip((k, v), state):
+            x.copy_(y)
+        m2.copy_(mass)
+        p2.copy_(pos)
+        ws.fill_(0xEE)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((k, v, m2, p2, mid, out), want))
 
 
 def test_decay_zero_reads_no_old_weight():

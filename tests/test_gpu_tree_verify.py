@@ -111,7 +111,7 @@ def test_defects_are_reported_request_by_request(copies):
     import torch
     sdv = _sdv()
     rng = np.random.default_rng(3)
-    V, T, R = 600, 4, 8
+    V, T, R = 600, 4, 9
     z = rng.standard_normal((R * T, V)).astype(np.float32)
     parents = np.tile([-1, 0, 1, 2], R).astype(np.int32)
     tokens = rng.integers(0, V, R * T).astype(np.int32)
@@ -124,16 +124,18 @@ def test_defects_are_reported_request_by_request(copies):
     parents[6 * T] = 1                               # a root with a parent
     z[7 * T] = -np.inf                               # all masked: the first token
     tokens[7 * T + 1] = 0
+    z[8 * T + 2, V - 1] = np.nan                     # a NaN two steps down the walk
+    tokens[8 * T + 1], tokens[8 * T + 2] = int(z[8 * T].argmax()), int(z[8 * T + 1].argmax())
     z, parents, tokens = np.tile(z, (copies, 1)), np.tile(parents, copies), np.tile(tokens, copies)
     off = (np.arange(R * copies + 1) * T).astype(np.int32)
     st = torch.full((R * copies,), -1, dtype=torch.int32, device="cuda")
     acc, path, tok = sdv.tree_verify_greedy(dev(z), dev(tokens), dev(parents), dev(off), T, status=st)
     want = [0, sdv.SD_ST_NONFINITE, 0, sdv.SD_ST_BAD_DRAFT_ID, sdv.SD_ST_BAD_DRAFT_ID, sdv.SD_ST_BAD_TREE,
-            sdv.SD_ST_BAD_TREE, 0]
+            sdv.SD_ST_BAD_TREE, 0, sdv.SD_ST_NONFINITE]
     assert st.tolist() == want * copies
     acc = acc.cpu().numpy().reshape(copies, R)
-    assert (acc[:, [1, 3, 4]] == -1).all() and (acc[:, [0, 2, 5, 6]] >= 0).all() and (acc[:, 7] >= 1).all()
-    bad = np.isin(np.arange(R * copies) % R, (1, 3, 4))
+    assert (acc[:, [1, 3, 4, 8]] == -1).all() and (acc[:, [0, 2, 5, 6]] >= 0).all() and (acc[:, 7] >= 1).all()
+    bad = np.isin(np.arange(R * copies) % R, (1, 3, 4, 8))
     assert (path.cpu().numpy()[bad] == -1).all() and (tok.cpu().numpy()[bad] == -1).all()
     # node offsets that decrease, pass N, or give a request too many nodes or none
     off2 = np.array([0, 4, 3, 4, 4, 10, 14, R * T * copies + 1], dtype=np.int32)
