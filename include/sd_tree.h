@@ -75,8 +75,8 @@ typedef struct sd_kv_cache {
   int64_t        ld_table;       /* entries between rows, >= max_pages          */
   const int32_t *context_lens;   /* [B] in [0, max_pages * page_size]           */
   int32_t        dtype;          /* SD_BF16 or SD_F16                           */
-  int32_t        B;              /* requests, >= 1                              */
-  int32_t        H_kv;           /* KV heads, >= 1                              */
+  int32_t        B;              /* requests, 1 .. 65535                        */
+  int32_t        H_kv;           /* KV heads, 1 .. 65535                        */
   int32_t        D;              /* head size: 64 or 128                        */
   int32_t        page_size;      /* a power of two, <= SD_MAX_PAGE_SIZE         */
   int32_t        num_pages;      /* pages of the pool                           */
@@ -147,8 +147,8 @@ typedef struct sd_tree_verify_args {
   const int32_t *parents;        /* [N]                                         */
   const int32_t *node_offsets;   /* [B + 1]                                     */
   int32_t        dtype;
-  int32_t        B;
-  int32_t        N;
+  int32_t        B;              /* 1 .. 65535                                  */
+  int32_t        N;              /* 1 .. 2^24                                   */
   int32_t        V;              /* < 2^28                                      */
   int32_t        max_nodes;
   uint32_t       flags;          /* SD_NO_BONUS                                 */
@@ -259,7 +259,7 @@ typedef struct sd_beam_select_args {
   const float   *scores;         /* [B][W]                                      */
   const uint8_t *ended;          /* [B][W] or NULL                              */
   int32_t        dtype;
-  int32_t        B;
+  int32_t        B;              /* 1 .. 2^20                                   */
   int32_t        W;              /* 1 .. SD_MAX_BEAMS                           */
   int32_t        V;              /* < 2^24                                      */
   int32_t        n_out;          /* 1 .. SD_MAX_BEAMS                           */
@@ -281,7 +281,7 @@ int sd_beam_select(const sd_beam_select_args_t *args, void *workspace,
  * permuted in place; otherwise the two must not overlap.  A parent outside
  * [0, W_in) leaves its row as it was.  Units past the length are left as they
  * were.  unit_bytes and all strides are multiples of 16, pointers 16-byte
- * aligned. */
+ * aligned; W_in, W_out <= SD_MAX_BEAMS, B and layers * segs <= 65535. */
 typedef struct sd_beam_reorder_args {
   const void    *in;
   void          *out;

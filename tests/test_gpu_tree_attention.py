@@ -49,13 +49,14 @@ def test_chains_and_trees_match_the_oracle(case, dtype):
     c.check_attention(*_run(c, parents=dev(parents)), c.reference(parents=parents))
 
 
+@pytest.mark.parametrize("longest", [90, 1100])
 @pytest.mark.parametrize("D,Hq", [(64, 4), (128, 14)])
-def test_many_requests(D, Hq):
+def test_many_requests(D, Hq, longest):
     """More requests than a wave has lanes, some without nodes or slots, in a
-    table with room for long contexts."""
+    short table and in one with room for long contexts."""
     rng = np.random.default_rng(D)
     lens = rng.integers(0, 90, 150).tolist()
-    lens[70], lens[149] = 700, 1100
+    lens[70], lens[149] = longest * 2 // 3, longest
     nodes = rng.integers(0, 4, 150).tolist()
     c = Cached(41, lens, nodes, Hq, 2, D, 16, "bf16")
     c.check_attention(*_run(c), c.reference())
