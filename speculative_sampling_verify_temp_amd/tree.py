@@ -16,8 +16,9 @@ are not passed in are allocated on that stream too, as in a
 `with torch.cuda.stream(stream)` block.
 """
 import ctypes
-import functools
 import struct
+
+import torch
 
 from . import SD_BF16, SD_F32, SD_OK, SD_ST_INVALID_MASK, SdVerifyError, lib
 
@@ -129,7 +130,6 @@ _beam_select_bytes = _size_entry("sd_beam_select_workspace_bytes")
 
 def _here(first, *rest):
     """All tensors on the current GPU, which is where the call's work goes."""
-    import torch
     dev = first.get_device()
     if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError("tensors must be on the current GPU")
@@ -138,43 +138,34 @@ def _here(first, *rest):
             raise ValueError("all tensors of a call must be on the same GPU")
 
 
-def _plain(t, dtype, name, *shape):
+def _plain(t, dtype, name, shape):
     """Pointer of a contiguous tensor of this type and shape."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
     return t.data_ptr()
 
 
-def _ints(t, name, *shape):
-    import torch
-    return _plain(t, torch.int32, name, *shape)
-
-
-def _floats(t, name, *shape):
-    import torch
-    return _plain(t, torch.float32, name, *shape)
+def _output(t, dtype, name, shape, like):
+    """The given output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _plain(t, dtype, name, shape)
+    return t
 
 
 def _status(status, B):
-    return None if status is None else _ints(status, "status", B)
+    return None if status is None else _plain(status, torch.int32, "status", (B,))
 
 
-def _streamed(f):
-    """f with a `stream` keyword: the call, and what it allocates, on it."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        import torch
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
+def _on(stream, f, args):
+    """f with these keyword arguments, and what it allocates, on the stream."""
+    with torch.cuda.stream(stream):
+        return f(**{**args, "stream": None})
 
 
 def _stream():
     """The current stream's handle, without building a Stream object, which
     takes longer than the rest of the argument checks."""
-    import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is None:
         return torch.cuda.current_stream().cuda_stream
@@ -193,7 +184,6 @@ def _rows(t, name, like, N, H, D):
 
 def _cache(k, v, table, lens):
     """The fields of sd_kv_cache_t."""
-    import torch
     if k.dtype is torch.bfloat16:
         code = SD_BF16
     elif k.dtype is torch.float16:
@@ -213,12 +203,11 @@ def _cache(k, v, table, lens):
     B, cols = table.shape
     return (k.data_ptr(), v.data_ptr(), ps, hs, ss, table.data_ptr(),
             table.stride(0) if B > 1 else max(cols, table.stride(0)),
-            _ints(lens, "context_lens", B), code, B, H, D, page, pages, cols)
+            _plain(lens, torch.int32, "context_lens", (B,)), code, B, H, D, page, pages, cols)
 
 
 def _workspace(size, a, given, like):
     """The given workspace or a new one, if one is needed: (tensor, pointer, bytes)."""
-    import torch
     if given is not None:
         if not given.is_contiguous():
             raise ValueError("the workspace must be contiguous")
@@ -240,7 +229,6 @@ def _done(rc, name):
 
 def _attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets,
                     max_nodes, parents, tree_mask, scale):
-    import torch
     c = _cache(k_cache, v_cache, page_table, context_lens)
     B, H = c[9:11]
     N, Hq, D = q.shape
@@ -250,9 +238,10 @@ def _attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens,
     kp, kn, kh = _rows(k_new, "k_new", k_cache, N, H, D)
     vp, vn, vh = _rows(v_new, "v_new", k_cache, N, H, D)
     return _TREE_ATTENTION.pack(
-        *c, qp, kp, vp, qn, qh, kn, kh, vn, vh, _ints(node_offsets, "node_offsets", B + 1),
-        0 if parents is None else _ints(parents, "parents", N),
-        0 if tree_mask is None else _plain(tree_mask, torch.int64, "tree_mask", N), N, max_nodes,
+        *c, qp, kp, vp, qn, qh, kn, kh, vn, vh,
+        _plain(node_offsets, torch.int32, "node_offsets", (B + 1,)),
+        0 if parents is None else _plain(parents, torch.int32, "parents", (N,)),
+        0 if tree_mask is None else _plain(tree_mask, torch.int64, "tree_mask", (N,)), N, max_nodes,
         Hq, D ** -0.5 if scale is None else scale)
 
 
@@ -272,29 +261,24 @@ def tree_attention_workspace_bytes(args):
     return _tree_attention_bytes(bytes(args))
 
 
-@_streamed
 def tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets,
                    max_nodes, parents=None, tree_mask=None, scale=None, want_lse=False, out=None,
-                   lse=None, status=None, workspace=None):
+                   lse=None, status=None, workspace=None, stream=None):
     """Attention of the packed nodes of B drafted trees over the paged cache
     and each other; returns (out [N][H_q][D], lse [N][H_q] or None).
 
     out, lse: optional preallocated contiguous outputs; status: optional [B]
     int32 tensor for the per-request bits."""
-    import torch
+    if stream is not None:
+        return _on(stream, tree_attention, locals())
     _here(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets, parents,
           tree_mask, out, lse, status)
     a = _attention_args(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets,
                         max_nodes, parents, tree_mask, scale)
     shape = q.shape
-    if out is None:
-        out = q.new_empty(shape)
-    else:
-        _plain(out, q.dtype, "out", *shape)
-    if lse is not None:
-        _floats(lse, "lse", *shape[:2])
-    elif want_lse:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    out = _output(out, q.dtype, "out", shape, q)
+    if want_lse or lse is not None:
+        lse = _output(lse, torch.float32, "lse", shape[:2], q)
     ws, wp, n = _workspace(_tree_attention_bytes, a, workspace, q)
     rc = _tree_attention(a, wp, n, out.data_ptr(), None if lse is None else lse.data_ptr(),
                          _status(status, page_table.shape[0]), _stream())
@@ -306,7 +290,6 @@ def tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, context_lens, 
 
 def _logits(t, name):
     """Rows with unit element stride: (pointer, row stride, type code)."""
-    import torch
     if t.dtype == torch.float32:
         code = SD_F32
     elif t.dtype == torch.bfloat16:
@@ -323,15 +306,15 @@ def _logits(t, name):
     return t.data_ptr(), (ld if rows > 1 else max(ld, V)), code
 
 
-@_streamed
 def tree_verify_greedy(logits, tokens, parents, node_offsets, max_nodes, flags=0, status=None,
-                       out=None, workspace=None):
+                       out=None, workspace=None, stream=None):
     """Greedy verify of B drafted trees: logits [N][V], tokens and parents
     [N], node_offsets [B + 1].  Returns (accepted [B], path [B][max_nodes],
     tokens [B][max_nodes]).
 
     out: optional dict of preallocated outputs (accepted, path, tokens)."""
-    import torch
+    if stream is not None:
+        return _on(stream, tree_verify_greedy, locals())
     if logits.dim() != 2:
         raise ValueError("logits must be [N][V]")
     N, V = logits.shape
@@ -340,19 +323,15 @@ def tree_verify_greedy(logits, tokens, parents, node_offsets, max_nodes, flags=0
     acc, path, tok = o.get("accepted"), o.get("path"), o.get("tokens")
     _here(logits, tokens, parents, node_offsets, status, acc, path, tok)
     ptr, ld, code = _logits(logits, "logits")
-    a = _TREE_VERIFY.pack(ptr, ld, _ints(tokens, "tokens", N), _ints(parents, "parents", N),
-                          _ints(node_offsets, "node_offsets", B + 1), code, B, N, V, max_nodes, flags)
+    a = _TREE_VERIFY.pack(ptr, ld, _plain(tokens, torch.int32, "tokens", (N,)),
+                          _plain(parents, torch.int32, "parents", (N,)),
+                          _plain(node_offsets, torch.int32, "node_offsets", (B + 1,)), code, B, N, V,
+                          max_nodes, flags)
     ws, wp, n = _workspace(_tree_verify_bytes, a, workspace, logits)
 
-    def output(t, name, *shape):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.int32, device=logits.device)
-        else:
-            _ints(t, name, *shape)
-        return t
-
-    acc = output(acc, "accepted", B)
-    path, tok = output(path, "path", B, max_nodes), output(tok, "tokens", B, max_nodes)
+    acc = _output(acc, torch.int32, "accepted", (B,), logits)
+    path = _output(path, torch.int32, "path", (B, max_nodes), logits)
+    tok = _output(tok, torch.int32, "tokens", (B, max_nodes), logits)
     rc = _tree_verify(a, wp, n, acc.data_ptr(), path.data_ptr(), tok.data_ptr(),
                       _status(status, B), _stream())
     _done(rc, "sd_tree_verify_greedy")
@@ -361,10 +340,9 @@ def tree_verify_greedy(logits, tokens, parents, node_offsets, max_nodes, flags=0
 
 # ---- append to and eviction from the cache ----
 
-@_streamed
 def cache_commit(k_new, v_new, k_cache, v_cache, page_table, context_lens, node_offsets, max_nodes,
                  path, path_lens, out_context, q=None, lse=None, scale=None, mass_in=None,
-                 mass_out=None, decay=1.0, positions=None, seen=None, status=None):
+                 mass_out=None, decay=1.0, positions=None, seen=None, status=None, stream=None):
     """Append the nodes path[b][: path_lens[b]] to the cache; out_context [B]
     receives the new lengths.
 
@@ -372,6 +350,8 @@ def cache_commit(k_new, v_new, k_cache, v_cache, page_table, context_lens, node_
     accumulated from q, lse (of tree_attention) and mass_in (mass_out's own
     values when None); positions [B][H_kv][L] and seen [B] record where the
     appended tokens stand."""
+    if stream is not None:
+        return _on(stream, cache_commit, locals())
     if mass_out is not None and (q is None or lse is None):
         raise ValueError("weights need q and lse")
     if mass_out is not None and mass_in is None:
@@ -387,33 +367,39 @@ def cache_commit(k_new, v_new, k_cache, v_cache, page_table, context_lens, node_
     weights = (0, 0, 0, 0, 0, 0.0, 0.0, 0, 0)
     if mass_out is not None:
         L, Hq = mass_out.shape[-1], q.shape[1]
-        weights = (*_rows(q, "q", k_cache, N, Hq, D), _floats(lse, "lse", N, Hq), Hq,
+        weights = (*_rows(q, "q", k_cache, N, Hq, D), _plain(lse, torch.float32, "lse", (N, Hq)), Hq,
                    D ** -0.5 if scale is None else scale, decay,
-                   _floats(mass_in, "mass_in", B, H, L), _floats(mass_out, "mass_out", B, H, L))
+                   _plain(mass_in, torch.float32, "mass_in", (B, H, L)),
+                   _plain(mass_out, torch.float32, "mass_out", (B, H, L)))
     places = (0, 0)
     if positions is not None:
         if seen is None:
             raise ValueError("positions need seen")
         L = L or positions.shape[-1]
-        places = _ints(positions, "positions", B, H, L), _ints(seen, "seen", B)
+        places = (_plain(positions, torch.int32, "positions", (B, H, L)),
+                  _plain(seen, torch.int32, "seen", (B,)))
     cols = path.shape[-1]
-    a = _CACHE_COMMIT.pack(*c, kp, vp, kn, kh, vn, vh, _ints(node_offsets, "node_offsets", B + 1),
-                           _ints(path, "path", B, cols), cols, _ints(path_lens, "path_lens", B), N,
-                           max_nodes, *weights, L, *places)
-    rc = _cache_commit(a, _ints(out_context, "out_context", B), _status(status, B), _stream())
+    a = _CACHE_COMMIT.pack(*c, kp, vp, kn, kh, vn, vh,
+                           _plain(node_offsets, torch.int32, "node_offsets", (B + 1,)),
+                           _plain(path, torch.int32, "path", (B, cols)), cols,
+                           _plain(path_lens, torch.int32, "path_lens", (B,)), N, max_nodes,
+                           *weights, L, *places)
+    rc = _cache_commit(a, _plain(out_context, torch.int32, "out_context", (B,)),
+                       _status(status, B), _stream())
     _done(rc, "sd_cache_commit")
     return out_context
 
 
-@_streamed
 def cache_evict(k_cache, v_cache, page_table, context_lens, mass_in, mass_out, positions_in,
                 positions_out, seen, out_context, budget, recent=0, sinks=0, status=None,
-                workspace=None):
+                workspace=None, stream=None):
     """Cut every request's cache to its `budget` slots of the largest mass,
     keeping positions below `sinks` and the last `recent` ones; out_context
     [B] receives the new lengths.  mass_* [B][H_kv][L] float32 and positions_*
     [B][H_kv][L] int32 (or None, None, with recent = sinks = 0); outputs may
     be the inputs."""
+    if stream is not None:
+        return _on(stream, cache_evict, locals())
     _here(k_cache, v_cache, page_table, context_lens, mass_in, mass_out, positions_in,
           positions_out, seen, out_context, status)
     c = _cache(k_cache, v_cache, page_table, context_lens)
@@ -423,30 +409,31 @@ def cache_evict(k_cache, v_cache, page_table, context_lens, mass_in, mass_out, p
         raise ValueError("positions_in and positions_out go together")
     places = (0, 0)
     if positions_in is not None:
-        places = (_ints(positions_in, "positions_in", B, H, L),
-                  _ints(positions_out, "positions_out", B, H, L))
-    a = _CACHE_EVICT.pack(*c, _floats(mass_in, "mass_in", B, H, L),
-                          _floats(mass_out, "mass_out", B, H, L), *places, L,
-                          0 if seen is None else _ints(seen, "seen", B), budget, recent, sinks)
+        places = (_plain(positions_in, torch.int32, "positions_in", (B, H, L)),
+                  _plain(positions_out, torch.int32, "positions_out", (B, H, L)))
+    a = _CACHE_EVICT.pack(*c, _plain(mass_in, torch.float32, "mass_in", (B, H, L)),
+                          _plain(mass_out, torch.float32, "mass_out", (B, H, L)), *places, L,
+                          0 if seen is None else _plain(seen, torch.int32, "seen", (B,)), budget,
+                          recent, sinks)
     ws, wp, n = _workspace(_cache_evict_bytes, a, workspace, k_cache)
-    rc = _cache_evict(a, wp, n, _ints(out_context, "out_context", B), _status(status, B),
-                      _stream())
+    rc = _cache_evict(a, wp, n, _plain(out_context, torch.int32, "out_context", (B,)),
+                      _status(status, B), _stream())
     _done(rc, "sd_cache_evict")
     return out_context
 
 
 # ---- a beam step ----
 
-@_streamed
 def beam_select(logits, scores, n_out, ended=None, eos_id=-1, out_ended=None, status=None,
-                out=None, workspace=None):
+                out=None, workspace=None, stream=None):
     """The n_out best continuations over the beams of each request: logits
     [B][W][V] (float32 or bfloat16), scores [B][W] float32, ended [B][W] uint8
     or None.  Returns (scores [B][n_out], parents [B][n_out], tokens
     [B][n_out]); out_ended: optional [B][n_out] uint8 output.
 
     out: optional dict of preallocated outputs (scores, parents, tokens)."""
-    import torch
+    if stream is not None:
+        return _on(stream, beam_select, locals())
     if logits.dim() != 3:
         raise ValueError("logits must be [B][W][V]")
     B, W, V = logits.shape
@@ -454,33 +441,28 @@ def beam_select(logits, scores, n_out, ended=None, eos_id=-1, out_ended=None, st
     sc, par, tok = o.get("scores"), o.get("parents"), o.get("tokens")
     _here(logits, scores, ended, out_ended, status, sc, par, tok)
     ptr, ld, code = _logits(logits, "logits")
-    a = _BEAM_SELECT.pack(ptr, ld, _floats(scores, "scores", B, W),
-                          0 if ended is None else _plain(ended, torch.uint8, "ended", B, W), code,
+    a = _BEAM_SELECT.pack(ptr, ld, _plain(scores, torch.float32, "scores", (B, W)),
+                          0 if ended is None else _plain(ended, torch.uint8, "ended", (B, W)), code,
                           B, W, V, n_out, eos_id)
-    oe = None if out_ended is None else _plain(out_ended, torch.uint8, "out_ended", B, n_out)
+    oe = None if out_ended is None else _plain(out_ended, torch.uint8, "out_ended", (B, n_out))
     ws, wp, n = _workspace(_beam_select_bytes, a, workspace, logits)
 
-    def output(t, name, dtype, check):
-        if t is None:
-            t = torch.empty((B, n_out), dtype=dtype, device=logits.device)
-        else:
-            check(t, name, B, n_out)
-        return t
-
-    sc = output(sc, "scores", torch.float32, _floats)
-    par, tok = output(par, "parents", torch.int32, _ints), output(tok, "tokens", torch.int32, _ints)
+    sc = _output(sc, torch.float32, "scores", (B, n_out), logits)
+    par = _output(par, torch.int32, "parents", (B, n_out), logits)
+    tok = _output(tok, torch.int32, "tokens", (B, n_out), logits)
     rc = _beam_select(a, wp, n, sc.data_ptr(), par.data_ptr(), tok.data_ptr(), oe,
                       _status(status, B), _stream())
     _done(rc, "sd_beam_select")
     return sc, par, tok
 
 
-@_streamed
-def beam_reorder(state, parents, lengths=None, out=None):
+def beam_reorder(state, parents, lengths=None, out=None, stream=None):
     """Move beam states to the beams that continue them: state
     [layers][B][W][segs][units][..] (the trailing part of a unit contiguous,
     a multiple of 16 bytes), parents [B][W_out] int32, lengths [B] int32 units
     in use or None.  In place without `out`; returns the tensor written."""
+    if stream is not None:
+        return _on(stream, beam_reorder, locals())
     if state.dim() < 5:
         raise ValueError("state must be [layers][B][W][segs][units][..]")
     dst = state if out is None else out
@@ -506,8 +488,9 @@ def beam_reorder(state, parents, lengths=None, out=None):
             want //= max(1, n)
         strides += [step * es for step in s[:4]]
     a = _BEAM_REORDER.pack(state.data_ptr(), dst.data_ptr(), *strides,
-                           _ints(parents, "parents", B, W_out),
-                           0 if lengths is None else _ints(lengths, "lengths", B), unit, layers, B,
+                           _plain(parents, torch.int32, "parents", (B, W_out)),
+                           0 if lengths is None else _plain(lengths, torch.int32, "lengths", (B,)), unit,
+                           layers, B,
                            W, W_out, segs, units)
     _done(_beam_reorder(a, _stream()), "sd_beam_reorder")
     return dst
