@@ -24,8 +24,8 @@
 //                over 32 chains of 9 nodes, 3.8 TB/s over longer contexts: a
 //                run's start and end take as long as 3 of its tiles), past
 //                that by the issue of softmax and products, which overlap
-//                little: 16 trees of 64 nodes over 16k to 32k slots take 460
-//                us, 670 TFLOP/s, with the matrix cores busy 36 %, the vector
+//                little: 16 trees of 64 nodes over 16k to 32k slots take 476
+//                us, 640 TFLOP/s, with the matrix cores busy 36 %, the vector
 //                ALU 44 % and LDS 34 % of the time.
 // k_attn_join    one thread per 4 output columns of a split row; latency, 6 to
 //                12 us.
@@ -684,7 +684,7 @@ AttnArgs device_args(const sd_tree_attention_args_t* p) {
 // The shape for `rows` packed rows a KV head: fewer rows leave more waves to
 // the keys.  16 rows a wave need no register spills and win up to 128 rows (63
 // rows 49 us against 64 for 32 a wave, 28 rows 52 against 90, 112 rows 61 against
-// 78); past that 32 a wave halve the LDS reads (448 rows 460 us against 600).
+// 78); past that 32 a wave halve the LDS reads (448 rows 462 us against 600).
 // f(Shape{}) is called with the one taken.
 template <int D, typename F>
 auto with_shape(int rows, F&& f) {

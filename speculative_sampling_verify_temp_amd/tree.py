@@ -490,7 +490,6 @@ def beam_reorder(state, parents, lengths=None, out=None, stream=None):
     a = _BEAM_REORDER.pack(state.data_ptr(), dst.data_ptr(), *strides,
                            _plain(parents, torch.int32, "parents", (B, W_out)),
                            0 if lengths is None else _plain(lengths, torch.int32, "lengths", (B,)), unit,
-                           layers, B,
-                           W, W_out, segs, units)
+                           layers, B, W, W_out, segs, units)
     _done(_beam_reorder(a, _stream()), "sd_beam_reorder")
     return dst
