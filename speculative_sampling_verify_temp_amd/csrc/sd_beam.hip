@@ -155,16 +155,17 @@ __global__ __launch_bounds__(NT_B, 6) void k_beam_rows(BeamArgs a) {
   }
   if (nan) top = INFINITY;           // reported like one
   // exponentials against the thread's own maximum: at most 32 terms of at most
-  // 1 in fp32; the threads' sums meet in 64 bits
+  // 1 in fp32; the threads' sums meet in 64 bits.  The maximum is taken off before
+  // the scaling: the term of the maximum is exactly 1 whatever the logits' level,
+  // and the lowest finite logits, as masks hold them, stay in range.
   constexpr float C = 1.4426950408889634f;
   float s = 0.0f;
   if (top > -INFINITY && top < INFINITY) {
-    const float g = top * C;
 #pragma unroll
     for (int u = 0; u < NV; ++u)
       if (u < mine) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += fast_exp2(fmaf(logit_of<DT>(w[u], e), C, -g));
+        for (int e = 0; e < E; ++e) s += fast_exp2((logit_of<DT>(w[u], e) - top) * C);
       }
   }
   const uint32_t o = ord_key(top), group = lanes_max<4>(o);

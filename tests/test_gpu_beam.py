@@ -83,6 +83,58 @@ def test_ties_go_to_the_lowest_beam_and_token(dtype):
     assert torch.equal(got[0], _sdv().beam_select(dev(z, torch_dtype(dtype)), dev(sc), 40)[0])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", ["lowest", -1e30, -1e20, -1e10])
+def test_masked_vocabularies(dtype, value):
+    """Finite mask values over runs of neighbouring tokens, the end of the
+    vocabulary, or all tokens but a few: the sums of the others stand, and the
+    masked tokens are candidates behind them."""
+    import torch
+    rng = np.random.default_rng(11)
+    B, W, V, n = 4, 3, 9001, 12
+    low = float(torch.finfo(torch_dtype(dtype)).min) if value == "lowest" else value
+    z = rng.standard_normal((B, W, V)) * 3
+    z[0, :, 64:4000] = low                        # a run
+    z[1, :, 7000:] = low                          # a padded vocabulary
+    keep = rng.integers(0, V, (W, 3))             # a constraint that leaves three tokens
+    few = np.full((W, V), low)
+    for w in range(W):
+        few[w, keep[w]] = z[2, w, keep[w]]
+    z[2] = few
+    z[3, :, ::2] = low                            # every other one
+    z = rounded(z, dtype)
+    sc = (-rng.random((B, W)) * 2).astype(np.float32)
+    ld = -(-V // 8) * 8
+    full = np.full((B, W, ld), np.nan)
+    full[..., :V] = z
+    status = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    print(f"masked {dtype} {value}", flush=True)
+    got = _sdv().beam_select(dev(full, torch_dtype(dtype))[..., :V], dev(sc), n, status=status)
+    assert status.tolist() == [0] * B
+    assert _check(z, sc, n, got) >= 3 * B
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scores_do_not_depend_on_the_level_of_the_logits(dtype):
+    """Rows far from zero, another level for every beam: a score is a
+    difference, as exact there as anywhere."""
+    rng = np.random.default_rng(12)
+    B, W, V, n = 3, 6, 20011, 10
+    z = rng.standard_normal((B, W, V)) * 3
+    z[0] += np.array([1000.0, -5000.0, 0.0, 30.0, 100.0, -77.0])[:, None]
+    z[1] += 1000.0
+    z[2] -= np.array([4000.0, 4100.0, 1e5, 2e4, 3e4, 5e4])[:, None]
+    z[2, 3, 77] += 400.0                          # one token that dominates
+    z = rounded(z, dtype)
+    sc = (-rng.random((B, W)) * 2).astype(np.float32)
+    ld = -(-V // 8) * 8
+    full = np.full((B, W, ld), np.nan)
+    full[..., :V] = z
+    print(f"levels {dtype}", flush=True)
+    got = _sdv().beam_select(dev(full, torch_dtype(dtype))[..., :V], dev(sc), n)
+    assert _check(z, sc, n, got) >= n
+
+
 def test_ended_inactive_and_bad_beams():
     import torch
     sdv = _sdv()
