@@ -131,8 +131,7 @@ def beam_select_ref(logits, scores, n_out, ended=None, eos=-1):
             continue
         z = logits[w]
         m = z.max()
-        lse = m + math.log(np.exp(z - m).sum())
-        x = float(scores[w]) + (z - lse)
+        x = float(scores[w]) + ((z - m) - math.log(np.exp(z - m).sum()))     # the level cancels first
         order = np.argsort(-z, kind="stable")[:n_out]
         cand += [(float(x[i]), w, int(i)) for i in order if z[i] > -math.inf]
     cand.sort(key=lambda c: (-c[0], c[1], c[2]))

@@ -3,8 +3,9 @@
 // k_beam_rows    one workgroup per (beam, slice of the vocabulary), the slice in
 //                registers: its maximum, its sum of exponentials and its n_out
 //                best logits in order (larger logit, then lower id);
-// k_beam_merge   one workgroup per request: each beam's log-sum-exp from its
-//                slices, the candidates' scores in 64 bits, the n_out best.
+// k_beam_merge   one workgroup per request: each beam's maximum and the logarithm
+//                of its sum from its slices, the candidates' scores in 64 bits,
+//                the n_out best.
 //
 // Both choose the n best of many in the same way: the n-th largest of 64 maxima,
 // each of a 64th of the threads, bounds the n-th largest of all from below, so
@@ -254,7 +255,10 @@ struct Candidate {
 // Latency: 8 us for 8 beams of 19 slices (14 us with 256 threads, which took the
 // beams four at a time).
 __global__ __launch_bounds__(NT_M) void k_beam_merge(BeamArgs a) {
-  __shared__ double lse[MAXO];
+  // log-sum-exp = top + rest, kept apart: where the logits are far from zero (a
+  // row of nothing but masks) their sum would lose the rest, even in 64 bits
+  __shared__ double rest[MAXO];
+  __shared__ float top_of[MAXO];
   __shared__ uint8_t kind[MAXO];      // 0: no candidates, 1: its slices', 2: ended
   __shared__ uint32_t st_sh;
   __shared__ __align__(16) uint64_t keys[WAVE];
@@ -268,13 +272,13 @@ __global__ __launch_bounds__(NT_M) void k_beam_merge(BeamArgs a) {
     const int bw = b * a.W + w;
     const float sc = a.scores[bw];
     uint32_t st = 0;
+    float m = -INFINITY;
     double e = 0.0;
     const int kd = !(sc > -INFINITY) ? 0 : a.ended && a.ended[bw] ? 2 : 1;
     if (sc != sc || sc == INFINITY) st |= SD_ST_BAD_PARAM;
     if (kd == 1 && !st) {
       const float* pm = a.part_m + (int64_t)bw * a.slices;
       const double* ps = a.part_s + (int64_t)bw * a.slices;
-      float m = -INFINITY;
       bool bad = false;
       for (int s = l; s < a.slices; s += WAVE) {
         bad |= pm[s] != pm[s];
@@ -286,11 +290,11 @@ __global__ __launch_bounds__(NT_M) void k_beam_merge(BeamArgs a) {
         double z = 0.0;
         for (int s = l; s < a.slices; s += WAVE)
           if (pm[s] > -INFINITY) z += ps[s] * exp((double)pm[s] - (double)m);
-        e = (double)m + log(wave_sum(z));
+        e = log(wave_sum(z));
       }
     }
     if (l == 0) {
-      lse[w] = e, kind[w] = (uint8_t)kd, score[w] = sc;
+      rest[w] = e, top_of[w] = m, kind[w] = (uint8_t)kd, score[w] = sc;
       if (st) atomicOr(&st_sh, st);
     }
   }
@@ -308,7 +312,7 @@ __global__ __launch_bounds__(NT_M) void k_beam_merge(BeamArgs a) {
       const uint64_t k = a.part_best[(int64_t)b * a.W * per + c];
       if (k) {
         id = (int)~(uint32_t)k;
-        sc = (double)score[w] + ((double)from_ord32((uint32_t)(k >> 32)) - lse[w]);
+        sc = (double)score[w] + (((double)from_ord32((uint32_t)(k >> 32)) - (double)top_of[w]) - rest[w]);
       }
     }
     if (sc > -INFINITY) x.s = ord64(sc), x.i = ~((uint64_t)w << 32 | (uint32_t)id);

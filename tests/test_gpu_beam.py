@@ -135,6 +135,30 @@ def test_scores_do_not_depend_on_the_level_of_the_logits(dtype):
     assert _check(z, sc, n, got) >= n
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_nothing_but_masks_are_uniform(dtype):
+    """A beam whose logits are all the same mask value spreads its score evenly,
+    -log V each, whatever that value: it does not outrank a beam that chose."""
+    import torch
+    rng = np.random.default_rng(13)
+    V, n = 5003, 9
+    low = float(torch.finfo(torch_dtype(dtype)).min)
+    z = rng.standard_normal((6, 3, V)) * 3
+    for b, value in enumerate((low, -1e30, -1e20, -1e10, 1e30, -low)):
+        z[b, 1] = value
+    z[0, 2, 1:] = low                             # one token left
+    z = rounded(z, dtype)
+    sc = np.zeros((6, 3), dtype=np.float32)
+    sc[:, 0], sc[:, 2] = -5.0, -6.0
+    ld = -(-V // 8) * 8
+    full = np.full((6, 3, ld), np.nan)
+    full[..., :V] = z
+    got = _sdv().beam_select(dev(full, torch_dtype(dtype))[..., :V], dev(sc), n)
+    assert _check(z, sc, n, got) >= 3 * 6
+    s, par, _ = (t.cpu().numpy() for t in got)
+    assert np.abs(s[par == 1] + math.log(V)).max() < 1e-5
+
+
 def test_ended_inactive_and_bad_beams():
     import torch
     sdv = _sdv()

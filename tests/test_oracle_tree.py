@@ -126,3 +126,14 @@ def test_beam_against_a_full_sort():
     np.testing.assert_allclose([x for x, _, _ in got], p.ravel()[order])
     ended = oracle.beam_select_ref(z, np.array([0.0, 5.0, -np.inf]), 3, ended=[0, 1, 0], eos=4)
     assert ended[0] == (5.0, 1, 4) and all(w == 0 for _, w, _ in ended[1:])
+
+
+def test_beam_scores_do_not_depend_on_the_level_of_the_logits():
+    z = np.array([[2.0, 1.0, 0.0, 2.0]])
+    want = oracle.beam_select_ref(z, np.zeros(1), 4)
+    for level in (-1e4, 2.0 ** 40):
+        got = oracle.beam_select_ref(z + level, np.zeros(1), 4)
+        assert [c[1:] for c in got] == [c[1:] for c in want]
+        np.testing.assert_allclose([c[0] for c in got], [c[0] for c in want], atol=1e-12)
+    flat = oracle.beam_select_ref(np.full((1, 8), -3e38), np.zeros(1), 2)
+    assert [c[1:] for c in flat] == [(0, 0), (0, 1)] and flat[0][0] == pytest.approx(-math.log(8))
