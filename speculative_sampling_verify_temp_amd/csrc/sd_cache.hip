@@ -185,18 +185,28 @@ __global__ __launch_bounds__(NT_C, 2) void k_commit(CommitArgs a, int chunk) {
           q[ks] = *(const s16x8*)(sq + lr * (D * 2) + (((ks * 4 + g4) ^ swz<D>(lr)) * 16));
         }
         const f32x4 e = *(const f32x4*)(se + rt * 16 + g4 * 4);
+        // Row i sees the slots in use and the appended ones 0 .. i.  Rows past the last
+        // one have e = +inf; their zeros times an infinite key are not numbers, so
+        // they are left out, not added: up[r] is the last appended slot whose key
+        // row r counts for.
+        const bool chosen = fresh || __any(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) == INFINITY);
+        int up[4] = {};
+        if (chosen) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            up[r] = fresh ? (q0 + rt * 16 + g4 * 4 + r) / a.G : INT_MAX;
+            if (e[r] == INFINITY) up[r] = INT_MIN;
+          }
+        }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) x = mfma<DT>(q[ks], k[s][ks], x);
-          if (fresh) {              // row i sees the appended slots 0 .. i
+          if (chosen) {
             const int j = base + w * 64 + s * 16 + n - br.ctx;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int i = (q0 + rt * 16 + g4 * 4 + r) / a.G;
-              sum[s] += j <= i ? fast_exp2(fmaf(x[r], c, -e[r])) : 0.0f;
-            }
+            for (int r = 0; r < 4; ++r) sum[s] += j <= up[r] ? fast_exp2(fmaf(x[r], c, -e[r])) : 0.0f;
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) sum[s] += fast_exp2(fmaf(x[r], c, -e[r]));

@@ -104,6 +104,35 @@ def test_commit_matches_the_oracle(case, dtype):
     _check_commit(c, paths, decay, mass, kw, in_place)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,Hq,Hkv,kept", [(64, 4, 2, 1), (128, 28, 4, 3), (128, 16, 1, 1), (64, 32, 1, 5)])
+def test_infinite_keys_have_no_weight_where_their_scores_are_minus_infinity(D, Hq, Hkv, kept, dtype):
+    """Cached and drafted keys with an infinite element, against queries that all
+    have the other sign there: weight zero, whatever the number of rows."""
+    c = Cached(224, [150, 20], [6, 6], Hq, Hkv, D, 16, dtype, room=8)
+    c.q[:, :, 3] = -np.abs(c.q[:, :, 3]) - 1.0
+    c.d["q"].copy_(dev(c.q, c.d["q"].dtype))
+    c.q = c.d["q"].double().cpu().numpy()
+    paths = [list(range(kept)), [0]]
+    for b, t in ((0, 0), (0, 77), (0, 149), (1, 19)):
+        for x in (c.k, c.k_dev):
+            x[c.table[b, t // 16], :, t % 16, 3] = np.inf
+        c.d["k_cache"][int(c.table[b, t // 16]), :, t % 16, 3] = float("inf")
+    c.kn[kept - 1, :, 3] = np.inf
+    c.d["k_new"][kept - 1, :, 3] = float("inf")
+    # finite magnitudes for the bound of the scores' errors
+    bound = Cached.score_error(type("", (), dict(scale=c.scale, D=D, q=c.q, k=np.nan_to_num(c.k, posinf=0.0),
+                                                 kn=np.nan_to_num(c.kn, posinf=0.0)))())
+    c.score_error = lambda: bound
+    L = c.table.shape[1] * 16
+    print(f"infinite keys {D} {Hq} {Hkv} {kept} {dtype}", flush=True)
+    mass, kw = _commit(c, paths, 0.5, L, 3)
+    assert np.isfinite(c.lse).all()
+    _check_commit(c, paths, 0.5, mass, kw, False)
+    for t in (0, 77, 149):
+        np.testing.assert_array_equal(kw["mass_out"][0, :, t].cpu().numpy(), 0.5 * mass[0, :, t])
+
+
 def test_a_branch_may_name_a_node_twice():
     c = Cached(223, [40, 3], [4, 4], 4, 2, 64, 16, "bf16", room=8)
     L = c.table.shape[1] * 16
