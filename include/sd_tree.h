@@ -173,7 +173,8 @@ int sd_tree_verify_greedy(const sd_tree_verify_args_t *args, void *workspace,
  *   mass_out[t] = decay * mass_in[t] + w(t)   for t < context_lens[b]
  *   mass_out[t] = w(t)                        for the appended slots;
  * slots behind them are left as they were.  With decay = 0 mass_in is not
- * read.  lse is what sd_tree_attention gave for these rows.  A slot of a bad
+ * read.  lse is what sd_tree_attention gave for these rows; one of -inf (the row
+ * saw nothing) makes its row add no weight.  A slot of a bad
  * page has w = 0; an appended slot on one is not written.  mass_in may be
  * mass_out.  out_context must not be context_lens.  An invalid request appends
  * nothing: its mass and positions stay and out_context[b] = context_lens[b].

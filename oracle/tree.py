@@ -103,6 +103,8 @@ def commit_weights_ref(q, lse, k_new, k_cache, table_row, ctx, rows, h, scale):
     w = np.zeros(ctx + len(rows))
     for i, r in enumerate(rows):
         for g in range(q.shape[1]):
+            if lse[r, g] == -math.inf:      # the row saw nothing
+                continue
             w[:ctx] += np.where(there, np.exp(scale * (k @ q[r, g]) - lse[r, g]), 0.0)
             for j in range(i + 1):
                 w[ctx + j] += math.exp(scale * float(k_new[rows[j], h] @ q[r, g]) - lse[r, g])

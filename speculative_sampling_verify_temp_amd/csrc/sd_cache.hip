@@ -123,7 +123,7 @@ __global__ __launch_bounds__(NT_C, 2) void k_commit(CommitArgs a, int chunk) {
   const int rows = br.m * a.G;
   const float c = a.scale * 1.4426950408889634f;
 
-  auto stage = [&](int q0) {       // query rows q0 .. q0 + QB - 1, zeros and +inf past the last
+  auto stage = [&](int q0) {       // query rows q0 .. q0 + QB - 1, zeros past the last; e = +inf: not counted
     __syncthreads();
     for (int u = tid; u < QB * CPR; u += NT_C) {
       const int lr = u / CPR, col = u % CPR, r = q0 + lr;
@@ -141,6 +141,7 @@ __global__ __launch_bounds__(NT_C, 2) void k_commit(CommitArgs a, int chunk) {
       if (r < rows) {
         const int64_t node = br.first + a.path[b * a.ld_path + r / a.G];
         e = a.lse[node * a.Hq + h * a.G + r % a.G] * 1.4426950408889634f;
+        if (e == -INFINITY) e = INFINITY;      // it saw nothing: no weight
       }
       se[lr] = e;
     }
@@ -185,8 +186,8 @@ __global__ __launch_bounds__(NT_C, 2) void k_commit(CommitArgs a, int chunk) {
           q[ks] = *(const s16x8*)(sq + lr * (D * 2) + (((ks * 4 + g4) ^ swz<D>(lr)) * 16));
         }
         const f32x4 e = *(const f32x4*)(se + rt * 16 + g4 * 4);
-        // Row i sees the slots in use and the appended ones 0 .. i.  Rows past the last
-        // one have e = +inf; their zeros times an infinite key are not numbers, so
+        // Row i sees the slots in use and the appended ones 0 .. i.  Rows that do not
+        // count have e = +inf.  Products with an infinite key may not be numbers, so
         // they are left out, not added: up[r] is the last appended slot whose key
         // row r counts for.
         const bool chosen = fresh || __any(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) == INFINITY);

@@ -133,6 +133,18 @@ def test_infinite_keys_have_no_weight_where_their_scores_are_minus_infinity(D, H
         np.testing.assert_array_equal(kw["mass_out"][0, :, t].cpu().numpy(), 0.5 * mass[0, :, t])
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (32, 2), (28, 4)])
+def test_rows_that_saw_nothing_give_no_weight(Hq, Hkv):
+    """An lse of -inf, as attention leaves it for a row whose mask is empty."""
+    c = Cached(225, [0, 40], [4, 4], Hq, Hkv, 64, 16, "bf16", room=8)
+    _, e, _ = c.reference()
+    e[0] = -np.inf
+    e[5, 1::2] = -np.inf
+    mass, kw = _commit(c, [[0, 1, 3], [0, 1]], 0.5, c.table.shape[1] * 16, 1, lse=dev(e.astype(np.float32)))
+    c.lse = kw["lse"].double().cpu().numpy()
+    _check_commit(c, [[0, 1, 3], [0, 1]], 0.5, mass, kw, False)
+
+
 def test_a_branch_may_name_a_node_twice():
     c = Cached(223, [40, 3], [4, 4], 4, 2, 64, 16, "bf16", room=8)
     L = c.table.shape[1] * 16

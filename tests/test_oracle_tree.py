@@ -69,6 +69,16 @@ def test_weights_of_a_branch_sum_to_its_rows():
     assert w.sum() == pytest.approx(6.0)
 
 
+def test_rows_that_saw_nothing_give_no_weight():
+    rng = np.random.default_rng(7)
+    q, kn, vn, k, v, table, off = _tiny(rng, B=1)
+    _, lse, _ = oracle.tree_attention_ref(q, kn, vn, k, v, table, [0], off, 0.5, mask=[0, 2, 6])
+    assert lse[0, 2] == -math.inf and np.isfinite(lse[1:]).all()
+    w = oracle.commit_weights_ref(q[:, 2:4], lse[:, 2:4], kn, k, table[0], 0, [0, 1], 1, 0.5)
+    one = oracle.commit_weights_ref(q[1:, 2:4], lse[1:, 2:4], kn[1:], k, table[0], 0, [0], 1, 0.5)
+    assert w[1] == pytest.approx(one[0]) == pytest.approx(2.0)
+
+
 def test_greedy_walk_against_all_branches():
     """The walk's branch is the longest one whose every token is its parent's
     argmax, the lowest sibling first."""
