@@ -221,7 +221,11 @@ int sd_cache_commit(const sd_cache_commit_args_t *args, int32_t *out_context,
  * mass_out and positions_out are written for the slots kept; they may be
  * mass_in and positions_in.  out_context[b] = min(context_lens[b], budget).
  * positions NULL: sinks = recent = 0.  An invalid request is left as it was.
- * Moves from or to a bad page are left out.  The request's pages are its own.
+ * A bad page's slots are ranked like the others, and their masses and positions
+ * move like the others', but their keys and values are neither read nor written:
+ * the place that such a row would move to keeps the row that it held, under the
+ * mass and position of the other.  So a request reported with SD_ST_BAD_PAGE has
+ * a cache that is no longer that of its tokens.  The request's pages are its own.
  * ------------------------------------------------------------------------ */
 typedef struct sd_cache_evict_args {
   sd_kv_cache_t  cache;

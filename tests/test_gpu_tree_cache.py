@@ -338,6 +338,32 @@ def test_evict_without_positions_and_with_bad_pages():
     assert status.tolist() == [sdv.SD_ST_BAD_PAGE, 0]
 
 
+def test_evict_moves_masses_and_positions_but_not_rows_of_bad_pages():
+    """One slot on a bad page moves into a hole of a good one, and one of a good
+    page into a hole of a bad one: the bookkeeping follows the ranking, no row of
+    either move is touched."""
+    import torch
+    sdv = _sdv()
+    c = Cached(323, [64], [1], 1, 1, 64, 16, "bf16")
+    c.table[0, 0], c.table[0, 3] = -1, c.k.shape[0]                    # slots 0..15 and 48..63
+    c.d["page_table"] = dev(c.table)
+    mass = torch.arange(80, dtype=torch.float32, device="cuda").flip(0).reshape(1, 1, 80).contiguous()
+    mass[0, 0, [3, 20, 21, 40, 41, 50]] = torch.tensor([-1.0, -2.0, -3.0, 99.0, 98.0, 97.0], device="cuda")
+    pos = torch.arange(80, dtype=torch.int32, device="cuda").reshape(1, 1, 80).contiguous()
+    want = list(range(32))
+    want[3], want[20], want[21] = 40, 41, 50
+    m0, k0, v0 = mass[0, 0].clone(), c.d["k_cache"].clone(), c.d["v_cache"].clone()
+    out, st = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    sdv.cache_evict(c.d["k_cache"], c.d["v_cache"], c.d["page_table"], c.d["context_lens"], mass, mass, pos, pos,
+                    dev(np.array([64], np.int32)), out, 32, status=st)
+    assert st.tolist() == [sdv.SD_ST_BAD_PAGE] and out.tolist() == [32]
+    assert pos[0, 0, :32].tolist() == want and torch.equal(mass[0, 0, :32], m0[want])
+    p, q = int(c.table[0, 1]), int(c.table[0, 2])
+    k0[p, 0, 4], v0[p, 0, 4] = k0[q, 0, 9], v0[q, 0, 9]                # 41 -> 20: both pages are good
+    assert torch.equal(c.d["k_cache"].view(torch.int16), k0.view(torch.int16))
+    assert torch.equal(c.d["v_cache"].view(torch.int16), v0.view(torch.int16))
+
+
 def test_evict_leaves_a_request_of_wrong_length_alone():
     import torch
     sdv = _sdv()
