@@ -64,7 +64,10 @@ extern "C" {
                                        as -1 (a node that no walk reaches)       */
 #define SD_ST_BAD_PATH  (1u << 12)  /* path length outside [0, nodes], or a path
                                        node outside the request         invalid */
-#define SD_ST_TREE_INVALID_MASK (SD_ST_INVALID_MASK | SD_ST_BAD_LEN | SD_ST_BAD_NODES | SD_ST_BAD_PATH)
+#define SD_ST_UNFINISHED (1u << 13) /* a walk was given up: calls that overlap in time
+                                       shared its workspace              invalid */
+#define SD_ST_TREE_INVALID_MASK (SD_ST_INVALID_MASK | SD_ST_BAD_LEN | SD_ST_BAD_NODES | SD_ST_BAD_PATH | \
+                                 SD_ST_UNFINISHED)
 
 typedef struct sd_kv_cache {
   void          *k, *v;          /* 16-byte aligned, the same strides           */
@@ -138,7 +141,7 @@ int sd_tree_attention(const sd_tree_attention_args_t *args, void *workspace,
  * without children).  Rows of nodes that the walk does not visit do not enter
  * the results: a NaN there is not reported.  An invalid request (SD_ST_BAD_NODES,
  * SD_ST_BAD_DRAFT_ID: a drafted token outside [0, V), SD_ST_NONFINITE: a
- * NaN in a visited row) gets -1 everywhere.
+ * NaN in a visited row, SD_ST_UNFINISHED) gets -1 everywhere.
  * ------------------------------------------------------------------------ */
 typedef struct sd_tree_verify_args {
   const void    *logits;         /* [N] rows of V, SD_F32 or SD_BF16, 16-byte aligned rows */

@@ -345,6 +345,16 @@ int sd_debug_fallback_units(const sd_verify_args_t *args, const void *workspace,
                             size_t workspace_bytes, int32_t *out_count, uint32_t *out_why,
                             void *stream);
 
+/* Test export: sd_tree_verify_greedy (sd_tree.h) whose workgroups wait for each
+ * other for at most `polls` looks.  With 0 they give up at once, as they would in
+ * the end where overlapping calls took each other's work: requests whose walk
+ * needs a row report SD_ST_UNFINISHED.  Only batches large enough for walks that
+ * read their own rows wait at all. */
+struct sd_tree_verify_args;
+int sd_debug_tree_verify_polls(const struct sd_tree_verify_args *args, void *workspace,
+                               size_t workspace_bytes, int32_t *out_accepted, int32_t *out_path,
+                               int32_t *out_tokens, uint32_t *out_status, int32_t polls, void *stream);
+
 /* Test export: the Philox uniforms u, v for rows 0..B-1 and positions
  * 0..npos-1, written to out_u / out_v [B][npos] (fp32, exact). */
 int sd_debug_uniforms(uint64_t seed, uint64_t offset, int32_t B, int32_t npos,

@@ -436,7 +436,7 @@ def debug_lmhead_logits(args, out_target, out_draft=None, workspace=None, stream
 
 from .tree import (  # noqa: E402  (needs the loaded library)
     SD_F16, SD_MAX_BEAMS, SD_MAX_NODES, SD_ST_BAD_LEN, SD_ST_BAD_NODES, SD_ST_BAD_PAGE,
-    SD_ST_BAD_PATH, SD_ST_BAD_TREE, SD_ST_TREE_INVALID_MASK, beam_reorder, beam_select,
-    cache_commit, cache_evict, make_tree_attention_args, tree_attention,
+    SD_ST_BAD_PATH, SD_ST_BAD_TREE, SD_ST_TREE_INVALID_MASK, SD_ST_UNFINISHED, beam_reorder,
+    beam_select, cache_commit, cache_evict, make_tree_attention_args, tree_attention,
     tree_attention_workspace_bytes, tree_verify_greedy,
 )

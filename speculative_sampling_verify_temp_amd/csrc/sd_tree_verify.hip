@@ -34,6 +34,7 @@ struct VerifyArgs {
   int B, N, V, max_nodes;
   uint32_t flags;
   int slices, slice_vecs;   // 16-byte vectors of a slice
+  int polls;                // looks at a row that is waited for
   uint64_t* part;           // [N][slices] ([B][slices] where walks read their rows)
   Team* team;               // [B], there
   int32_t *accepted, *path, *out_tokens;
@@ -220,8 +221,7 @@ __global__ __launch_bounds__(WAVE) void k_tree_walk(VerifyArgs a) {
 // an earlier one is running, so every wait ends however few workgroups of a
 // team the chip holds at a time.  (Calls that overlap on one workspace, which
 // the interface forbids, could take each other's tickets: waits are bounded, and
-// such a request keeps the -1 that its results begin with.)
-
+// such a request keeps the -1 and SD_ST_UNFINISHED that its results begin with.)
 //
 // What the team shares is only touched by relaxed agent-scope atomics, which
 // act where all of the chip's caches meet; a wait for the ones before stands
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(WAVE) void k_tree_begin(VerifyArgs a) {
   const int b = blockIdx.x, l = threadIdx.x;
   Walk w(a, b);
   const bool go = w.valid() && w.enter(a.flags);
-  finish(a, b, w.st, go ? -1 : 0, go ? -1 : w.my_path, -1);
+  finish(a, b, w.st | (go ? SD_ST_UNFINISHED : 0u), 0, w.my_path, -1);
   if (l == 0) {
     Team& t = a.team[b];
     t.ticket = t.left = 0;
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(NT_D) void k_tree_descend(VerifyArgs a) {
     if (tid == 0) {
       const uint32_t depth = next / (uint32_t)a.slices;
       uint32_t r = DONE;
-      for (int i = 0; i < MAX_POLLS; ++i) {
+      for (int i = 0; i < a.polls; ++i) {
         r = shared_load(&team.row);
         if (r == DONE || (r >> 8) >= depth) break;
         r = DONE;
@@ -398,6 +398,14 @@ extern "C" int sd_tree_verify_greedy(const sd_tree_verify_args_t* args, void* wo
                                      size_t workspace_bytes, int32_t* out_accepted,
                                      int32_t* out_path, int32_t* out_tokens,
                                      uint32_t* out_status, void* stream) {
+  return sd_debug_tree_verify_polls(args, workspace, workspace_bytes, out_accepted, out_path, out_tokens,
+                                    out_status, MAX_POLLS, stream);
+}
+
+extern "C" int sd_debug_tree_verify_polls(const sd_tree_verify_args_t* args, void* workspace,
+                                          size_t workspace_bytes, int32_t* out_accepted,
+                                          int32_t* out_path, int32_t* out_tokens,
+                                          uint32_t* out_status, int32_t polls, void* stream) {
   size_t need = 0;
   const int rc = sd_tree_verify_workspace_bytes(args, &need);
   if (rc) return rc;
@@ -411,6 +419,7 @@ extern "C" int sd_tree_verify_greedy(const sd_tree_verify_args_t* args, void* wo
   a.B = args->B, a.N = args->N, a.V = args->V, a.max_nodes = args->max_nodes;
   a.flags = args->flags;
   a.slices = s.count, a.slice_vecs = s.vecs;
+  a.polls = polls;
   a.part = static_cast<uint64_t*>(workspace);
   a.team = reinterpret_cast<Team*>(static_cast<char*>(workspace) + parts_bytes(args, s));
   a.accepted = out_accepted, a.path = out_path, a.out_tokens = out_tokens, a.status = out_status;

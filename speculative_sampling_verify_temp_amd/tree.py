@@ -28,8 +28,9 @@ SD_MAX_BEAMS = 64
 SD_MAX_PAGE_SIZE = 1024
 SD_MAX_GROUP = 32
 SD_ST_BAD_LEN, SD_ST_BAD_NODES, SD_ST_BAD_PAGE = 1 << 8, 1 << 9, 1 << 10
-SD_ST_BAD_TREE, SD_ST_BAD_PATH = 1 << 11, 1 << 12
-SD_ST_TREE_INVALID_MASK = SD_ST_INVALID_MASK | SD_ST_BAD_LEN | SD_ST_BAD_NODES | SD_ST_BAD_PATH
+SD_ST_BAD_TREE, SD_ST_BAD_PATH, SD_ST_UNFINISHED = 1 << 11, 1 << 12, 1 << 13
+SD_ST_TREE_INVALID_MASK = (SD_ST_INVALID_MASK | SD_ST_BAD_LEN | SD_ST_BAD_NODES | SD_ST_BAD_PATH |
+                           SD_ST_UNFINISHED)
 
 _P, _I32, _I64, _U32, _F, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
                                  ctypes.c_float, ctypes.c_size_t)

@@ -146,6 +146,55 @@ def test_defects_are_reported_request_by_request(copies):
     assert not any(st[b].item() & sdv.SD_ST_BAD_NODES for b in (0, 2, 5))
 
 
+def test_a_walk_that_is_given_up_is_reported():
+    """The bounded waits of walks that read their own rows, forced to run out at
+    once: such requests are -1 with a status of their own, the others stand, and
+    the next call on the same workspace is whole."""
+    import ctypes
+    import torch
+    import speculative_sampling_verify_temp_amd.tree as tree
+    sdv = _sdv()
+    rng = np.random.default_rng(5)
+    B, T, V = 400, 8, 20011
+    ld = -(-V // 4) * 4
+    nodes = [T] * B
+    nodes[9] = 1                                      # a single node needs no row without a bonus
+    off = np.concatenate([[0], np.cumsum(nodes)]).astype(np.int32)
+    N = int(off[-1])
+    x = torch.randn((N, ld), device="cuda")[:, :V]
+    parents = np.concatenate([np.arange(-1, n - 1) for n in nodes]).astype(np.int32)
+    tokens = rng.integers(0, V, N).astype(np.int32)
+    tokens[5 * T + 3] = -1                            # an invalid request says why it is so
+    t, p, o = dev(tokens), dev(parents), dev(off)
+    a = tree._TREE_VERIFY.pack(x.data_ptr(), ld, t.data_ptr(), p.data_ptr(), o.data_ptr(), 0, B, N, V, T, 1)
+    n = tree._tree_verify_bytes(a)
+    ws = torch.full((n,), 0xEE, dtype=torch.uint8, device="cuda")
+    out = dict(accepted=torch.full((B,), 7, dtype=torch.int32, device="cuda"),
+               path=torch.full((B, T), 7, dtype=torch.int32, device="cuda"),
+               tokens=torch.full((B, T), 7, dtype=torch.int32, device="cuda"))
+    st = torch.full((B,), 7, dtype=torch.int32, device="cuda")
+    P = ctypes.c_void_p
+    rc = sdv.lib.sd_debug_tree_verify_polls(ctypes.c_char_p(a), P(ws.data_ptr()), ctypes.c_size_t(n), P(out["accepted"].data_ptr()),
+                                            P(out["path"].data_ptr()), P(out["tokens"].data_ptr()), P(st.data_ptr()),
+                                            ctypes.c_int32(0), P(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0
+    torch.cuda.synchronize()
+    want = np.full(B, sdv.SD_ST_UNFINISHED)
+    want[5], want[9] = sdv.SD_ST_BAD_DRAFT_ID, 0
+    assert np.array_equal(st.cpu().numpy(), want)
+    assert sdv.SD_ST_UNFINISHED & sdv.SD_ST_TREE_INVALID_MASK
+    acc = out["accepted"].cpu().numpy()
+    assert acc[9] == 0 and (np.delete(acc, 9) == -1).all()
+    assert out["path"][9].tolist() == [0] + [-1] * (T - 1)
+    bad = torch.arange(B, device="cuda") != 9
+    assert (out["path"][bad] == -1).all() and (out["tokens"] == -1).all()
+    got = sdv.tree_verify_greedy(x, t, p, o, T, flags=1, status=st, out=out, workspace=ws)
+    want[want == sdv.SD_ST_UNFINISHED] = 0
+    assert np.array_equal(st.cpu().numpy(), want)
+    ref = sdv.tree_verify_greedy(x, t, p, o, T, flags=1)
+    assert all(torch.equal(r, g) for r, g in zip(ref, got)) and (np.delete(got[0].cpu().numpy(), 5) >= 0).all()
+
+
 def test_verify_in_a_graph():
     import torch
     sdv = _sdv()
