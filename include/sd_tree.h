@@ -151,7 +151,7 @@ typedef struct sd_tree_verify_args {
   const int32_t *node_offsets;   /* [B + 1]                                     */
   int32_t        dtype;
   int32_t        B;              /* 1 .. 65535                                  */
-  int32_t        N;              /* 1 .. 2^24                                   */
+  int32_t        N;              /* 1 .. 2^24 - 1                               */
   int32_t        V;              /* < 2^28                                      */
   int32_t        max_nodes;
   uint32_t       flags;          /* SD_NO_BONUS                                 */
@@ -267,7 +267,7 @@ typedef struct sd_beam_select_args {
   const float   *scores;         /* [B][W]                                      */
   const uint8_t *ended;          /* [B][W] or NULL                              */
   int32_t        dtype;
-  int32_t        B;              /* 1 .. 2^20                                   */
+  int32_t        B;              /* 1 .. 2^20, B * W < 2^24                     */
   int32_t        W;              /* 1 .. SD_MAX_BEAMS                           */
   int32_t        V;              /* < 2^24                                      */
   int32_t        n_out;          /* 1 .. SD_MAX_BEAMS                           */

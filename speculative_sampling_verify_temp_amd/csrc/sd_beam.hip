@@ -419,6 +419,8 @@ int check(const sd_beam_select_args_t* p) {
     return SD_EINVAL;
   if (p->W > SD_MAX_BEAMS || p->n_out > SD_MAX_BEAMS || p->V >= (1 << 24) || p->B > (1 << 20))
     return SD_EUNSUPPORTED;
+  // a grid dimension holds less than 2^32 threads
+  if ((int64_t)p->B * p->W * NT_B > UINT32_MAX) return SD_EUNSUPPORTED;
   return SD_OK;
 }
 

@@ -348,7 +348,9 @@ int check(const sd_tree_verify_args_t* p) {
   if (p->B < 1 || p->N < 1 || p->V < 1 || p->max_nodes < 1 || p->ld < p->V || (p->ld * es) % 16 ||
       (p->flags & ~(uint32_t)SD_NO_BONUS))
     return SD_EINVAL;
-  if (p->max_nodes > SD_MAX_NODES || p->V >= (1 << 28) || p->N > (1 << 24) || p->B > 65535) return SD_EUNSUPPORTED;
+  if (p->max_nodes > SD_MAX_NODES || p->V >= (1 << 28) || p->B > 65535) return SD_EUNSUPPORTED;
+  // a grid dimension holds less than 2^32 threads
+  if ((int64_t)p->N * NT_A > UINT32_MAX) return SD_EUNSUPPORTED;
   return SD_OK;
 }
 

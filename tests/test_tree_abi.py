@@ -195,6 +195,24 @@ def test_reorder_sizes_beyond_the_limits_are_refused(sdv):
     assert _call(sdv, "reorder", a) == -4
 
 
+@pytest.mark.parametrize("kind,sizes,code", [
+    ("select", dict(B=1 << 18, W=64), -4), ("select", dict(B=(1 << 18) - 1, W=64), 0), ("select", dict(B=1 << 20, W=16), -4),
+    ("select", dict(B=1 << 20, W=15), 0), ("select", dict(B=(1 << 20) + 1, W=1), -4),
+    ("verify", dict(N=1 << 24, V=3, ld=8), -4), ("verify", dict(N=(1 << 24) - 1, V=3, ld=8), 0),
+    ("verify", dict(N=1 << 24, V=1000), -4)])
+def test_grids_beyond_the_hardware_are_refused(sdv, kind, sizes, code):
+    """A grid dimension holds less than 2^32 threads: what would pass that is
+    refused with the sizes, not at the launch."""
+    a = MAKE[kind]()
+    for k, v in sizes.items():
+        setattr(a, k, v)
+    n = ctypes.c_size_t()
+    f = sdv.lib.sd_beam_select_workspace_bytes if kind == "select" else sdv.lib.sd_tree_verify_workspace_bytes
+    assert f(ctypes.byref(a), ctypes.byref(n)) == code
+    if code:
+        assert _call(sdv, kind, a) == code
+
+
 @pytest.mark.parametrize("kind", ["verify", "select", "evict"])
 def test_missing_outputs_and_small_workspaces_are_refused(sdv, kind):
     assert _call(sdv, kind, MAKE[kind](), out=None) == -1
