@@ -720,7 +720,8 @@ Plan plan(const sd_kv_cache_t& c, int rows) {
   p.segments = (int64_t)c.B * c.H_kv * p.mts_max;
   p.tiles = ((int64_t)c.max_pages * c.page_size + S::KT - 1) / S::KT + 1;
   p.fits = p.segments <= 0x7FFFFFFF / p.tiles;      // units are counted in 32 bits
-  p.whole = p.tiles <= WHOLE_TILES;
+  // (and a grid dimension holds less than 2^32 threads)
+  p.whole = p.tiles <= WHOLE_TILES && p.segments * S::NT <= UINT32_MAX;
   return p;
 }
 

@@ -213,6 +213,17 @@ def test_grids_beyond_the_hardware_are_refused(sdv, kind, sizes, code):
         assert _call(sdv, kind, a) == code
 
 
+def test_short_tables_of_very_many_heads_are_split(sdv):
+    """One workgroup per (request, KV head, row tile) needs no workspace; where
+    these pass a grid dimension the work is cut into runs instead."""
+    n = ctypes.c_size_t()
+    for heads, whole in ((8, True), (255, True), (2048, False)):
+        a = _attention()
+        a.cache.B, a.cache.H_kv, a.H_q, a.cache.page_size, a.cache.max_pages = 65535, heads, heads, 16, 1
+        assert sdv.lib.sd_tree_attention_workspace_bytes(ctypes.byref(a), ctypes.byref(n)) == 0
+        assert (n.value == 0) == whole, heads
+
+
 @pytest.mark.parametrize("kind", ["verify", "select", "evict"])
 def test_missing_outputs_and_small_workspaces_are_refused(sdv, kind):
     assert _call(sdv, kind, MAKE[kind](), out=None) == -1
