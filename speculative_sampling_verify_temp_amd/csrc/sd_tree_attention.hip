@@ -192,7 +192,7 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
     const auto [total, per] = cut_units<S::RT, S::KT>(a, rq, runs);
     run = (int)(blockIdx.x % 8) * (runs / 8) + (int)(blockIdx.x / 8);      // runs is a multiple of 8
     if ((int64_t)run * per >= total) return;
-    u0 = run * per, u1 = min(total, u0 + per);
+    u0 = run * per, u1 = u0 + min(per, total - u0);      // (u0 + per may pass 31 bits)
   }
 
   // the request (lane f of this 64) that holds unit u0, and its units before
