@@ -214,8 +214,8 @@ int sd_cache_commit(const sd_cache_commit_args_t *args, int32_t *out_context,
                     uint32_t *out_status, void *stream);
 
 /* ------------------------------------------------------------------------
- * Eviction.  Every KV head of request b keeps min(context_lens[b], budget)
- * of its slots: first those of positions < sinks or >= seen[b] - recent, then
+ * Eviction.  Every KV head of request b (B * H_kv < 2^31) keeps
+ * min(context_lens[b], budget) of its slots: first those of positions < sinks or >= seen[b] - recent, then
  * those of the largest mass (a NaN counts as -inf), the lower slot first among
  * equals.  The kept slots end up as slots 0 .. budget - 1: those below the
  * budget stay, and the j-th kept slot at or past it moves (keys, values, mass,

@@ -522,6 +522,7 @@ int check(const sd_cache_evict_args_t* p) {
       p->ld_mass < (int64_t)p->cache.max_pages * p->cache.page_size)
     return SD_EINVAL;
   if (p->positions_in ? !p->seen : (p->recent || p->sinks)) return SD_EINVAL;
+  if ((int64_t)p->cache.B * p->cache.H_kv > INT32_MAX) return SD_EUNSUPPORTED;      // heads are counted in 32 bits
   return SD_OK;
 }
 

@@ -224,6 +224,17 @@ def test_short_tables_of_very_many_heads_are_split(sdv):
         assert (n.value == 0) == whole, heads
 
 
+def test_evictions_of_more_heads_than_31_bits_count_are_refused(sdv):
+    n = ctypes.c_size_t()
+    for heads, code in ((32768, 0), (32769, -4), (65535, -4)):
+        a = _evict()
+        a.cache.B, a.cache.H_kv, a.cache.page_size, a.cache.max_pages = 65535, heads, 1, 1
+        a.budget, a.recent, a.sinks = 1, 0, 0
+        assert sdv.lib.sd_cache_evict_workspace_bytes(ctypes.byref(a), ctypes.byref(n)) == code, heads
+        if code:
+            assert _call(sdv, "evict", a) == code
+
+
 @pytest.mark.parametrize("kind", ["verify", "select", "evict"])
 def test_missing_outputs_and_small_workspaces_are_refused(sdv, kind):
     assert _call(sdv, kind, MAKE[kind](), out=None) == -1
