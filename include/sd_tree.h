@@ -223,7 +223,7 @@ int sd_cache_commit(const sd_cache_commit_args_t *args, int32_t *out_context,
  * order of the slots, so only displaced rows are read and written.
  * mass_out and positions_out are written for the slots kept; they may be
  * mass_in and positions_in.  out_context[b] = min(context_lens[b], budget).
- * positions NULL: sinks = recent = 0.  An invalid request is left as it was.
+ * positions NULL: sinks = recent = 0, no slot comes first.  An invalid request is left as it was.
  * A bad page's slots are ranked like the others, and their masses and positions
  * move like the others', but their keys and values are neither read nor written:
  * the place that such a row would move to keeps the row that it held, under the

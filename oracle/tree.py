@@ -114,7 +114,7 @@ def commit_weights_ref(q, lse, k_new, k_cache, table_row, ctx, rows, h, scale):
 def evict_ref(mass, positions, n, seen, budget, recent, sinks):
     """(source slot of each of the slots kept, in their new order)."""
     def rank(t):
-        if positions is not None and (positions[t] < sinks or (recent > 0 and positions[t] >= seen - recent)):
+        if positions is not None and (positions[t] < sinks or positions[t] >= seen - recent):
             return (0, 0.0, t)
         return (1, math.inf if math.isnan(mass[t]) else -float(mass[t]), t)
     kept = set(sorted(range(n), key=rank)[:budget])

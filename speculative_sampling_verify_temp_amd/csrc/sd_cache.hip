@@ -304,8 +304,7 @@ __global__ __launch_bounds__(NT_E) void k_evict_select(EvictArgs a) {
     if (tid == 0) a.count[bh] = 0;
     return;
   }
-  const int recent_from = a.pos_in && a.recent > 0
-      ? (int)max((int64_t)a.seen[b] - a.recent, (int64_t)INT_MIN) : INT_MAX;
+  const int recent_from = a.pos_in ? (int)max((int64_t)a.seen[b] - a.recent, (int64_t)INT_MIN) : INT_MAX;
   const bool held = n <= LCAP;
   auto key = [&](int t) { return held ? keys[t] : evict_key(a, row, t, recent_from); };
 

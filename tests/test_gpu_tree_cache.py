@@ -329,6 +329,31 @@ def test_evict_matches_the_oracle(lens, H, D, page, budget, recent, sinks, kind)
            dtype="f16" if H == 2 else "bf16", in_place=kind in ("ties", "odd"))
 
 
+@pytest.mark.parametrize("n", [70, 5000])
+@pytest.mark.parametrize("recent,sinks", [(0, 0), (0, 2), (3, 1), (20, 0)])
+def test_evict_protects_positions_at_or_past_seen(n, recent, sinks):
+    """`seen` before it counts the last eight tokens; with and without a window of
+    recent ones, and with more protected slots than the budget."""
+    import torch
+    rng = np.random.default_rng(n + recent)
+    H, page = 2, 16
+    c = Cached(324, [n], [1], H, H, 64, page, "bf16")
+    L = c.table.shape[1] * page
+    pos = np.zeros((1, H, L), dtype=np.int32)
+    for h in range(H):
+        pos[0, h, :n] = rng.permutation(n)
+    mass = rng.random((1, H, L)).astype(np.float32)
+    mass[pos >= n - 8] = -1.0                     # the just appended: no weight yet
+    for budget in (24, 40):
+        m, p, out = dev(mass), dev(pos), torch.zeros(1, dtype=torch.int32, device="cuda")
+        _sdv().cache_evict(c.d["k_cache"], c.d["v_cache"], c.d["page_table"], c.d["context_lens"], m, m, p, p,
+                           dev(np.array([n - 8], np.int32)), out, budget, recent, sinks)
+        for h in range(H):
+            src = oracle.evict_ref(mass[0, h], pos[0, h], n, n - 8, budget, recent, sinks)
+            assert p[0, h, :budget].tolist() == [int(pos[0, h, s]) for s in src], (h, budget)
+            assert set(range(n - 8, n)) <= set(p[0, h, :budget].tolist()) or recent + sinks + 8 > budget
+
+
 def test_evict_without_positions_and_with_bad_pages():
     import torch
     sdv = _sdv()

@@ -126,6 +126,13 @@ def test_eviction_protects_positions():
     assert src == [4, 1, 5]
 
 
+def test_eviction_protects_what_is_at_or_past_seen_also_without_a_recent_window():
+    """Tokens just appended, before `seen` counts them."""
+    pos = np.array([0, 1, 2, 3, 10, 11])
+    assert oracle.evict_ref(np.array([9.0, 8, 7, 6, 0, 0]), pos, 6, 10, 3, 0, 0) == [0, 4, 5]
+    assert oracle.evict_ref(np.array([9.0, 8, 7, 6, 0, 0]), pos, 6, 12, 3, 0, 0) == [0, 1, 2]
+
+
 def test_beam_against_a_full_sort():
     rng = np.random.default_rng(6)
     z, s = rng.standard_normal((3, 11)), rng.standard_normal(3)
