@@ -468,7 +468,8 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
         } else {
           uint64_t on[MT];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) on[m] = tree ? valid & vis[m] >> (kg * S::KEYS) : valid;
+          for (int m = 0; m < MT; ++m)      // (the tree's 64 nodes are in the first groups' keys)
+            on[m] = !tree ? valid : S::KT <= 64 || kg * S::KEYS < 64 ? valid & vis[m] >> (kg * S::KEYS) : 0;
           tile(std::true_type{}, on);
         }
         if (RG == 1) __builtin_amdgcn_wave_barrier();
