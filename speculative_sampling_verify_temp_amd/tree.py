@@ -301,8 +301,11 @@ def _logits(t, name):
     if V > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the logits of a row must be contiguous")
     ld = t.stride(-2)
-    if t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * ld:
-        raise ValueError(f"{name} must have its rows back to back")
+    if t.dim() == 3 and t.shape[0] > 1:
+        if t.shape[1] == 1:      # the stride of an axis of one says nothing
+            ld = t.stride(0)
+        elif t.stride(0) != t.shape[1] * ld:
+            raise ValueError(f"{name} must have its rows back to back")
     rows = t.numel() // max(1, V)
     return t.data_ptr(), (ld if rows > 1 else max(ld, V)), code
 

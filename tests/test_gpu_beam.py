@@ -159,6 +159,18 @@ def test_rows_of_nothing_but_masks_are_uniform(dtype):
     assert np.abs(s[par == 1] + math.log(V)).max() < 1e-5
 
 
+def test_single_beams_of_any_layout():
+    """[B][1][V] logits made of padded rows and of the last position of each request."""
+    import torch
+    rng = np.random.default_rng(14)
+    z = rounded(rng.standard_normal((5, 3, 1001)) * 3, "f32")
+    x = torch.full((5, 3, 1004), float("nan"), device="cuda")
+    x[..., :1001] = dev(z, torch.float32)
+    sc = -rng.random((5, 1)).astype(np.float32)
+    assert _check(z[:, 2:], sc, 4, _sdv().beam_select(x[:, -1:, :1001], dev(sc), 4)) == 20
+    assert _check(z[:, 1:2], sc, 4, _sdv().beam_select(x[:, 1, :1001].unsqueeze(1), dev(sc), 4)) == 20
+
+
 def test_ended_inactive_and_bad_beams():
     import torch
     sdv = _sdv()

@@ -251,6 +251,24 @@ def test_outputs_that_may_not_be_inputs_are_refused(sdv):
     assert _call(sdv, "select", _select(), out=P(0x200000)) == -1         # the scores
 
 
+def test_rows_of_logits_however_their_axes_came_about():
+    """The row stride of logits, whatever an axis of one says of itself."""
+    import torch
+    rows = lambda t: _tree()._logits(t, "logits")[1]  # noqa: E731
+    x = torch.zeros(6, 1008)
+    assert rows(x) == 1008 and rows(x[:, :1000]) == 1008
+    y = x[:, :1000]
+    assert rows(y.unsqueeze(1)) == rows(y.unsqueeze(0)) == rows(y.reshape(6, 1, 1000).contiguous()) + 8 == 1008
+    assert rows(y.view(2, 3, 1000)) == 1008
+    z = torch.zeros(4, 7, 1008)
+    assert rows(z[:, -1:]) == rows(z[:, -1:, :1000]) == 7 * 1008       # the last position of each request
+    assert rows(z[:, -1]) == 7 * 1008
+    assert rows(z[:1, 2:5]) == 1008 and rows(z[3:, 6:]) == 1008
+    for bad in (z[:, :3], z.transpose(0, 1), x[:, ::2]):
+        with pytest.raises(ValueError):
+            rows(bad)
+
+
 def test_the_binding_refuses_what_it_can_see(sdv):
     """Tensors that are not on the current GPU, wrong types, shapes and
     strides raise before any call (CPU tensors here)."""
