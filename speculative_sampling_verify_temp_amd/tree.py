@@ -485,12 +485,12 @@ def beam_reorder(state, parents, lengths=None, out=None, stream=None):
     strides = []
     for t in (state, dst):
         s = t.stride()
-        want = unit
-        for n, step in zip((*shape[5:], 1), s[4:]):
-            if step * es != want:
+        want = es
+        for n, step in zip(shape[:3:-1], s[:3:-1]):
+            if n > 1 and step * es != want:      # (the stride of an axis of one says nothing)
                 raise ValueError("the units of a state row must be contiguous")
-            want //= max(1, n)
-        strides += [step * es for step in s[:4]]
+            want *= n
+        strides += [step * es if n > 1 else 0 for n, step in zip(t.shape, s[:4])]
     a = _BEAM_REORDER.pack(state.data_ptr(), dst.data_ptr(), *strides,
                            _plain(parents, torch.int32, "parents", (B, W_out)),
                            0 if lengths is None else _plain(lengths, torch.int32, "lengths", (B,)), unit,

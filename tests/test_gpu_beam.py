@@ -262,6 +262,26 @@ def test_reorder_is_a_gather(layers, B, W, segs, L, E, in_place):
             assert np.array_equal(src.cpu().numpy(), x)
 
 
+def test_reorder_whatever_axes_of_one_say():
+    """States with a single unit, layer, beam or segment whose strides come from
+    other shapes."""
+    import torch
+    rng = np.random.default_rng(10)
+    x = rng.integers(-9, 9, (2, 3, 4, 1, 5, 8)).astype(np.int16)
+    par = rng.integers(0, 4, (3, 4)).astype(np.int32)
+    for view in (lambda t: t.transpose(3, 4), lambda t: t.as_strided(t.shape, (480, 160, 40, 7, 8, 1)),
+                 lambda t: t[:1].as_strided((1, *t.shape[1:]), (3, 160, 40, 40, 8, 1)),
+                 lambda t: t[:, :, :, :, :1].as_strided((2, 3, 4, 1, 1, 8), (480, 160, 40, 40, 5, 1))):
+        t = dev(x)
+        want = t.clone()
+        w = view(want)
+        w.copy_(w.clone()[:, torch.arange(3, device="cuda")[:, None], dev(par).long()])
+        _sdv().beam_reorder(view(t), dev(par))
+        assert torch.equal(t, want)
+    with pytest.raises(ValueError):
+        _sdv().beam_reorder(dev(x).transpose(4, 5), dev(par))
+
+
 def test_reorder_of_strided_states():
     """Beams that are not the outermost rows: [B][W][layers][segs] in memory."""
     import torch
