@@ -179,6 +179,11 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
   // scores in base 2; a negative scale is in the queries' signs, and one of zero
   // stays above it so that a masked score times it is still -inf
   const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+  // Weights are taken against a reference `LIFT` below the running maximum, which
+  // may grow by 8 before it moves: fp16 weights lie below 2^15 and keep their
+  // precision down to 2^-21 of the largest, something down to 2^-32 of it (a long
+  // context's tail beside one dominating key).  bf16 has fp32's exponents.
+  constexpr float LIFT = DT == SD_F16 ? 7.0f : 0.0f;
 
   Requests rq = requests<S::RT, S::KT>(a, l);
   int run, u0, u1;
@@ -381,9 +386,9 @@ __global__ __launch_bounds__(S::NT, 2) void k_attn_tiles(AttnArgs a) {
                 x[s][m][r] = (mine >> (s * 16 + r) & 1) ? x[s][m][r] : -INFINITY;
               top[m] = fmaxf(top[m], x[s][m][r]);
             }
-          top[m] = quad_max(top[m]) * c;
+          top[m] = quad_max(top[m]) * c - LIFT;
           // the sums are rescaled only when a maximum grows by more than 2^8:
-          // until then weights up to 2^8 are as exact as those below 1
+          // until then weights up to 2^8 (2^15) are as exact as those below
           grown |= top[m] > mx[m] + 8.0f;
         }
         if (__any(grown)) {

@@ -124,6 +124,48 @@ def test_queries_and_keys_of_large_scores():
         c.check_attention(*_run(c), c.reference())
 
 
+@pytest.mark.parametrize("below", [14.0, 20.0, 26.0])
+@pytest.mark.parametrize("Hq,T", [(2, 1), (8, 9), (8, 64)])
+def test_small_weights_of_many_keys_beside_a_dominating_one(Hq, T, below):
+    """fp16: a first key that every query likes, its value zero, and 30000 keys
+    whose weights are 2^-below of its weight each and carry all of the result."""
+    import torch
+    n, page, H, D = 30000, 64, 2, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    k = (torch.randn((-(-n // page), H, page, D), generator=g, device="cuda") * 0.05).half()
+    v = (torch.randn(k.shape, generator=g, device="cuda") + 3.0).half()
+    k[:, :, :, 0] = 0.0
+    k[0, :, 0, 0], v[0, :, 0] = 8.0, 0.0
+    q = (torch.randn((T, Hq, D), generator=g, device="cuda")).half()
+    q[:, :, 0] = below * 0.6931 / 8.0 * D ** 0.5
+    kn, vn = torch.zeros((T, H, D), device="cuda").half(), torch.zeros((T, H, D), device="cuda").half()
+    kn[:, :, 0], kn[:, :, 1] = -8.0, 0.0
+    table = torch.arange(k.shape[0], dtype=torch.int32, device="cuda")[None].contiguous()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    print(f"tail {Hq} {T} {below}", flush=True)
+    out, lse = _sdv().tree_attention(q, kn, vn, k, v, table, lens, off, T, want_lse=True)
+    for head in range(Hq):
+        h = head * H // Hq
+        kk, vv = (x[:, h].reshape(-1, D)[:n].double() for x in (k, v))
+        x = torch.cat([q[:, head].double() @ kk.t(), q[:, head].double() @ kn[:, h].double().t()], 1) * D ** -0.5
+        x[:, n:][torch.ones((T, T), device="cuda").triu(1).bool()] = float("-inf")
+        p = torch.softmax(x, 1)
+        vv = torch.cat([vv, vn[:, h].double()])
+        o, mag = p @ vv, p @ vv.abs()
+        # half a step for the result; each weight w of the largest one is off by
+        # half a step, 2^-11 w, or 2^-25 of the scale 2^7 that weights are held at;
+        # the scores by (D + 4) 2^-24 of the sum of magnitudes (under 30), the
+        # exponent's argument by 2^-24 of its own; fp32 sums of n terms by n 2^-24
+        scores = (2 * 68 * 30 + 60) * 2.0 ** -24
+        tol = 2.0 ** -11 * o.abs() + (2.0 ** -11 + scores + n * 2.0 ** -24) * 1.01 * mag \
+            + 2.0 ** -32 * p.amax(1, keepdim=True) * vv.abs().sum(0) + 2.0 ** -25
+        err = (out[:, head].double() - o).abs()
+        assert (err <= tol).all(), (head, (err / o.abs()).max())
+        assert ((lse[:, head].double() - torch.logsumexp(x, 1)).abs() <= scores + n * 2.0 ** -24 + 2e-5).all()
+
+
 def test_bad_pages_lengths_and_nodes_are_reported():
     sdv = _sdv()
     c = Cached(11, [100, 100, 100, 100], [4, 4, 4, 4], 8, 2, 128, 16, "bf16", behind=5)
