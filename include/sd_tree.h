@@ -18,7 +18,10 @@
  * asynchronous work on `stream`, host-checkable errors by return code,
  * data-dependent ones per request in out_status, no memory allocated,
  * workspaces that need no initialization and are not shared by calls that
- * overlap in time).  The device that owns the pointers is the current one.
+ * overlap in time).  The device that owns the pointers is the current one.  An
+ * output overlaps no input, no other output and not the workspace, except where
+ * an operator says so; the same pointer for both is refused where that would
+ * change results.
  *
  * Trees.  Request b has the nodes node_offsets[b] .. node_offsets[b + 1] - 1
  * of the packed node arrays, at most max_nodes (<= SD_MAX_NODES) of them.
@@ -102,7 +105,7 @@ typedef struct sd_kv_cache {
  * whatever they hold.  Rows of a request of wrong length get zeros and -inf;
  * rows of one whose node offsets are wrong, and rows of packed nodes that belong
  * to no request, are left as they were.
- * out [N][H_q][D] and out_lse [N][H_q] are contiguous.
+ * out [N][H_q][D] and out_lse [N][H_q] are contiguous; out may be q where q is.
  * ------------------------------------------------------------------------ */
 typedef struct sd_tree_attention_args {
   sd_kv_cache_t   cache;
@@ -179,7 +182,7 @@ int sd_tree_verify_greedy(const sd_tree_verify_args_t *args, void *workspace,
  * read.  lse is what sd_tree_attention gave for these rows; one of -inf (the row
  * saw nothing) makes its row add no weight.  A slot of a bad
  * page has w = 0; an appended slot on one is not written.  mass_in may be
- * mass_out.  out_context must not be context_lens.  An invalid request appends
+ * mass_out.  An invalid request appends
  * nothing: its mass and positions stay and out_context[b] = context_lens[b].
  * The pages that hold the appended slots belong to one request only.
  * ------------------------------------------------------------------------ */

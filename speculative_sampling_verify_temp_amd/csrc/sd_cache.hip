@@ -536,7 +536,9 @@ extern "C" int sd_cache_commit(const sd_cache_commit_args_t* args, int32_t* out_
                                uint32_t* out_status, void* stream) {
   const int rc = check(args);
   if (rc) return rc;
-  if (!out_context || out_context == args->cache.context_lens) return SD_EINVAL;
+  if (!out_context) return SD_EINVAL;
+  for (const int32_t* in : {args->cache.context_lens, args->node_offsets, args->path, args->path_lens, args->seen})
+    if (out_context == in) return SD_EINVAL;
   CommitArgs a{};
   a.c = device_cache(args->cache);
   a.kn = static_cast<const char*>(args->k_new);

@@ -772,6 +772,11 @@ extern "C" int sd_tree_attention(const sd_tree_attention_args_t* args, void* wor
   int rc = sd_tree_attention_workspace_bytes(args, &need);
   if (rc) return rc;
   if (!out || !aligned16(out)) return SD_EINVAL;
+  if (out == args->k_new || out == args->v_new || out == args->cache.k || out == args->cache.v) return SD_EINVAL;
+  // a query row is read by the workgroups of its own result alone, before they
+  // write it or before the join does
+  if (out == args->q && (args->q_head != args->cache.D || args->q_node != (int64_t)args->H_q * args->cache.D))
+    return SD_EINVAL;
   if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return SD_EWORKSPACE;
   AttnArgs a = device_args(args);
   a.out = static_cast<char*>(out);

@@ -412,6 +412,8 @@ extern "C" int sd_debug_tree_verify_polls(const sd_tree_verify_args_t* args, voi
   const int rc = sd_tree_verify_workspace_bytes(args, &need);
   if (rc) return rc;
   if (!out_accepted || !out_path || !out_tokens) return SD_EINVAL;
+  for (const int32_t* in : {args->tokens, args->parents, args->node_offsets})
+    if (out_accepted == in || out_path == in || out_tokens == in) return SD_EINVAL;
   if (!workspace || workspace_bytes < need || (uintptr_t)workspace % 8) return SD_EWORKSPACE;
   const Slices s = slices_of(args);
   VerifyArgs a;

@@ -247,6 +247,16 @@ def test_interleaved_caches_and_wide_tables():
     c.check_attention(*_run(c), c.reference())
 
 
+@pytest.mark.parametrize("lens,nodes", [([40, 7], [64, 3]), ([3000, 0, 900], [9, 64, 17]), ([9000], [2])])
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 64), (28, 4, 128), (32, 1, 64)])
+def test_results_in_place_of_the_queries(lens, nodes, Hq, Hkv, D):
+    import torch
+    c = Cached(20, lens, nodes, Hq, Hkv, D, 16, "bf16")
+    want, lse = _run(c)
+    got, e = _run(c, out=c.d["q"])
+    assert got.data_ptr() == c.d["q"].data_ptr() and torch.equal(got, want) and torch.equal(e, lse)
+
+
 def test_two_streams_at_once():
     """Calls on two streams with workspaces of their own."""
     import torch

@@ -269,6 +269,28 @@ def test_rows_of_logits_however_their_axes_came_about():
             rows(bad)
 
 
+@pytest.mark.parametrize("kind,inputs", [
+    ("attention", ("k_new", "v_new")), ("verify", ("tokens", "parents", "node_offsets")),
+    ("commit", ("node_offsets", "path", "path_lens", "seen"))])
+def test_an_output_that_is_an_input_is_refused(sdv, kind, inputs):
+    """Other workgroups still read it while its first results are written."""
+    for field in inputs:
+        a = MAKE[kind]()
+        assert _call(sdv, kind, a, out=P(getattr(a, field))) == -1, field
+    if kind == "attention":
+        for field in ("k", "v"):
+            a = MAKE[kind]()
+            assert _call(sdv, kind, a, out=P(getattr(a.cache, field))) == -1, field
+        for field, value in (("q_node", 1032), ("q_head", 136), ("q_head", 0)):      # rows of others' queries
+            a = MAKE[kind]()
+            setattr(a, field, value)
+            assert _call(sdv, kind, a, out=P(a.q)) == -1, field
+    if kind == "verify":
+        a = MAKE[kind]()
+        for outs in ((OUT, P(a.tokens), P(0x910000)), (OUT, P(0x910000), P(a.parents))):
+            assert sdv.lib.sd_tree_verify_greedy(ctypes.byref(a), P(0xA00000), 1 << 40, *outs, None, None) == -1
+
+
 def test_the_binding_refuses_what_it_can_see(sdv):
     """Tensors that are not on the current GPU, wrong types, shapes and
     strides raise before any call (CPU tensors here)."""
