@@ -231,7 +231,8 @@ int sd_cache_commit(const sd_cache_commit_args_t *args, int32_t *out_context,
  * move like the others', but their keys and values are neither read nor written:
  * the place that such a row would move to keeps the row that it held, under the
  * mass and position of the other.  So a request reported with SD_ST_BAD_PAGE has
- * a cache that is no longer that of its tokens.  The request's pages are its own.
+ * a cache that is no longer that of its tokens.  The request's pages are its own,
+ * and so are each head's rows of a page: strides of 0 are refused.
  * ------------------------------------------------------------------------ */
 typedef struct sd_cache_evict_args {
   sd_kv_cache_t  cache;
@@ -291,7 +292,8 @@ int sd_beam_select(const sd_beam_select_args_t *args, void *workspace,
  * Where out is in (the same pointer; W_in = W_out and equal strides), the rows are
  * permuted in place; otherwise the two must not overlap.  A parent outside
  * [0, W_in) leaves its row as it was.  Units past the length are left as they
- * were.  unit_bytes and all strides are multiples of 16, pointers 16-byte
+ * were.  No two rows of out share memory (strides of 0 are refused; in may be
+ * broadcast).  unit_bytes and all strides are multiples of 16, pointers 16-byte
  * aligned; W_in, W_out <= SD_MAX_BEAMS, B and layers * segs <= 65535. */
 typedef struct sd_beam_reorder_args {
   const void    *in;

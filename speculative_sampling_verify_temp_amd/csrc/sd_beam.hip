@@ -501,6 +501,10 @@ extern "C" int sd_beam_reorder(const sd_beam_reorder_args_t* p, void* stream) {
                              p->out_request, p->out_beam, p->out_seg, p->unit_bytes};
   for (int64_t s : strides)
     if (s < 0 || s % 16) return SD_EINVAL;
+  // rows of out that share their memory
+  if ((p->out_layer == 0 && p->layers > 1) || (p->out_request == 0 && p->B > 1) ||
+      (p->out_beam == 0 && p->W_out > 1) || (p->out_seg == 0 && p->segs > 1))
+    return SD_EINVAL;
   if (p->in == p->out && (p->W_in != p->W_out || p->in_layer != p->out_layer ||
                           p->in_request != p->out_request || p->in_beam != p->out_beam ||
                           p->in_seg != p->out_seg))

@@ -521,6 +521,9 @@ int check(const sd_cache_evict_args_t* p) {
       p->ld_mass < (int64_t)p->cache.max_pages * p->cache.page_size)
     return SD_EINVAL;
   if (p->positions_in ? !p->seen : (p->recent || p->sinks)) return SD_EINVAL;
+  // heads or pages that share their memory cannot be cut apart
+  if ((p->cache.head_stride == 0 && p->cache.H_kv > 1) || (p->cache.page_stride == 0 && p->cache.num_pages > 1))
+    return SD_EINVAL;
   if ((int64_t)p->cache.B * p->cache.H_kv > INT32_MAX) return SD_EUNSUPPORTED;      // heads are counted in 32 bits
   return SD_OK;
 }

@@ -282,6 +282,18 @@ def test_reorder_whatever_axes_of_one_say():
         _sdv().beam_reorder(dev(x).transpose(4, 5), dev(par))
 
 
+def test_reorder_of_a_broadcast_state():
+    """One prompt's state for all requests and beams, spread into their own."""
+    rng = np.random.default_rng(15)
+    x = rng.integers(-9, 9, (2, 1, 1, 2, 10, 8)).astype(np.int16)
+    par = np.zeros((3, 4), dtype=np.int32)
+    old = dev(np.full((2, 3, 4, 2, 10, 8), 5, dtype=np.int16))
+    got = _sdv().beam_reorder(dev(x).expand(2, 3, 2, 2, 10, 8), dev(par), dev(np.array([10, 3, 0], np.int32)), out=old)
+    want = np.full((2, 3, 4, 2, 10, 8), 5, dtype=np.int16)
+    want[:, 0], want[:, 1, :, :, :3] = x[:, 0], x[:, 0, :, :, :3]
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_reorder_of_strided_states():
     """Beams that are not the outermost rows: [B][W][layers][segs] in memory."""
     import torch

@@ -291,6 +291,19 @@ def test_an_output_that_is_an_input_is_refused(sdv, kind, inputs):
             assert sdv.lib.sd_tree_verify_greedy(ctypes.byref(a), P(0xA00000), 1 << 40, *outs, None, None) == -1
 
 
+def test_rows_that_share_memory_are_not_written(sdv):
+    """Expanded caches and states: the rows of one would be written over another's."""
+    for field in ("head_stride", "page_stride"):
+        a = _evict()
+        setattr(a.cache, field, 0)
+        assert _call(sdv, "evict", a) == -1, field
+    for field in ("layer", "request", "beam", "seg"):
+        a = _reorder()
+        setattr(a, "in_" + field, 0)
+        setattr(a, "out_" + field, 0)
+        assert _call(sdv, "reorder", a) == -1, field
+
+
 def test_the_binding_refuses_what_it_can_see(sdv):
     """Tensors that are not on the current GPU, wrong types, shapes and
     strides raise before any call (CPU tensors here)."""
