@@ -93,9 +93,10 @@ __device__ __forceinline__ float logit_of(const uint4& w, int e) {
   return __uint_as_float(q[e]);
 }
 
-// A logit is read once and its exponential costs about 7 issue slots; with the
-// bound and the list the vector ALU is the limit: 27 us for 256 rows of 152064
-// bf16 logits, a fifth of them ended (62 MB, 2.3 TB/s).  Slices of 4 vectors a
+// A logit is read once and its exponential costs about 8 issue slots; with the
+// bound and the list, which every slice makes anew, the vector ALU is the limit:
+// 26.6 us for 256 rows of 152064 bf16 logits, a fifth of them ended (62 MB, 2.3
+// TB/s).  Slices of 4 vectors a
 // thread beat 8 (34 against 36 us: more workgroups a CU hide the two
 // synchronizations).
 template <int DT>

@@ -104,8 +104,8 @@ __device__ void append(const CommitArgs& a, const Branch& r, int b, int h) {
 // at a time from LDS: S = Q . K^T, so a lane holds 4 rows of one key and the
 // sum over the rows is in its own registers but for two lane swaps at the end.
 // The keys are read once; row blocks past the first are staged again for every
-// tile.  Bound by HBM up to about 150 rows: 363 MB of keys and weights in 85 us
-// (4.3 TB/s) for 32 requests of 5k to 16k slots, 4 KV heads and up to 42 rows.
+// tile.  Bound by HBM up to about 150 rows: 363 MB of keys and weights in 86 us
+// (4.2 TB/s) for 32 requests of 5k to 16k slots, 4 KV heads and up to 42 rows.
 template <int DT, int D>
 __global__ __launch_bounds__(NT_C, 2) void k_commit(CommitArgs a, int chunk) {
   constexpr int KS = D / 32, CPR = D / 8;
@@ -568,7 +568,10 @@ extern "C" int sd_cache_commit(const sd_cache_commit_args_t* args, int32_t* out_
   }
   // Slots of a workgroup: 256 (one tile) unless that makes more than about
   // 1024 workgroups, since each stages the query rows anew (32 requests of 5k to
-  // 16k slots: 85 us, 88 with 2048, 97 with 4096).
+  // 16k slots: 86 us, 3 % more with 2048, 13 % with 4096).  The lengths are not
+  // known here, so the table's room is what is cut: where most of it is unused,
+  // the slots in use lie in few workgroups (the same requests in tables of 32768
+  // slots 227 us, of 131072 597 us).
   const int64_t tiles = (a.c.cap + NT_C - 1) / NT_C;
   const int64_t per = std::max<int64_t>(1, std::min(tiles, tiles * a.c.H * a.c.B / 1024));
   const int chunk = (int)per * NT_C;

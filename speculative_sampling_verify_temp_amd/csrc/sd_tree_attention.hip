@@ -20,13 +20,13 @@
 //                out of LDS transposed (ds_read_b64_tr_b16).  Keys are staged
 //                through registers into swizzled LDS rows, the next tile's
 //                loads in flight behind the products.
-//                Up to about 130 rows a KV head it is bound by HBM (3.2 TB/s
-//                over 32 chains of 9 nodes, 3.8 TB/s over longer contexts: a
-//                run's start and end take as long as 3 of its tiles), past
-//                that by the issue of softmax and products, which overlap
-//                little: 16 trees of 64 nodes over 16k to 32k slots take 476
-//                us, 640 TFLOP/s, with the matrix cores busy 36 %, the vector
-//                ALU 44 % and LDS 34 % of the time.
+//                Up to about 130 rows a KV head it is bound by the latencies of
+//                a run's start and end, as long as 3 of its tiles: 3.2 TB/s over
+//                32 chains of 9 nodes, 3.8 TB/s over longer contexts, where a
+//                copy reaches 4.85.  Past that it is bound by the issue of
+//                softmax and products, which overlap little: 16 trees of 64 nodes
+//                over 16k to 32k slots take 476 us, 640 TFLOP/s, with the matrix
+//                cores busy 37 %, the vector ALU 43 % and LDS 33 % of the time.
 // k_attn_join    one thread per 4 output columns of a split row; latency, 6 to
 //                12 us.
 #include <type_traits>
