@@ -19,6 +19,8 @@ lmhead   The step fed from hidden states through the LM heads: logits as the
          fp64 product of hidden states and head weights, then verify.
 tree    Tree drafting: attention over a paged cache, greedy verify of a tree,
         append and eviction by attention weight, and a beam step.
+serve   A serving step of drafted trees: norms and rotation of queries and keys,
+        an 8-bit cache with its attention, the verify against probabilities.
 
 Parity status of each function is stated in its docstring.  Two readings are
 "parity unpinned" by the pages (the repetition-penalty formula and the top-p
@@ -39,6 +41,10 @@ from .lmhead import lmhead_logits, lmhead_verify_sample_ref, lmhead_verify_greed
 from .tree import (
     visible_nodes, tree_attention_ref, tree_verify_greedy_ref, commit_weights_ref, evict_ref,
     beam_select_ref,
+)
+from .serve import (
+    norm_rope_ref, e4m3_round, quant_scale, quant_codes, quant_append_ref, quant_rows, quant_attention_ref,
+    tree_sample_ref,
 )
 
 __all__ = [n for n in dir() if not n.startswith("_")]

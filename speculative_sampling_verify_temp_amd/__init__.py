@@ -15,7 +15,9 @@ Functions mirror the C entry points:
     debug_process_rows(...), debug_uniforms(...)  (test exports)
 The operators for drafted trees (include/sd_tree.h) are in tree.py and are
 exported here too: tree_attention, tree_verify_greedy, cache_commit,
-cache_evict, beam_select, beam_reorder.
+cache_evict, beam_select, beam_reorder; so are those of a serving step around
+them (include/sd_serve.h, serve.py): qk_norm_rope, quant_attention, quant_append,
+tree_verify_sample.
 """
 import ctypes
 import os
@@ -439,4 +441,8 @@ from .tree import (  # noqa: E402  (needs the loaded library)
     SD_ST_BAD_PATH, SD_ST_BAD_TREE, SD_ST_TREE_INVALID_MASK, SD_ST_UNFINISHED, beam_reorder,
     beam_select, cache_commit, cache_evict, make_tree_attention_args, tree_attention,
     tree_attention_workspace_bytes, tree_verify_greedy,
+)
+from .serve import (  # noqa: E402
+    SD_E4M3, SD_I8, SD_MIN_BLOCK, SD_NO_REPLACEMENT, SD_ST_BAD_SCALE, make_quant_attention_args,
+    qk_norm_rope, quant_append, quant_attention, quant_attention_workspace_bytes, tree_verify_sample,
 )

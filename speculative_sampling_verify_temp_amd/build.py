@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsdverify.so")
 SOURCES = ["sd_verify.hip", "sd_confidence.hip", "sd_lmhead.hip", "sd_tree_attention.hip",
-           "sd_tree_verify.hip", "sd_cache.hip", "sd_beam.hip"]
+           "sd_tree_verify.hip", "sd_cache.hip", "sd_beam.hip", "sd_rope.hip", "sd_quant_cache.hip",
+           "sd_tree_sample.hip", "sd_quant_attention.hip"]
 ARCH = os.environ.get("SDV_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

@@ -1,0 +1,236 @@
+"""sd_quant_attention on the GPU against the fp64 oracle."""
+import numpy as np
+import pytest
+
+from servetools import Quantised, code_dev
+from treetools import dev, random_tree, torch_dtype
+
+pytestmark = pytest.mark.gpu
+
+
+def _sdv():
+    import speculative_sampling_verify_temp_amd as sdv
+    return sdv
+
+
+def _parents(s):
+    return np.concatenate([random_tree(s.rng, n)[:n] for n in s.nodes]).astype(np.int32)
+
+
+def _run(s, parents=None, **kw):
+    return _sdv().quant_attention(**s.attention_args(), max_nodes=max(s.nodes),
+                                  parents=None if parents is None else dev(parents), want_lse=True, **kw)
+
+
+@pytest.mark.parametrize("code,dtype", [("i8", "bf16"), ("i8", "f16"), ("e4m3", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("lens,nodes,Hq,Hkv,D,page,block,tree", [
+    ([517], [1], 14, 2, 64, 16, 16, False), ([1], [1], 4, 1, 128, 16, 16, False), ([0, 0], [3, 1], 4, 2, 64, 16, 16, True),
+    ([15, 16, 17, 127, 128, 129], [1] * 6, 7, 1, 128, 16, 16, False),
+    ([300, 0, 77, 1025], [9, 4, 1, 7], 28, 4, 128, 32, 16, False),
+    ([700, 64, 31], [23, 5, 64], 4, 4, 64, 64, 64, True),
+    ([2000, 999], [64, 33], 14, 2, 64, 128, 32, True),
+    ([1100, 10], [64, 64], 28, 4, 128, 64, 64, True),
+    ([40] * 70, [2] * 70, 2, 1, 64, 16, 16, False), ([3000], [2], 32, 1, 128, 1024, 256, False)])
+def test_rows_match_the_oracle(lens, nodes, Hq, Hkv, D, page, block, tree, code, dtype):
+    s = Quantised(7, lens, nodes, Hq=Hq, Hkv=Hkv, D=D, page=page, block=block, code=code, dtype=dtype, sigma=1.5)
+    parents = _parents(s) if tree else None
+    print(f"attention {lens[:4]} {nodes[:4]} {Hq}/{Hkv} {D} {page}/{block} {code} {dtype}", flush=True)
+    out, lse = _run(s, parents)
+    s.check(out, lse, s.reference(parents))
+
+
+@pytest.mark.parametrize("code,dtype", [("i8", "f16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (2, 1), (5, 0), (17, 40), (130, 4), (513, 200), (700, 129),
+                                          (2 ** 31 - 1, 7)])
+def test_windows_and_sinks(window, sinks, code, dtype):
+    lens, nodes = [1500, 0, 3, 640, 129, 20, 1281], [7, 20, 12, 1, 16, 9, 3]
+    s = Quantised(8, lens, nodes, Hq=8, Hkv=2, D=64, page=32, block=16, code=code, dtype=dtype)
+    for parents in (None, _parents(s)):
+        out, lse = _run(s, parents, window=window, sinks=sinks)
+        s.check(out, lse, s.reference(parents, window, sinks))
+
+
+def test_many_rows_through_a_window():
+    lens, nodes = [4000, 2777, 90], [64, 40, 64]
+    s = Quantised(9, lens, nodes, Hq=14, Hkv=2, D=128, page=64, block=32)
+    parents = _parents(s)
+    out, lse = _run(s, parents, window=1025, sinks=5)
+    s.check(out, lse, s.reference(parents, 1025, 5))
+
+
+def test_what_a_window_hides_is_not_read():
+    """Pages outside the window and the sinks may be gone: their table entries are
+    not followed, and nothing is reported."""
+    import torch
+    s = Quantised(10, [2000, 900], [4, 1], Hq=4, Hkv=2, D=64)
+    ref = s.reference(None, 300, 20)
+    t = s.table.copy()
+    t[0, 2:106] = -5
+    t[1, 2:37] = 10 ** 6
+    s.d["page_table"] = dev(t)
+    st = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    out, lse = _run(s, window=300, sinks=20, status=st)
+    s.check(out, lse, ref)
+    assert st.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_scales_of_any_sign(scale):
+    s = Quantised(11, [200, 33], [5, 2], Hq=4, Hkv=2, D=64, sigma=0.7)
+    out, lse = _run(s, scale=scale)
+    s.check(out, lse, s.reference(scale=scale), scale)
+
+
+def test_scales_far_apart():
+    """Value scales over 2^80: what a token of a small one adds is as exact as its
+    share, and rows that see only small ones are whole."""
+    for D in (64, 128):
+        s = Quantised(12, [96, 48], [3, 2], Hq=4, Hkv=2, D=D)
+        for b, p in enumerate(s.table[:, :6].tolist()):
+            for i, page in enumerate(p):
+                e = [0, 40, -40, 12, -30, 25][i] if b == 0 else -45 - i
+                s.vs[page] = np.float32(2.0) ** e
+        s.d["v_scale"] = dev(s.vs)
+        # the second request's own values would drown its cache's
+        s.vn[3:] *= 0
+        s.d["v_new"] = dev(s.vn, torch_dtype("bf16"))
+        out, lse = _run(s)
+        o, e, mag = s.reference()
+        got = out.double().cpu().numpy()
+        # n weights below 2^-32 of the largest w = p vs each, the rest as elsewhere
+        es = s.score_error()
+        tol = (2.0 ** -8 + 2.0 ** -11 + 2 * es + 200 * 2.0 ** -24) * mag + 160 * 2.0 ** -32 * 128 * mag.max(-1, keepdims=True)
+        assert (np.abs(got - o) <= tol).all()
+        assert (np.abs(lse.double().cpu().numpy() - e) <= es + 2.0 ** -16).all()
+
+
+def test_blocks_of_zeros_and_unsound_scales():
+    import torch
+    sdv = _sdv()
+    s = Quantised(13, [130, 64, 32], [4, 1, 2], Hq=4, Hkv=2, D=64)
+    p = s.table
+    s.ks[p[0, 1], 0] = 0                       # keys of zeros: scores 0
+    s.vs[p[0, 2], 1] = 0                       # values of zeros, whatever the codes
+    s.ks[p[0, 3], 1] = np.nan
+    s.vs[p[0, 5], 0] = np.inf
+    s.vs[p[1, 0], 0] = -1.0
+    s.ks[p[1, 3], 1] = 2.0 ** -51
+    s.d["k_scale"], s.d["v_scale"] = dev(s.ks), dev(s.vs)
+    st = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    out, lse = _run(s, status=st)
+    ref = s.reference()
+    for x in (s.ks, s.vs):
+        x[~(np.abs(x) < 1e6)] = 1.0
+    s.check(out, lse, ref)
+    assert st.tolist() == [sdv.SD_ST_BAD_SCALE, sdv.SD_ST_BAD_SCALE, 0]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_e4m3_codes_that_are_not_numbers_count_as_zero(D):
+    s = Quantised(14, [300, 50], [3, 2], Hq=8, Hkv=2, D=D, code="e4m3", page=32, block=32)
+    p = s.table
+    s.k[p[0, 1], 0, 5, 7] = np.nan
+    s.v[p[0, 4], 1, 30, D - 1] = np.nan
+    s.v[p[1, 0], 0, 0] = np.nan
+    s.d["k_cache"], s.d["v_cache"] = code_dev(s.k, "e4m3"), code_dev(s.v, "e4m3")
+    for window in (0, 40):
+        out, lse = _run(s, window=window)
+        s.check(out, lse, s.reference(None, window))
+
+
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them():
+    import torch
+    s = Quantised(15, [60, 20], [6, 3], Hq=4, Hkv=2, D=64)
+    parents = np.array([-1, 0, 0, 1, 2, 4, -1, 0, 0], dtype=np.int32)
+    ref = s.reference(parents)
+    s.vn[3, 0, 5], s.vn[4, 1, 6] = np.inf, np.nan
+    s.vn[7, 1, 0] = -np.inf
+    s.kn[8, 0, 3] = np.nan
+    s.d["v_new"], s.d["k_new"] = dev(s.vn, torch.bfloat16), dev(s.kn, torch.bfloat16)
+    out, lse = _run(s, parents)
+    o = out.double().cpu().numpy()
+    touched = np.zeros(o.shape, dtype=bool)
+    touched[3, :2, 5] = touched[4, 2:, 6] = touched[5, 2:, 6] = touched[7, 2:, 0] = True
+    assert (o[3, :2, 5] == np.inf).all() and np.isnan(o[4:6, 2:, 6]).all() and (o[7, 2:, 0] == -np.inf).all()
+    assert np.isnan(o[8, :2]).all() and torch.isnan(lse[8, :2]).all()
+    touched[8, :2] = True
+    clean = np.where(touched, ref[0], o)
+    lse = lse.clone()
+    lse[8, :2] = torch.from_numpy(ref[1][8, :2]).float().cuda()
+    s.vn, s.kn = np.nan_to_num(s.vn, posinf=1, neginf=-1), np.nan_to_num(s.kn)
+    s.check(torch.from_numpy(clean), lse, ref)
+
+
+def test_defects_and_rows_of_no_request():
+    import torch
+    sdv = _sdv()
+    s = Quantised(16, [100, 40, 64, 30, 20], [4, 3, 2, 1, 5], Hq=4, Hkv=2, D=64, behind=3)
+    t = s.table.copy()
+    t[0, 1] = -1                                            # bad pages are left out
+    t[2, :4] = 10 ** 6
+    s.table = t
+    s.d["page_table"] = dev(t)
+    parents = np.concatenate([_parents(s), [-1, 0, 0]]).astype(np.int32)
+    parents[s.offsets[4] + 2] = 2                           # its own parent: a root
+    ref_parents = parents.copy()
+    ref = s.reference(ref_parents)
+    ctx = np.array(s.lens, dtype=np.int32)
+    ctx[1] = 10 ** 6
+    s.d["context_lens"] = dev(ctx)
+    st = torch.full((5,), -1, dtype=torch.int32, device="cuda")
+    out = torch.full((s.N + 3, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((s.N + 3, 4), 7.0, device="cuda")
+    _sdv().quant_attention(**s.attention_args(), max_nodes=5, parents=dev(parents), out=out, lse=lse, status=st)
+    assert st.tolist() == [sdv.SD_ST_BAD_PAGE, sdv.SD_ST_BAD_LEN, sdv.SD_ST_BAD_PAGE, 0, sdv.SD_ST_BAD_TREE]
+    assert (out[s.N:] == 7).all() and (lse[s.N:] == 7).all()
+    lo, hi = s.offsets[1], s.offsets[2]
+    assert (out[lo:hi] == 0).all() and (lse[lo:hi] == -np.inf).all()
+    ref[0][lo:hi], ref[1][lo:hi], ref[2][lo:hi] = 0, -np.inf, 0
+    s.check(out, lse, ref)
+    off = np.array([0, 4, 2, 9, 10, 99], dtype=np.int32)    # decreasing, too many, past N
+    st.fill_(-1)
+    out.fill_(7.0)
+    s.d["node_offsets"], s.d["context_lens"] = dev(off), dev(np.array(s.lens, dtype=np.int32))
+    _sdv().quant_attention(**s.attention_args(), max_nodes=5, out=out, status=st)
+    N = sdv.SD_ST_BAD_NODES
+    assert [x & N for x in st.tolist()] == [0, N, N, 0, N]
+    assert (out[4:9] == 7).all() and (out[10:] == 7).all() and not (out[:4] == 7).all()
+
+
+def test_in_place_of_queries_and_strided_caches():
+    import torch
+    for kw in (dict(slot_major=True), dict(packed=True)):
+        s = Quantised(17, [90, 300], [6, 2], Hq=4, Hkv=2, D=128, **kw)
+        out, lse = _run(s)
+        s.check(out, lse, s.reference())
+    q = s.d["q"] = s.d["q"].contiguous()
+    got, lse2 = _run(s, out=q)
+    assert got is q and torch.equal(got, out) and torch.equal(lse, lse2)
+
+
+def test_results_repeat_and_graphs_replay():
+    import torch
+    sdv = _sdv()
+    s = Quantised(18, [3000, 170, 1200], [9, 3, 5], Hq=8, Hkv=2, D=128)
+    a = s.attention_args()
+    out, lse = _run(s)
+    again, lse2 = _run(s)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    n = sdv.quant_attention_workspace_bytes(sdv.make_quant_attention_args(**a, max_nodes=9))
+    assert n > 0
+    ws = [torch.full((n,), 0xEE, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    res = [torch.zeros_like(out) for _ in range(2)]
+    graphs = []
+    for w, r in zip(ws, res):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sdv.quant_attention(**a, max_nodes=9, out=r, workspace=w, window=0 if r is res[0] else 700)
+        graphs.append(g)
+    for _ in range(3):
+        a["q"].copy_(torch.randn_like(a["q"]))
+        want = [sdv.quant_attention(**a, max_nodes=9, window=w)[0] for w in (0, 700)]
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want[0], res[0]) and torch.equal(want[1], res[1])
