@@ -43,13 +43,13 @@ using sdq::QuantCache;
 
 namespace {
 
-constexpr int WAVES = 4, KEYS = 32, KT = WAVES * KEYS;      // keys of a wave's step, of a unit
-constexpr int NT_Q = WAVES * WAVE;
+constexpr int KEYS = 32;      // keys of a wave's step
 constexpr float LIFT = 7.0f;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef const __attribute__((address_space(1))) char global_char;
+typedef __attribute__((address_space(1))) u32x2 global_u32x2;
+typedef __attribute__((address_space(1))) uint32_t global_u32;
 
 struct QAttnArgs {
   QuantCache c;
@@ -79,7 +79,7 @@ struct Requests {
 
 __device__ __forceinline__ int first_seen(int position, int window) { return window > position ? 0 : position - window + 1; }
 
-template <int RT>
+template <int RT, int KT>
 __device__ __forceinline__ Requests requests(const QAttnArgs& a, int b) {
   Requests r{0, 0, 0, 0, 0, 0, 0, 0, 0};
   if (b < a.c.B) {
@@ -117,11 +117,11 @@ struct Cut {
   int total, per;
 };
 
-template <int RT>
+template <int RT, int KT>
 __device__ __forceinline__ Cut cut_units(const QAttnArgs& a, const Requests& r, int runs) {
   int total = lane_units(r), nt = r.nt;
   for (int b0 = WAVE; b0 < a.c.B; b0 += WAVE) {
-    const Requests q = requests<RT>(a, b0 + (int)threadIdx.x % WAVE);
+    const Requests q = requests<RT, KT>(a, b0 + (int)threadIdx.x % WAVE);
     total += lane_units(q);
     nt = max(nt, q.nt);
   }
@@ -169,30 +169,18 @@ __device__ __forceinline__ Seen seen_by_lane(const QAttnArgs& a, int first, int 
 
 // ---- codes as operands ----
 
-// 4 codes, as two pairs of 16-bit elements of type DT, without their scale.
-template <int DT, int CODE>
+// 4 codes as two pairs of fp16 numbers: e4m3 by value; int8 as (code + 128) 2^-24,
+// which a byte with its sign turned is as the bits of an fp16 number.
+template <int CODE>
 __device__ __forceinline__ u32x2 widen(uint32_t u) {
   u32x2 r;
   if constexpr (CODE == SD_E4M3) {
-    if constexpr (DT == SD_BF16) {
-      r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u, 1.0f, false));
-      r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u, 1.0f, true));
-    } else {
-      r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, false));
-      r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, true));
-    }
-  } else if constexpr (DT == SD_BF16) {
-    // whole numbers of 8 bits are exact in the upper half of an fp32
-    float f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(u >> (8 * i));
-    r[0] = __builtin_amdgcn_perm(__float_as_uint(f[1]), __float_as_uint(f[0]), 0x07060302u);
-    r[1] = __builtin_amdgcn_perm(__float_as_uint(f[3]), __float_as_uint(f[2]), 0x07060302u);
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, true));
   } else {
-    // 0x6480 ^ code is the fp16 number 1152 + code
-    const f16x2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
-    r[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0u, u, 0x0C010C00u) ^ 0x64806480u) - bias);
-    r[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0u, u, 0x0C030C02u) ^ 0x64806480u) - bias);
+    u ^= 0x80808080u;
+    r[0] = __builtin_amdgcn_perm(0u, u, 0x0C010C00u);
+    r[1] = __builtin_amdgcn_perm(0u, u, 0x0C030C02u);
   }
   return r;
 }
@@ -205,44 +193,41 @@ __device__ __forceinline__ uint32_t numbers(uint32_t u) {
   return u;
 }
 
-// Column `byte` of 8 keys as fp16 operand elements; w[s][r]: 4 columns of key
-// 16 s + 4 g4 + r.
+// 4 columns of 8 keys, a word a key, as operands: col[i] holds column i of the keys
+// in their order.
 template <int CODE>
-struct Columns {
-
-  s16x8 col[4];
-  __device__ Columns(const uint32_t (&w)[2][4]) {
-    u32x4 c[4];
-    if constexpr (CODE == SD_I8) {
-      const f16x2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+__device__ __forceinline__ void columns(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t w4, uint32_t w5,
+                                        uint32_t w6, uint32_t w7, s16x8 (&col)[4]) {
+  uint32_t w[8] = {w0, w1, w2, w3, w4, w5, w6, w7};
+  u32x4 c[4];
+  if constexpr (CODE == SD_I8) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x = __builtin_amdgcn_perm(w[s][2 * p + 1], w[s][2 * p], 0x0C040C00u + 0x00010001u * i);
-            c[i][2 * s + p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, x ^ 0x64806480u) - bias);
-          }
-    } else {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const u32x2 a = widen<SD_F16, CODE>(w[s][2 * p]), b = widen<SD_F16, CODE>(w[s][2 * p + 1]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            c[2 * i][2 * s + p] = __builtin_amdgcn_perm(b[i], a[i], 0x05040100u);
-            c[2 * i + 1][2 * s + p] = __builtin_amdgcn_perm(b[i], a[i], 0x07060302u);
-          }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) col[i] = __builtin_bit_cast(s16x8, c[i]);
+    for (int i = 0; i < 8; ++i) w[i] ^= 0x80808080u;
   }
-};
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    if constexpr (CODE == SD_I8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i][p] = __builtin_amdgcn_perm(w[2 * p + 1], w[2 * p], 0x0C040C00u + 0x00010001u * i);
+    } else {
+      const u32x2 a = widen<CODE>(w[2 * p]), b = widen<CODE>(w[2 * p + 1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        c[2 * i][p] = __builtin_amdgcn_perm(b[i], a[i], 0x05040100u);
+        c[2 * i + 1][p] = __builtin_amdgcn_perm(b[i], a[i], 0x07060302u);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) col[i] = __builtin_bit_cast(s16x8, c[i]);
+}
 
-// Any of the 8 elements infinite or not a number, and the others.
+// A scale by its bits: 0, or within the range that one may have.
+__device__ __forceinline__ bool sound_scale(uint32_t u) {
+  return u == 0 || (u >= 0x26800000u && u <= 0x58800000u);      // 2^-50, 2^50
+}
+
+// Elements that are infinite or not a number as 0.
 template <int DT>
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t u, bool& odd) {
   constexpr uint32_t E = DT == SD_BF16 ? 0x7F80u : 0x7C00u;
@@ -251,34 +236,49 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t u, bool& odd) {
   return u;
 }
 
-// A pointer whose loads go through the scalar cache (uniform addresses only, of
-// memory that the kernel does not write).
+// (fmaxf on numbers of unknown origin takes two instructions each)
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  return r;
+}
+
+// A load through the scalar cache (uniform addresses only, of memory that the
+// kernel does not write).
 template <typename T>
 __device__ __forceinline__ T scalar_load(const T* p) {
   return *(const __attribute__((address_space(4))) T*)(uint64_t)p;
 }
 
-// 32 slots of one KV head as loaded, and what is uniform about each 16 of them.
-template <int D>
-struct Raw {
-  static constexpr int KW = D / 64, VW = D / 64;      // 16-byte loads of a key; words of a key's columns
-  u32x4 k[2][KW];
-  uint32_t v[2][4][VW];
-  float kscale[2], vscale[2];
-  int n[2];      // slots that are there, if their scales are sound
+// MT row tiles of 16 a wave, RG groups of KG waves over the rows, each wave of a
+// group with 32 keys of a unit's.
+// OCC waves a SIMD at least.
+template <int D_, int MT_, int RG_, int KG_, int OCC_>
+struct Shape {
+  static constexpr int OCC = OCC_;
+  static constexpr int D = D_, MT = MT_, RG = RG_, KG = KG_;
+  static constexpr int WAVES = RG * KG, NT = WAVES * WAVE;
+  static constexpr int RT = 16 * MT * RG;           // rows of a workgroup
+  static constexpr int KT = KEYS * KG;              // keys of a unit
+  static constexpr int JR = D + 4;                  // floats of a row in the join of the key groups
+  static constexpr int SLOT = RT * (D + 2);         // floats of a partial result
+  static_assert(KT >= SD_MAX_NODES, "the tree is one unit");
 };
 
-template <int DT, int CODE, int D, int MT>
-__global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs a) {
-  constexpr int RT = 16 * MT, KS = D / 32, CB = D / 16, KW = D / 64, VW = D / 64, JR = D + 4;
-  constexpr int SLOT = RT * (D + 2);
-  __shared__ __align__(16) float join[(WAVES - 1) * RT * JR];
+template <int DT, int CODE, typename S>
+__global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
+  constexpr int D = S::D, MT = S::MT, RG = S::RG, KG = S::KG, RT = S::RT, KT = S::KT, JR = S::JR;
+  constexpr int KS = D / 32, CB = D / 16, KW = D / 64, VW = D / 64;      // steps of a product, columns of a lane, words
+  // int8 codes enter as (code + 128) 2^-24, the fp16 number whose bits they are
+  // with the sign turned
+  constexpr float UNIT = CODE == SD_I8 ? 0x1p24f : 1.0f, BIAS = CODE == SD_I8 ? 128.0f : 0.0f;
+  __shared__ __align__(16) float join[(KG - 1) * RT * JR];
   __shared__ int odd_value;      // a node's value is infinite or not a number
   const int tid = threadIdx.x, l = tid % WAVE, n = l & 15, g4 = l >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid / WAVE);
+  const int w = __builtin_amdgcn_readfirstlane(tid / WAVE), rg = w % RG, kg = w / RG;
   const float c = a.scale * 1.4426950408889634f;      // scores in base 2
 
-  Requests rq = requests<RT>(a, l);
+  Requests rq = requests<RT, KT>(a, l);
   int run, u0, u1;
   if (a.whole) {
     run = 0, u0 = 0, u1 = 0;
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
     // Workgroups of one XCD take neighbouring runs: row tiles of one KV head
     // find each other's keys in its L2.
     const int runs = gridDim.x;
-    const auto [total, per] = cut_units<RT>(a, rq, runs);
+    const auto [total, per] = cut_units<RT, KT>(a, rq, runs);
     run = (int)(blockIdx.x % 8) * (runs / 8) + (int)(blockIdx.x / 8);      // runs is a multiple of 8
     if ((int64_t)run * per >= total) return;
     u0 = run * per, u1 = u0 + min(per, total - u0);
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
   if (a.whole) {
     const int b = blockIdx.x / (a.c.H * a.mts_max), seg = blockIdx.x % (a.c.H * a.mts_max);
     b0 = b & ~(WAVE - 1), f = b & (WAVE - 1);
-    if (b0) rq = requests<RT>(a, b0 + l);
+    if (b0) rq = requests<RT, KT>(a, b0 + l);
     const int mts = lane_read(rq.mts, f), nt = lane_read(rq.nt, f);
     if (seg % a.mts_max >= mts) return;
     in = (seg / a.mts_max * mts + seg % a.mts_max) * nt;
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
     while (left >= lane_units(rq)) {
       left -= lane_units(rq);
       b0 += WAVE;
-      rq = requests<RT>(a, b0 + l);
+      rq = requests<RT, KT>(a, b0 + l);
     }
     f = __builtin_ctzll(__ballot(left < rq.incl));
     in = left - (f ? lane_read(rq.incl, f - 1) : 0);
@@ -330,26 +330,56 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
       const int seg = in / nt, t0 = in - seg * nt;
       const int h = seg / mts, mt = seg - h * mts;
       const int t1 = min(nt, t0 + (stop - u0));
-      const int row0 = mt * RT;
+      const int row0 = mt * RT + rg * 16 * MT;
 
-      // queries as the B operand: lane (n, g4) holds of row n the columns that it
-      // loads of a key, 64 (ks / 2) + 16 g4 + 8 (ks % 2) .. + 7
+      // The wave's rows: their nodes; queries as the B operand, lane (n, g4) holding
+      // of row n the columns that it loads of a key, 64 (ks / 2) + 16 g4 + 8 (ks % 2)
+      // .. + 7.  bf16 queries become fp16 ones times a power of 2 that takes the row's
+      // largest to 2^14: exact down to 2^-30 of it.
+      int node[MT];
+      auto query = [&](int m, int ks) {
+        const int r = row0 + 16 * m + n;
+        const int hd = h * a.G + (r < rows ? r - node[m] * a.G : 0);
+        const char* qp = a.q + (int64_t)(first + node[m]) * a.q_node + hd * a.q_head;
+        return r < rows ? *(const s16x8*)(qp + (ks / 2 * 64 + g4 * 16 + ks % 2 * 8) * 2) : s16x8{};
+      };
       s16x8 q[MT][KS];
-      int node[MT], from[MT];
+      float cr[MT], bias[MT];      // what a product is times, and what it holds too much
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int r = row0 + 16 * m + n;
-        const bool on = r < rows;
-        node[m] = on ? row_node(a, r) : 0;
-        const int hd = h * a.G + (on ? r - node[m] * a.G : 0);
-        const char* qp = a.q + (int64_t)(first + node[m]) * a.q_node + hd * a.q_head;
+        node[m] = r < rows ? row_node(a, r) : 0;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[m][ks] = query(m, ks);
+        float up = 1.0f;
+        if constexpr (DT == SD_BF16) {
+          float top = 0.0f;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(to_f32<DT>((uint16_t)q[m][ks][i])));
+          // (127 + 14) - the exponent, where the row is neither 0 nor infinite
+          const int e = (int)(__float_as_uint(quad_max(top)) >> 23);
+          up = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(127 + 14 + 127 - e, 227) << 23) : 1.0f;
+        }
+        float sum = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-          q[m][ks] = on ? *(const s16x8*)(qp + (ks / 2 * 64 + g4 * 16 + ks % 2 * 8) * 2) : s16x8{};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = to_f32<DT>((uint16_t)q[m][ks][i]) * up;
+            if constexpr (DT == SD_BF16) q[m][ks][i] = (short)from_f32<SD_F16>(x);
+            if constexpr (CODE == SD_I8) sum += x;
+          }
+        cr[m] = c * UNIT / up;
+        bias[m] = CODE == SD_I8 ? quad_sum(sum) * (BIAS / UNIT) : 0.0f;
       }
-      // what the rows see of the tree, and the first slot that their windows show
+      // the first slot that the rows' windows show; slots below all_from are past some
+      // row's
+      int from[MT];
       uint64_t vis[MT];
-      if (t1 == nt || a.window) {
+      const bool tree = t1 == nt;
+      if (tree || a.window) {
         const Seen seen = seen_by_lane(a, first, T, ctx);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -360,227 +390,167 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
 #pragma unroll
         for (int m = 0; m < MT; ++m) vis[m] = 0, from[m] = 0;
       }
-      // slots below this one are past some row's window
       const int all_from = a.window ? first_seen(ctx + T - 1, a.window) : 0;
-
       if (tid == 0) odd_value = 0;
-      __syncthreads();
 
-      f32x4 o[MT][CB];
-      float mx[MT], sum[MT];      // sums: of the lane's own keys
+      f32x4 o[MT][CB], norm[MT];            // norm: sums of the weights as the product sees them
+      float ref[MT], sum[MT], limit[MT];    // weights are taken against ref, moved where one passes 2^limit
 
+      const uint64_t kh = (uint64_t)(a.c.k + h * a.c.head_stride), vh = (uint64_t)(a.c.v + h * a.c.head_stride);
+      const uint32_t* const ksh = (const uint32_t*)a.c.ks + h * a.c.scale_head;
+      const uint32_t* const vsh = (const uint32_t*)a.c.vs + h * a.c.scale_head;
+
+      // 16 slots: where they lie.  What is not there reads the pool's first rows
+      // and is masked.
+      struct Place {
+        uint64_t at;          // byte offset in the head's keys and values
+        uint32_t ks, vs;      // scales
+        int n;                // slots that are there
+      };
+      auto slot_of = [&](int t, int s) { return (t < head ? t : t + skip) * KT + kg * KEYS + s * 16; };
       auto page_of = [&](int t, int s) {
-        const int slot = (t < head ? t : t + skip) * KT + w * KEYS + s * 16;
+        const int slot = slot_of(t, s);
         return t < nt - 1 && slot < ctx ? scalar_load(tab + (slot >> a.c.page_shift)) : -1;
       };
-      auto load = [&](int t, const int (&page)[2], Raw<D>& x) {
+      auto place_of = [&](int t, int s, int page) {
+        Place x;
+        const int slot = slot_of(t, s);
+        const bool there = (unsigned)page < (unsigned)a.c.num_pages;
+        const uint32_t p = there ? page : 0, in_page = there ? slot & a.c.page_mask : 0;
+        x.at = p * (uint64_t)a.c.page_stride + in_page * (uint32_t)a.c.slot_stride;      // (a page's: below 2^30)
+        const uint64_t sc = p * (uint64_t)a.c.scale_page + (in_page >> a.c.block_shift);
+        x.ks = scalar_load(ksh + sc);
+        x.vs = scalar_load(vsh + sc);
+        x.n = there ? min(16, ctx - slot) : 0;
+        return x;
+      };
+      u32x4 rk[2][KW];
+      uint32_t rv[2][4][VW];
+      auto load_k = [&](int s, uint64_t at) {
+        global_char* const p = (global_char*)(kh + at);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int slot = (t < head ? t : t + skip) * KT + w * KEYS + s * 16;
-          const bool there = (unsigned)page[s] < (unsigned)a.c.num_pages;
-          // (what is not there reads the pool's first rows and is masked)
-          const int p = there ? page[s] : 0, place = there ? slot & a.c.page_mask : 0;
-          const int64_t at = p * a.c.page_stride + h * a.c.head_stride + place * a.c.slot_stride;
-          const int64_t sc = p * a.c.scale_page + h * a.c.scale_head + (place >> a.c.block_shift);
-          x.kscale[s] = scalar_load(a.c.ks + sc);
-          x.vscale[s] = scalar_load(a.c.vs + sc);
-          x.n[s] = there ? min(16, ctx - slot) : 0;
-          const char* kb = a.c.k + at;
-          const char* vb = a.c.v + at;
+        for (int i = 0; i < KW; ++i) rk[s][i] = *(const global_u32x4*)(p + kat + i * 64);
+      };
+      auto load_v = [&](int s, uint64_t at) {
+        global_char* p = (global_char*)(vh + at);
 #pragma unroll
-          for (int i = 0; i < KW; ++i) x.k[s][i] = *(const global_u32x4*)((uint64_t)kb + kat + i * 64);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint64_t va = (uint64_t)vb + vat + r * (uint32_t)a.c.slot_stride;
-            if constexpr (VW == 2) {
-              const u32x2 y = *(const __attribute__((address_space(1))) u32x2*)va;
-              x.v[s][r][0] = y[0], x.v[s][r][1] = y[1];
-            } else {
-              x.v[s][r][0] = *(const __attribute__((address_space(1))) uint32_t*)va;
-            }
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (VW == 2) {
+            const u32x2 y = *(const global_u32x2*)(p + vat);
+            rv[s][r][0] = y[0], rv[s][r][1] = y[1];
+          } else {
+            rv[s][r][0] = *(const global_u32*)(p + vat);
           }
+          p += (uint32_t)a.c.slot_stride;
         }
       };
 
-      // Scores to weights: x[s][m] becomes 2^(x ks + lv - M), packed as elements of
-      // type PT; bit 16 s + j of on[m]: whether row m sees key j of the 16.
-      auto weigh = [&](auto masked, auto type, f32x4 (&x)[2][MT], const float (&ks)[2], const float (&lv)[2],
-                       const float (&iv)[2], const uint32_t (&on)[MT], s16x8 (&p)[MT]) {
-        constexpr bool MASKED = decltype(masked)::value;
+      // Scores z, relative to ref, to weights 2^z as elements of type PT.
+      auto weigh = [&](auto type, f32x4 (&z)[2][MT], const float (&iv)[2], s16x8 (&p)[MT]) {
         constexpr int PT = decltype(type)::value;
         bool grown = false;
         float top[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          top[m] = -INFINITY;
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float y = fmaf(x[s][m][r], ks[s], lv[s]);
-              if constexpr (MASKED) y = (on[m] >> (g4 * 4) >> (s * 16 + r) & 1) ? y : -INFINITY;
-              x[s][m][r] = y;
-              top[m] = fmaxf(top[m], y);
-            }
+          top[m] = max3(max3(z[0][m][0], z[0][m][1], z[0][m][2]), max3(z[0][m][3], z[1][m][0], z[1][m][1]),
+                        max3(z[1][m][2], z[1][m][3], z[1][m][3]));
           // the sums are rescaled only when a maximum grows by more than 2^8: until
           // then weights up to 2^15 are as exact as those below
-          grown |= top[m] - LIFT > mx[m] + 8.0f;
+          grown |= top[m] > limit[m];
         }
         if (__any(grown)) {
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            const float mn = fmaxf(mx[m], quad_max(top[m]) - LIFT);
-            const float fct = mn > -INFINITY ? fast_exp2(mx[m] - mn) : 1.0f;
-            mx[m] = mn;
-            sum[m] *= fct;
+            const float rise = quad_max(top[m]) - LIFT;
+            if (rise > limit[m] - (LIFT + 8.0f)) {      // > 0, or any rise at all where nothing was seen yet
+              const float fct = limit[m] > 0.0f ? fast_exp2(-rise) : 0.0f;
+              ref[m] += rise;
+              limit[m] = LIFT + 8.0f;
+              sum[m] *= fct;
+              norm[m] *= fct;
 #pragma unroll
-            for (int d = 0; d < CB; ++d) o[m][d] *= fct;
+              for (int d = 0; d < CB; ++d) o[m][d] *= fct;
+#pragma unroll
+              for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) z[s][m][r] -= rise;
+            }
           }
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const float ms = mx[m] > -INFINITY ? mx[m] : 0.0f;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             float y[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              y[r] = fast_exp2(x[s][m][r] - ms);
+              y[r] = fast_exp2(z[s][m][r]);
               p[m][s * 4 + r] = (short)from_f32<PT>(y[r]);
             }
             sum[m] = fmaf((y[0] + y[1]) + (y[2] + y[3]), iv[s], sum[m]);
           }
-        }
       };
-
-      // 32 slots against this wave's rows.
-      auto cached = [&](int t, Raw<D>& x, bool strict) {
-        const int s0 = (t < head ? t : t + skip) * KT + w * KEYS;
-        float ks[2], lv[2], iv[2];
-        uint32_t valid = 0;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const bool sound = sdq::scale_ok(x.kscale[s]) && sdq::scale_ok(x.vscale[s]);
-          const int m = sound ? max(x.n[s], 0) : 0;
-          valid |= ((1u << m) - 1) << (16 * s);
-          ks[s] = sound ? x.kscale[s] * c : 0.0f;
-          const float v = sound && x.vscale[s] > 0.0f ? x.vscale[s] : sdq::MIN_SCALE;
-          lv[s] = __log2f(v);
-          iv[s] = 1.0f / v;
-          if (m < 16 || x.vscale[s] == 0.0f) {
-            // a weight of 0 times a code that is not a number would not be 0
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (g4 * 4 + r >= m || x.vscale[s] == 0.0f)
-#pragma unroll
-                for (int j = 0; j < VW; ++j) x.v[s][r][j] = 0;
-          }
-        }
-        if (valid == 0) return;
-        if (CODE == SD_E4M3 && strict) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int i = 0; i < KW; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) x.k[s][i][j] = numbers(x.k[s][i][j]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-              for (int j = 0; j < VW; ++j) x.v[s][r][j] = numbers(x.v[s][r][j]);
-          }
-        }
-        f32x4 y[2][MT];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) y[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int k2 = 0; k2 < KS; ++k2) {
-            const u32x2 e = widen<DT, CODE>(x.k[s][k2 / 2][k2 % 2 * 2]), g = widen<DT, CODE>(x.k[s][k2 / 2][k2 % 2 * 2 + 1]);
-            const s16x8 kf = __builtin_bit_cast(s16x8, u32x4{e[0], e[1], g[0], g[1]});
-#pragma unroll
-            for (int m = 0; m < MT; ++m) y[s][m] = mfma<DT>(kf, q[m][k2], y[s][m]);
-          }
-        }
-        s16x8 p[MT];
-        using F16 = std::integral_constant<int, SD_F16>;
-        const bool edge = a.window && s0 < all_from && s0 + KEYS > a.sinks;
-        if (valid == 0xFFFFFFFFu && !edge) {
-          uint32_t on[MT] = {};
-          weigh(std::false_type{}, F16{}, y, ks, lv, iv, on, p);
-        } else {
-          uint32_t on[MT];
-          const int sn = min(max(a.sinks - s0, 0), 32);
-          const uint32_t first_ones = sn >= 32 ? 0xFFFFFFFFu : (1u << sn) - 1;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const int skip_keys = min(max(from[m] - s0, 0), 32);
-            const uint32_t near = skip_keys >= 32 ? 0u : 0xFFFFFFFFu << skip_keys;
-            on[m] = valid & (a.window ? near | first_ones : 0xFFFFFFFFu);
-          }
-          weigh(std::true_type{}, F16{}, y, ks, lv, iv, on, p);
-        }
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          const uint32_t words[2][4] = {{x.v[0][0][j], x.v[0][1][j], x.v[0][2][j], x.v[0][3][j]},
-                                        {x.v[1][0][j], x.v[1][1][j], x.v[1][2][j], x.v[1][3][j]}};
-          const Columns<CODE> cols(words);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) o[m][4 * j + i] = mfma<SD_F16>(cols.col[i], p[m], o[m][4 * j + i]);
-        }
-      };
-
-      // Nodes 32 w .. + 31 of the tree, of the queries' type, against this wave's rows.
-      auto nodes = [&]() {
-        if (w * KEYS >= T) return;
-        f32x4 y[2][MT];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int j = min(w * KEYS + s * 16 + n, T - 1);
-          const char* kp = a.kn + (int64_t)(first + j) * a.k_node + h * a.k_head;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) y[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int k2 = 0; k2 < KS; ++k2) {
-            const s16x8 kf = *(const s16x8*)(kp + (k2 / 2 * 64 + g4 * 16 + k2 % 2 * 8) * 2);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) y[s][m] = mfma<DT>(kf, q[m][k2], y[s][m]);
-          }
-        }
-        const float ks[2] = {c, c}, lv[2] = {0.0f, 0.0f}, iv[2] = {1.0f, 1.0f};
-        uint32_t on[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) on[m] = (uint32_t)(vis[m] >> (w * KEYS));      // (waves past the tree have returned)
-        s16x8 p[MT];
-        weigh(std::true_type{}, std::integral_constant<int, DT>{}, y, ks, lv, iv, on, p);
-        // columns 8 (or 4) n .. of the lane's 8 nodes
-        uint32_t v[2][4][CB / 2];
-        bool odd = false;
+      // Bit 16 s + j of on: whether the row sees key j of the 16.
+      auto mask = [&](f32x4 (&z)[2][MT], int m, uint32_t on) {
+        on >>= g4 * 4;
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = w * KEYS + s * 16 + g4 * 4 + r;
-            const char* vp = a.vn + (int64_t)(first + min(j, T - 1)) * a.v_node + h * a.v_head + n * CB * 2;
+          for (int r = 0; r < 4; ++r) z[s][m][r] = (on >> (s * 16 + r) & 1) ? z[s][m][r] : -INFINITY;
+      };
+
+      // Nodes 32 kg .. + 31 of the tree, of the queries' type, against the wave's rows.
+      auto nodes = [&]() {
+        if (kg * KEYS >= T) return;
+        f32x4 z[2][MT];
 #pragma unroll
-            for (int i = 0; i < CB / 2; ++i)
-              v[s][r][i] = j < T ? finite_or_zero<DT>(((const uint32_t*)vp)[i], odd) : 0u;
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) z[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          s16x8 qf[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) qf[m] = DT == SD_BF16 ? query(m, ks) : q[m][ks];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int j = min(kg * KEYS + s * 16 + n, T - 1);
+            const s16x8 kf = *(const s16x8*)(a.kn + (int64_t)(first + j) * a.k_node + h * a.k_head +
+                                             (ks / 2 * 64 + g4 * 16 + ks % 2 * 8) * 2);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) z[s][m] = mfma<DT>(kf, qf[m], z[s][m]);
           }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) z[s][m][r] = fmaf(z[s][m][r], c, -ref[m]);
+          mask(z, m, (uint32_t)(vis[m] >> (kg * KEYS)));
+        }
+        const float one[2] = {1.0f, 1.0f};
+        s16x8 p[MT];
+        weigh(std::integral_constant<int, DT>{}, z, one, p);
         // 0 x infinity in the product would reach rows that do not see this node:
         // such values are added at the end instead
-        if (odd) odd_value = 1;
+        bool odd = false;
 #pragma unroll
-        for (int i = 0; i < CB / 2; ++i) {
+        for (int i = 0; i < CB / 2; ++i) {      // columns n CB + 2 i and + 1 of the lane's 8 nodes
           u32x4 e, g;
 #pragma unroll
           for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              e[2 * s + r] = __builtin_amdgcn_perm(v[s][2 * r + 1][i], v[s][2 * r][i], 0x05040100u);
-              g[2 * s + r] = __builtin_amdgcn_perm(v[s][2 * r + 1][i], v[s][2 * r][i], 0x07060302u);
+              uint32_t v[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int j = kg * KEYS + s * 16 + g4 * 4 + 2 * r + x;
+                const char* vp = a.vn + (int64_t)(first + min(j, T - 1)) * a.v_node + h * a.v_head + n * CB * 2;
+                v[x] = j < T ? finite_or_zero<DT>(((const uint32_t*)vp)[i], odd) : 0u;
+              }
+              e[2 * s + r] = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);
+              g[2 * s + r] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
             }
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
@@ -588,55 +558,172 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
             o[m][2 * i + 1] = mfma<DT>(__builtin_bit_cast(s16x8, g), p[m], o[m][2 * i + 1]);
           }
         }
+        if (odd) odd_value = 1;
       };
 
-      // The key tiles of this run.  An e4m3 code that is not a number counts as 0;
-      // looking for them costs a tenth, so it is done only where a result came out as
-      // none (the second pass).
+      // The cache's key tiles of this run.  An e4m3 code that is not a number counts as
+      // 0; looking for them costs a fifth, so it is done only where a result came out
+      // as none (the second pass).
       const int cached_end = min(t1, nt - 1);
-      for (int strict = 0; strict < 2; ++strict) {
+      for (int strict = 0;; ++strict) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          mx[m] = -INFINITY, sum[m] = 0.0f;
+          ref[m] = 0.0f, limit[m] = -INFINITY, sum[m] = 0.0f;
+          norm[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int d = 0; d < CB; ++d) o[m][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        Raw<D> x[2];
-        int page[2] = {page_of(t0, 0), page_of(t0, 1)};
-        if (t0 < cached_end) load(t0, page, x[0]);
-        page[0] = page_of(t0 + 1, 0), page[1] = page_of(t0 + 1, 1);
-        for (int t = t0; t < cached_end; t += 2) {
-          if (t + 1 < cached_end) {
-            load(t + 1, page, x[1]);
-            page[0] = page_of(t + 2, 0), page[1] = page_of(t + 2, 1);
+        Place x[2];
+        int page[2];
+        if (t0 < cached_end) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            x[s] = place_of(t0, s, page_of(t0, s));
+            load_k(s, x[s].at);
+            load_v(s, x[s].at);
+            page[s] = page_of(t0 + 1, s);
           }
-          cached(t, x[0], strict);
-          if (t + 1 >= cached_end) break;
-          if (t + 2 < cached_end) {
-            load(t + 2, page, x[0]);
-            page[0] = page_of(t + 3, 0), page[1] = page_of(t + 3, 1);
+        }
+        // A tile's keys are loaded behind the products of the one before, its values
+        // behind the weighted sums.  (Loads are not skipped behind the last tile: a wait
+        // could not tell which are on their way.)
+        for (int t = t0; t < cached_end; ++t) {
+          f32x4 z[2][MT];
+          if (CODE == SD_E4M3 && strict) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int i = 0; i < KW; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) rk[s][i][j] = numbers(rk[s][i][j]);
           }
-          cached(t + 1, x[1], strict);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) z[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              const u32x2 e = widen<CODE>(rk[s][ks / 2][ks % 2 * 2]), g = widen<CODE>(rk[s][ks / 2][ks % 2 * 2 + 1]);
+              const s16x8 kf = __builtin_bit_cast(s16x8, u32x4{e[0], e[1], g[0], g[1]});
+#pragma unroll
+              for (int m = 0; m < MT; ++m) z[s][m] = mfma<SD_F16>(kf, q[m][ks], z[s][m]);
+            }
+          }
+          const int s0 = slot_of(t, 0);
+          uint32_t valid = 0;
+          float ks[2], lv[2], iv[2];
+          bool none[2];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const bool sound = sound_scale(x[s].ks) && sound_scale(x[s].vs);
+            const int there = sound ? max(x[s].n, 0) : 0;
+            valid |= ((1u << there) - 1) << (16 * s);
+            none[s] = x[s].vs == 0;
+            const float v = __uint_as_float(sound && !none[s] ? x[s].vs : __float_as_uint(sdq::MIN_SCALE));
+            ks[s] = __uint_as_float(sound ? x[s].ks : 0u);
+            lv[s] = __builtin_amdgcn_logf(v);
+            iv[s] = __builtin_amdgcn_rcpf(v);
+          }
+          Place y[2];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            y[s] = place_of(t + 1, s, page[s]);
+            load_k(s, y[s].at);
+            page[s] = page_of(t + 2, s);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const float k = ks[s] * cr[m], at = fmaf(-bias[m], k, lv[s] - ref[m]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) z[s][m][r] = fmaf(z[s][m][r], k, at);
+            }
+          if (valid != 0xFFFFFFFFu || (a.window && s0 < all_from && s0 + KEYS > a.sinks)) {
+            const int sn = min(max(a.sinks - s0, 0), 32);
+            const uint32_t sinks = sn >= 32 ? 0xFFFFFFFFu : (1u << sn) - 1;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const int past = min(max(from[m] - s0, 0), 32);
+              const uint32_t near = past >= 32 ? 0u : 0xFFFFFFFFu << past;
+              mask(z, m, valid & (near | sinks));      // (without a window `near` is everything)
+            }
+          }
+          s16x8 p[MT];
+          weigh(std::integral_constant<int, SD_F16>{}, z, iv, p);
+          if (valid != 0xFFFFFFFFu || none[0] || none[1]) {
+            // a weight of 0 times a code that is not a number would not be 0; a block
+            // whose scale is 0 has no values
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (none[s] || !(valid >> (16 * s + g4 * 4 + r) & 1))
+#pragma unroll
+                  for (int j = 0; j < VW; ++j) rv[s][r][j] = 0;
+          }
+          if (CODE == SD_E4M3 && strict) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < VW; ++j) rv[s][r][j] = numbers(rv[s][r][j]);
+          }
+          if constexpr (CODE == SD_I8) {
+            const s16x8 ones = s16x8{} + (short)0x3C00;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) norm[m] = mfma<SD_F16>(ones, p[m], norm[m]);
+          }
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            s16x8 col[4];
+            columns<CODE>(rv[0][0][j], rv[0][1][j], rv[0][2][j], rv[0][3][j], rv[1][0][j], rv[1][1][j], rv[1][2][j],
+                          rv[1][3][j], col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int m = 0; m < MT; ++m) o[m][4 * j + i] = mfma<SD_F16>(col[i], p[m], o[m][4 * j + i]);
+          }
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            load_v(s, y[s].at);
+            x[s] = y[s];
+          }
         }
-        if constexpr (CODE != SD_E4M3) break;
-        bool nan = false;
+        if constexpr (CODE == SD_I8) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          nan |= sum[m] != sum[m];
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int d = 0; d < CB; ++d)
+            for (int d = 0; d < CB; ++d)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) nan |= o[m][d][r] != o[m][d][r];
+              for (int r = 0; r < 4; ++r) o[m][d][r] = fmaf(o[m][d][r], UNIT, -BIAS * norm[m][0]);
+          break;
+        } else {
+          bool nan = false;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            nan |= sum[m] != sum[m];
+#pragma unroll
+            for (int d = 0; d < CB; ++d)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) nan |= o[m][d][r] != o[m][d][r];
+          }
+          if (strict || !__any(nan)) break;
         }
-        if (!__any(nan)) break;
       }
-      if (t1 == nt) nodes();
+      __syncthreads();      // odd_value; the join's LDS is free
+      if (tree) nodes();
+      float mx[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) sum[m] = quad_sum(sum[m]);
+      for (int m = 0; m < MT; ++m) {
+        sum[m] = quad_sum(sum[m]);
+        mx[m] = limit[m] > 0.0f ? ref[m] : -INFINITY;
+      }
 
-      // the waves' keys: the first one adds the others up
-      if (w > 0) {
-        float* const z = join + (w - 1) * RT * JR;
+      // the waves' keys: the first of a row group adds the others up
+      if (kg > 0) {
+        float* const z = join + ((kg - 1) * RG + rg) * 16 * MT * JR;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           float* const zr = z + (16 * m + n) * JR;
@@ -649,9 +736,9 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
         }
       }
       __syncthreads();
-      if (w == 0) {
-        for (int k2 = 1; k2 < WAVES; ++k2) {
-          const float* const z = join + (k2 - 1) * RT * JR;
+      if (kg == 0) {
+        for (int k2 = 1; k2 < KG; ++k2) {
+          const float* const z = join + ((k2 - 1) * RG + rg) * 16 * MT * JR;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const float* const zr = z + (16 * m + n) * JR;
@@ -669,7 +756,7 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
               }
           }
         }
-        if (t1 == nt && odd_value) {
+        if (tree && odd_value) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
             for (int j = 0; j < T; ++j) {
@@ -684,10 +771,10 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
             }
         }
         const bool whole = t0 == 0 && t1 == nt;
-        float* const part = a.part + (int64_t)(run * 2 + (t0 == 0)) * SLOT;
+        float* const part = a.part + (int64_t)(run * 2 + (t0 == 0)) * S::SLOT;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const int lr = 16 * m + n, r0 = row0 + lr;
+          const int lr = rg * 16 * MT + 16 * m + n, r0 = mt * RT + lr;
           if (r0 >= rows) continue;
           if (whole) {
             const bool none = sum[m] == 0.0f;
@@ -727,7 +814,7 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
     in = 0;
     if (++f == WAVE && u0 < u1) {
       f = 0, b0 += WAVE;
-      rq = requests<RT>(a, b0 + l);
+      rq = requests<RT, KT>(a, b0 + l);
     }
   }
 }
@@ -735,16 +822,16 @@ __global__ __launch_bounds__(NT_Q, MT == 4 ? 1 : 2) void k_quant_tiles(QAttnArgs
 // Rows whose key tiles went to several runs: their parts in the order of the
 // runs, JN at a time.  grid (4-column groups of a row tile / 256, H * row
 // tiles, B).
-template <int DT, int D, int MT>
+template <int DT, typename S>
 __global__ __launch_bounds__(256) void k_quant_join(QAttnArgs a, int runs) {
-  constexpr int RT = 16 * MT, GPR = D / 4, JN = 8, SLOT = RT * (D + 2);
+  constexpr int D = S::D, RT = S::RT, KT = S::KT, GPR = D / 4, JN = 8, SLOT = S::SLOT;
   const int b = blockIdx.z, h = blockIdx.y / a.mts_max, mt = blockIdx.y % a.mts_max, l = threadIdx.x % WAVE;
-  Requests rq = requests<RT>(a, l);
-  const int per = cut_units<RT>(a, rq, runs).per;
+  Requests rq = requests<RT, KT>(a, l);
+  const int per = cut_units<RT, KT>(a, rq, runs).per;
   int before = 0;
   for (int b0 = 0; b0 + WAVE <= b; b0 += WAVE) {
     before += lane_units(rq);
-    rq = requests<RT>(a, b0 + WAVE + l);
+    rq = requests<RT, KT>(a, b0 + WAVE + l);
   }
   const int f = b % WAVE, nt = lane_read(rq.nt, f), mts = lane_read(rq.mts, f);
   if (mt >= mts) return;
@@ -859,17 +946,19 @@ QAttnArgs device_args(const sd_quant_attention_args_t* p) {
   return a;
 }
 
-// Row tiles of 16 a wave for `rows` packed rows a KV head.
-template <typename F>
-auto with_rows(int rows, F&& f) {
-  if (rows <= 16) return f(std::integral_constant<int, 1>{});
-  if (rows <= 32) return f(std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 4>{});
+// The shape for `rows` packed rows a KV head.
+template <int D, typename F>
+auto with_shape(int rows, F&& f) {
+  if (rows <= 16) return f(Shape<D, 1, 1, 4, 4>{});
+  if (rows <= 32) return f(Shape<D, 2, 1, 4, 2>{});
+  return f(Shape<D, 2, 2, 4, 2>{});
 }
 
-// Workgroups that share the unit list: one a CU of those with 4 row tiles, else
-// two.
-constexpr int run_count(int mt) { return mt == 4 ? 256 : 512; }
+// Workgroups that share the unit list: two a CU of 4 waves, one of 8.
+template <typename S>
+constexpr int run_count() {
+  return S::NT == 512 ? 256 : 512;
+}
 
 // Where there are no more key tiles than this, splitting them and joining the
 // parts in a second launch costs more than it saves.
@@ -882,33 +971,36 @@ struct Plan {
   bool fits, whole;
 };
 
-Plan plan(const sd_quant_attention_args_t* p, int mt) {
+template <typename S>
+Plan plan(const sd_quant_attention_args_t* p) {
   const sd_quant_cache_t& c = p->cache;
-  const int rt = 16 * mt, rows = p->max_nodes * (p->H_q / c.H_kv);
+  const int rows = p->max_nodes * (p->H_q / c.H_kv);
   Plan r;
-  r.mts_max = (rows + rt - 1) / rt;
+  r.mts_max = (rows + S::RT - 1) / S::RT;
   r.segments = (int64_t)c.B * c.H_kv * r.mts_max;
-  r.tiles = ((int64_t)c.max_pages * c.page_size + KT - 1) / KT + 1;
-  if (p->window) r.tiles = std::min(r.tiles, ((int64_t)p->sinks + KT - 1) / KT + ((int64_t)p->window + KT - 1) / KT + 2);
+  r.tiles = ((int64_t)c.max_pages * c.page_size + S::KT - 1) / S::KT + 1;
+  if (p->window)
+    r.tiles = std::min(r.tiles, ((int64_t)p->sinks + S::KT - 1) / S::KT + ((int64_t)p->window + S::KT - 1) / S::KT + 2);
   r.fits = r.segments <= 0x7FFFFFFF / r.tiles;      // units are counted in 32 bits
   // (and a grid dimension holds less than 2^32 threads)
-  r.whole = r.tiles <= WHOLE_TILES && r.segments * NT_Q <= UINT32_MAX;
+  r.whole = r.tiles <= WHOLE_TILES && r.segments * S::NT <= UINT32_MAX;
   return r;
 }
 
 template <int DT, int CODE, int D>
 int launch(QAttnArgs a, const sd_quant_attention_args_t* p, hipStream_t st) {
-  return with_rows(a.max_nodes * a.G, [&](auto mt) {
-    constexpr int MT = decltype(mt)::value, runs = run_count(MT);
-    const Plan r = plan(p, MT);
+  return with_shape<D>(a.max_nodes * a.G, [&](auto s) {
+    using S = decltype(s);
+    constexpr int runs = run_count<S>();
+    const Plan r = plan<S>(p);
     a.mts_max = r.mts_max;
     a.whole = r.whole;
-    hipLaunchKernelGGL((k_quant_tiles<DT, CODE, D, MT>), dim3(a.whole ? (unsigned)r.segments : (unsigned)runs),
-                       dim3(NT_Q), 0, st, a);
+    hipLaunchKernelGGL((k_quant_tiles<DT, CODE, S>), dim3(a.whole ? (unsigned)r.segments : (unsigned)runs),
+                       dim3(S::NT), 0, st, a);
     if (hipGetLastError() != hipSuccess) return SD_EHIP;
     if (a.whole) return SD_OK;
-    const dim3 grid((16 * MT * (D / 4) + 255) / 256, a.c.H * a.mts_max, a.c.B);
-    hipLaunchKernelGGL((k_quant_join<DT, D, MT>), grid, dim3(256), 0, st, a, runs);
+    const dim3 grid((S::RT * (D / 4) + 255) / 256, a.c.H * a.mts_max, a.c.B);
+    hipLaunchKernelGGL((k_quant_join<DT, S>), grid, dim3(256), 0, st, a, runs);
     return hipGetLastError() == hipSuccess ? SD_OK : SD_EHIP;
   });
 }
@@ -919,12 +1011,14 @@ extern "C" int sd_quant_attention_workspace_bytes(const sd_quant_attention_args_
   if (!bytes) return SD_EINVAL;
   const int rc = check(args);
   if (rc) return rc;
-  return with_rows(args->max_nodes * (args->H_q / args->cache.H_kv), [&](auto mt) {
-    constexpr int MT = decltype(mt)::value;
-    const Plan p = plan(args, MT);
-    *bytes = p.whole ? 0 : (size_t)run_count(MT) * 2 * (16 * MT) * (args->cache.D + 2) * sizeof(float);
+  const int rows = args->max_nodes * (args->H_q / args->cache.H_kv);
+  auto size = [&](auto s) {
+    using S = decltype(s);
+    const Plan p = plan<S>(args);
+    *bytes = p.whole ? 0 : (size_t)run_count<S>() * 2 * S::SLOT * sizeof(float);
     return p.fits ? SD_OK : SD_EUNSUPPORTED;
-  });
+  };
+  return args->cache.D == 64 ? with_shape<64>(rows, size) : with_shape<128>(rows, size);
 }
 
 extern "C" int sd_quant_attention(const sd_quant_attention_args_t* args, void* workspace,

@@ -104,7 +104,9 @@ class Quantised:
         the type it enters the product in (fp16 for the cache, the queries' for the
         nodes), and twice the scores' error, all times the weighted mean of |v|; fp32
         sums over n keys add n 2^-24 of the same; fp16 weights far below the largest
-        lose at most 2^-32 of it each."""
+        lose at most 2^-32 of it each.  int8 codes are summed up as code + 128, so n
+        additions are off by n 2^-24 of a sum of up to 255 scales times the weights
+        where |v| would be less."""
         o, e, mag = ref
         n = max(self.lens) + max(self.nodes) + 64
         out, lse = out.double().cpu().numpy()[: self.N], lse.double().cpu().numpy()[: self.N]
@@ -112,6 +114,8 @@ class Quantised:
         eps, es = EPS[self.dtype], self.score_error(scale)
         big = max((self.vs.max() * oracle.serve.TOP[self.code]), np.abs(self.vn).max())
         tol = eps * np.abs(o) + (eps + 2 * es + n * 2.0 ** -24) * (1 + eps) * mag + n * 2.0 ** -32 * big + 2.0 ** -24
+        if self.code == "i8":
+            tol = tol + n * 2.0 ** -24 * 255 * np.nan_to_num(self.vs).max()
         bad = ~(np.abs(out - o) <= tol)
         assert not bad.any(), (np.argwhere(bad)[:5], np.nanmax(np.abs(out - o)))
         none = np.isinf(e)
