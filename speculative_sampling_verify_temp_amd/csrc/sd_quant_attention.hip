@@ -44,12 +44,13 @@ using sdq::QuantCache;
 namespace {
 
 constexpr int KEYS = 32;      // keys of a wave's step
-constexpr float LIFT = 7.0f;
+constexpr float LIFT = 7.0f, LOG2E = 1.4426950408889634f;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef const __attribute__((address_space(1))) char global_char;
 typedef __attribute__((address_space(1))) u32x2 global_u32x2;
 typedef __attribute__((address_space(1))) uint32_t global_u32;
+typedef __attribute__((address_space(1))) s16x8 global_s16x8;
 
 struct QAttnArgs {
   QuantCache c;
@@ -222,18 +223,21 @@ __device__ __forceinline__ void columns(uint32_t w0, uint32_t w1, uint32_t w2, u
   for (int i = 0; i < 4; ++i) col[i] = __builtin_bit_cast(s16x8, c[i]);
 }
 
-// A scale by its bits: 0, or within the range that one may have.
-__device__ __forceinline__ bool sound_scale(uint32_t u) {
-  return u == 0 || (u >= 0x26800000u && u <= 0x58800000u);      // 2^-50, 2^50
-}
-
 // Elements that are infinite or not a number as 0.
 template <int DT>
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t u, bool& odd) {
   constexpr uint32_t E = DT == SD_BF16 ? 0x7F80u : 0x7C00u;
-  if ((u & E) == E) u &= 0xFFFF0000u, odd = true;
-  if (((u >> 16) & E) == E) u &= 0x0000FFFFu, odd = true;
-  return u;
+  const bool lo = (u & E) == E, hi = (u & (E << 16)) == E << 16;
+  odd = lo || hi;
+  return u & (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+}
+
+// The kernel's arguments, read again where they are next needed: held over the loops
+// they would not fit the scalar registers.
+__device__ __forceinline__ const QAttnArgs& args_again() {
+  uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const QAttnArgs*)(const __attribute__((address_space(4))) QAttnArgs*)p;
 }
 
 // (fmaxf on numbers of unknown origin takes two instructions each)
@@ -241,13 +245,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
   return r;
-}
-
-// A load through the scalar cache (uniform addresses only, of memory that the
-// kernel does not write).
-template <typename T>
-__device__ __forceinline__ T scalar_load(const T* p) {
-  return *(const __attribute__((address_space(4))) T*)(uint64_t)p;
 }
 
 // MT row tiles of 16 a wave, RG groups of KG waves over the rows, each wave of a
@@ -276,8 +273,6 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
   __shared__ int odd_value;      // a node's value is infinite or not a number
   const int tid = threadIdx.x, l = tid % WAVE, n = l & 15, g4 = l >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid / WAVE), rg = w % RG, kg = w / RG;
-  const float c = a.scale * 1.4426950408889634f;      // scores in base 2
-
   Requests rq = requests<RT, KT>(a, l);
   int run, u0, u1;
   if (a.whole) {
@@ -314,8 +309,8 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
   }
 
   // offsets of a lane within 16 slots
-  const uint32_t kat = (uint32_t)(n * (int)a.c.slot_stride + g4 * 16);
-  const uint32_t vat = (uint32_t)(g4 * 4 * (int)a.c.slot_stride + n * CB);
+  const uint32_t slot_stride = (uint32_t)a.c.slot_stride;
+  const uint32_t kat = n * slot_stride + g4 * 16, vat = g4 * 4 * slot_stride + n * CB;
 
   while (u0 < u1) {
     const int units = lane_read(rq.incl, f) - (f ? lane_read(rq.incl, f - 1) : 0);
@@ -323,7 +318,6 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
     const int mts = lane_read(rq.mts, f), nt = lane_read(rq.nt, f);
     const int head = lane_read(rq.head, f), skip = lane_read(rq.skip, f);
     const uint32_t st = (uint32_t)lane_read((int)rq.st, f);
-    const int32_t* const tab = a.c.table + (b0 + f) * a.c.ld_table;
     const int rows = T * a.G;
     const int stop = u0 + min(u1 - u0, units - in);
     while (u0 < stop) {
@@ -331,17 +325,24 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       const int h = seg / mts, mt = seg - h * mts;
       const int t1 = min(nt, t0 + (stop - u0));
       const int row0 = mt * RT + rg * 16 * MT;
+      const QAttnArgs& a = args_again();
 
       // The wave's rows: their nodes; queries as the B operand, lane (n, g4) holding
       // of row n the columns that it loads of a key, 64 (ks / 2) + 16 g4 + 8 (ks % 2)
       // .. + 7.  bf16 queries become fp16 ones times a power of 2 that takes the row's
       // largest to 2^14: exact down to 2^-30 of it.
       int node[MT];
-      auto query = [&](int m, int ks) {
+      // (loads are unconditional: rows that are not there read the first one's)
+      auto queries = [&](const QAttnArgs& a, int m, s16x8 (&x)[KS]) {
         const int r = row0 + 16 * m + n;
         const int hd = h * a.G + (r < rows ? r - node[m] * a.G : 0);
-        const char* qp = a.q + (int64_t)(first + node[m]) * a.q_node + hd * a.q_head;
-        return r < rows ? *(const s16x8*)(qp + (ks / 2 * 64 + g4 * 16 + ks % 2 * 8) * 2) : s16x8{};
+        const uint64_t qp = (uint64_t)(a.q + (int64_t)(first + node[m]) * a.q_node + hd * a.q_head) + g4 * 32;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) x[ks] = *(const global_s16x8*)(qp + (ks / 2 * 64 + ks % 2 * 8) * 2);
+        if (r >= rows) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) x[ks] = s16x8{};
+        }
       };
       s16x8 q[MT][KS];
       float cr[MT], bias[MT];      // what a product is times, and what it holds too much
@@ -349,8 +350,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       for (int m = 0; m < MT; ++m) {
         const int r = row0 + 16 * m + n;
         node[m] = r < rows ? row_node(a, r) : 0;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q[m][ks] = query(m, ks);
+        queries(a, m, q[m]);
         float up = 1.0f;
         if constexpr (DT == SD_BF16) {
           float top = 0.0f;
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
             if constexpr (DT == SD_BF16) q[m][ks][i] = (short)from_f32<SD_F16>(x);
             if constexpr (CODE == SD_I8) sum += x;
           }
-        cr[m] = c * UNIT / up;
+        cr[m] = a.scale * LOG2E * UNIT / up;      // scores in base 2
         bias[m] = CODE == SD_I8 ? quad_sum(sum) * (BIAS / UNIT) : 0.0f;
       }
       // the first slot that the rows' windows show; slots below all_from are past some
@@ -390,39 +390,49 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) vis[m] = 0, from[m] = 0;
       }
-      const int all_from = a.window ? first_seen(ctx + T - 1, a.window) : 0;
+      const int all_from = a.window ? first_seen(ctx + T - 1, a.window) : 0, sinks = a.sinks;
       if (tid == 0) odd_value = 0;
 
       f32x4 o[MT][CB], norm[MT];            // norm: sums of the weights as the product sees them
       float ref[MT], sum[MT], limit[MT];    // weights are taken against ref, moved where one passes 2^limit
 
       const uint64_t kh = (uint64_t)(a.c.k + h * a.c.head_stride), vh = (uint64_t)(a.c.v + h * a.c.head_stride);
-      const uint32_t* const ksh = (const uint32_t*)a.c.ks + h * a.c.scale_head;
-      const uint32_t* const vsh = (const uint32_t*)a.c.vs + h * a.c.scale_head;
+      auto slot_of = [&](int t) { return (t < head ? t : t + skip) * KT + kg * KEYS; };
 
-      // 16 slots: where they lie.  What is not there reads the pool's first rows
-      // and is masked.
-      struct Place {
-        uint64_t at;          // byte offset in the head's keys and values
-        uint32_t ks, vs;      // scales
-        int n;                // slots that are there
+      // What there is to know about the next 32 tiles' slots, 16 a lane: lane 2 i + s
+      // has those of tile base + i, half s.  What is not there reads the pool's first
+      // rows and is masked.
+      int base;
+      int at_lo, at_hi;              // byte offset in the head's keys and values
+      int there;                     // slots that are there; 256 where their values are 0 altogether
+      float key_scale, value_log, value_inv;
+      const float *key_at, *value_at;
+      auto look_up = [&](int t0) {
+        const QAttnArgs& a = args_again();
+        const int32_t* const tab = a.c.table + (b0 + f) * a.c.ld_table;
+        base = t0;
+        const int t = t0 + l / 2, slot = slot_of(t) + (l & 1) * 16;
+        const int page = t < nt - 1 && slot < ctx ? tab[slot >> a.c.page_shift] : -1;
+        const bool found = (unsigned)page < (unsigned)a.c.num_pages;
+        const uint32_t p = found ? page : 0, place = found ? slot & a.c.page_mask : 0;
+        const uint64_t at = p * (uint64_t)a.c.page_stride + place * (uint32_t)a.c.slot_stride;      // (a page's: below 2^30)
+        at_lo = (int)(uint32_t)at, at_hi = (int)(uint32_t)(at >> 32);
+        const int64_t sc = p * a.c.scale_page + h * a.c.scale_head + (place >> a.c.block_shift);
+        there = found ? min(16, ctx - slot) : 0;
+        key_at = a.c.ks + sc, value_at = a.c.vs + sc;
       };
-      auto slot_of = [&](int t, int s) { return (t < head ? t : t + skip) * KT + kg * KEYS + s * 16; };
-      auto page_of = [&](int t, int s) {
-        const int slot = slot_of(t, s);
-        return t < nt - 1 && slot < ctx ? scalar_load(tab + (slot >> a.c.page_shift)) : -1;
+      auto look_up_scales = [&]() {
+        const float k = *key_at, v = *value_at;
+        const bool sound = sdq::scale_ok(k) && sdq::scale_ok(v), none = v == 0.0f;
+        const float x = sound && !none ? v : sdq::MIN_SCALE;
+        key_scale = sound ? k : 0.0f;
+        value_log = __builtin_amdgcn_logf(x);
+        value_inv = __builtin_amdgcn_rcpf(x);
+        there = (sound ? there : 0) | (none ? 256 : 0);
       };
-      auto place_of = [&](int t, int s, int page) {
-        Place x;
-        const int slot = slot_of(t, s);
-        const bool there = (unsigned)page < (unsigned)a.c.num_pages;
-        const uint32_t p = there ? page : 0, in_page = there ? slot & a.c.page_mask : 0;
-        x.at = p * (uint64_t)a.c.page_stride + in_page * (uint32_t)a.c.slot_stride;      // (a page's: below 2^30)
-        const uint64_t sc = p * (uint64_t)a.c.scale_page + (in_page >> a.c.block_shift);
-        x.ks = scalar_load(ksh + sc);
-        x.vs = scalar_load(vsh + sc);
-        x.n = there ? min(16, ctx - slot) : 0;
-        return x;
+      auto at_of = [&](int t, int s) {
+        const int i = 2 * (t - base) + s;
+        return (uint64_t)(uint32_t)lane_read(at_hi, i) << 32 | (uint32_t)lane_read(at_lo, i);
       };
       u32x4 rk[2][KW];
       uint32_t rv[2][4][VW];
@@ -441,7 +451,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
           } else {
             rv[s][r][0] = *(const global_u32*)(p + vat);
           }
-          p += (uint32_t)a.c.slot_stride;
+          p += slot_stride;
         }
       };
 
@@ -502,23 +512,43 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       // Nodes 32 kg .. + 31 of the tree, of the queries' type, against the wave's rows.
       auto nodes = [&]() {
         if (kg * KEYS >= T) return;
-        f32x4 z[2][MT];
+        const QAttnArgs& a = args_again();
+        const float c = a.scale * LOG2E;
+        // keys, and columns n CB .. of the lane's 8 nodes
+        s16x8 kf[2][KS];
+        uint32_t v[2][4][CB / 2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int j = min(kg * KEYS + s * 16 + n, T - 1);
+          const uint64_t kp = (uint64_t)(a.kn + (int64_t)(first + j) * a.k_node + h * a.k_head) + g4 * 32;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) kf[s][ks] = *(const global_s16x8*)(kp + (ks / 2 * 64 + ks % 2 * 8) * 2);
+        }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) z[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int r = 0; r < 4; ++r) {
+            const int j = min(kg * KEYS + s * 16 + g4 * 4 + r, T - 1);
+            const uint64_t vp = (uint64_t)(a.vn + (int64_t)(first + j) * a.v_node + h * a.v_head) + n * CB * 2;
+            if constexpr (CB == 8) {
+              const u32x4 y = *(const global_u32x4*)vp;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          s16x8 qf[MT];
+              for (int i = 0; i < 4; ++i) v[s][r][i] = y[i];
+            } else {
+              const u32x2 y = *(const global_u32x2*)vp;
+              v[s][r][0] = y[0], v[s][r][1] = y[1];
+            }
+          }
+        f32x4 z[2][MT];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) qf[m] = DT == SD_BF16 ? query(m, ks) : q[m][ks];
+        for (int m = 0; m < MT; ++m) {
+          s16x8 qf[KS];
+          if constexpr (DT == SD_BF16) queries(a, m, qf);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            const int j = min(kg * KEYS + s * 16 + n, T - 1);
-            const s16x8 kf = *(const s16x8*)(a.kn + (int64_t)(first + j) * a.k_node + h * a.k_head +
-                                             (ks / 2 * 64 + g4 * 16 + ks % 2 * 8) * 2);
+            z[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int m = 0; m < MT; ++m) z[s][m] = mfma<DT>(kf, qf[m], z[s][m]);
+            for (int ks = 0; ks < KS; ++ks) z[s][m] = mfma<DT>(kf[s][ks], DT == SD_BF16 ? qf[ks] : q[m][ks], z[s][m]);
           }
         }
 #pragma unroll
@@ -536,21 +566,27 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
         // such values are added at the end instead
         bool odd = false;
 #pragma unroll
-        for (int i = 0; i < CB / 2; ++i) {      // columns n CB + 2 i and + 1 of the lane's 8 nodes
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const bool in = kg * KEYS + s * 16 + g4 * 4 + r < T;
+#pragma unroll
+            for (int i = 0; i < CB / 2; ++i) {
+              bool strange = false;
+              const uint32_t y = finite_or_zero<DT>(v[s][r][i], strange);
+              v[s][r][i] = in ? y : 0u;
+              odd |= in && strange;
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < CB / 2; ++i) {
           u32x4 e, g;
 #pragma unroll
           for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              uint32_t v[2];
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int j = kg * KEYS + s * 16 + g4 * 4 + 2 * r + x;
-                const char* vp = a.vn + (int64_t)(first + min(j, T - 1)) * a.v_node + h * a.v_head + n * CB * 2;
-                v[x] = j < T ? finite_or_zero<DT>(((const uint32_t*)vp)[i], odd) : 0u;
-              }
-              e[2 * s + r] = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);
-              g[2 * s + r] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
+              e[2 * s + r] = __builtin_amdgcn_perm(v[s][2 * r + 1][i], v[s][2 * r][i], 0x05040100u);
+              g[2 * s + r] = __builtin_amdgcn_perm(v[s][2 * r + 1][i], v[s][2 * r][i], 0x07060302u);
             }
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
@@ -573,16 +609,13 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
 #pragma unroll
           for (int d = 0; d < CB; ++d) o[m][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        Place x[2];
-        int page[2];
         if (t0 < cached_end) {
+          look_up(t0);
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            x[s] = place_of(t0, s, page_of(t0, s));
-            load_k(s, x[s].at);
-            load_v(s, x[s].at);
-            page[s] = page_of(t0 + 1, s);
-          }
+          for (int s = 0; s < 2; ++s) load_k(s, at_of(t0, s));
+#pragma unroll
+          for (int s = 0; s < 2; ++s) load_v(s, at_of(t0, s));
+          look_up_scales();
         }
         // A tile's keys are loaded behind the products of the one before, its values
         // behind the weighted sums.  (Loads are not skipped behind the last tile: a wait
@@ -609,56 +642,51 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
               for (int m = 0; m < MT; ++m) z[s][m] = mfma<SD_F16>(kf, q[m][ks], z[s][m]);
             }
           }
-          const int s0 = slot_of(t, 0);
-          uint32_t valid = 0;
+          const int s0 = slot_of(t);
+          uint32_t valid = 0, none = 0;
           float ks[2], lv[2], iv[2];
-          bool none[2];
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            const bool sound = sound_scale(x[s].ks) && sound_scale(x[s].vs);
-            const int there = sound ? max(x[s].n, 0) : 0;
-            valid |= ((1u << there) - 1) << (16 * s);
-            none[s] = x[s].vs == 0;
-            const float v = __uint_as_float(sound && !none[s] ? x[s].vs : __float_as_uint(sdq::MIN_SCALE));
-            ks[s] = __uint_as_float(sound ? x[s].ks : 0u);
-            lv[s] = __builtin_amdgcn_logf(v);
-            iv[s] = __builtin_amdgcn_rcpf(v);
+            const int i = 2 * (t - base) + s, n16 = lane_read(there, i);
+            valid |= ((1u << (n16 & 255)) - 1) << (16 * s);
+            none |= (n16 >> 8) << s;
+            ks[s] = lane_read(key_scale, i), lv[s] = lane_read(value_log, i), iv[s] = lane_read(value_inv, i);
           }
-          Place y[2];
+          if (t + 1 - base == 32) look_up(t + 1), look_up_scales();
+          uint64_t at[2];
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            y[s] = place_of(t + 1, s, page[s]);
-            load_k(s, y[s].at);
-            page[s] = page_of(t + 2, s);
+            at[s] = at_of(t + 1, s);
+            load_k(s, at[s]);
           }
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-              const float k = ks[s] * cr[m], at = fmaf(-bias[m], k, lv[s] - ref[m]);
+              const float k = ks[s] * cr[m], off = fmaf(-bias[m], k, lv[s] - ref[m]);
 #pragma unroll
-              for (int r = 0; r < 4; ++r) z[s][m][r] = fmaf(z[s][m][r], k, at);
+              for (int r = 0; r < 4; ++r) z[s][m][r] = fmaf(z[s][m][r], k, off);
             }
-          if (valid != 0xFFFFFFFFu || (a.window && s0 < all_from && s0 + KEYS > a.sinks)) {
-            const int sn = min(max(a.sinks - s0, 0), 32);
-            const uint32_t sinks = sn >= 32 ? 0xFFFFFFFFu : (1u << sn) - 1;
+          if (valid != 0xFFFFFFFFu || (s0 < all_from && s0 + KEYS > sinks)) {
+            const int sn = min(max(sinks - s0, 0), 32);
+            const uint32_t first_ones = sn >= 32 ? 0xFFFFFFFFu : (1u << sn) - 1;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
               const int past = min(max(from[m] - s0, 0), 32);
               const uint32_t near = past >= 32 ? 0u : 0xFFFFFFFFu << past;
-              mask(z, m, valid & (near | sinks));      // (without a window `near` is everything)
+              mask(z, m, valid & (near | first_ones));      // (without a window `near` is everything)
             }
           }
           s16x8 p[MT];
           weigh(std::integral_constant<int, SD_F16>{}, z, iv, p);
-          if (valid != 0xFFFFFFFFu || none[0] || none[1]) {
+          if (valid != 0xFFFFFFFFu || none) {
             // a weight of 0 times a code that is not a number would not be 0; a block
             // whose scale is 0 has no values
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
               for (int r = 0; r < 4; ++r)
-                if (none[s] || !(valid >> (16 * s + g4 * 4 + r) & 1))
+                if ((none >> s & 1) || !(valid >> (16 * s + g4 * 4 + r) & 1))
 #pragma unroll
                   for (int j = 0; j < VW; ++j) rv[s][r][j] = 0;
           }
@@ -687,8 +715,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
           }
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            load_v(s, y[s].at);
-            x[s] = y[s];
+            load_v(s, at[s]);
           }
         }
         if constexpr (CODE == SD_I8) {
@@ -737,6 +764,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       }
       __syncthreads();
       if (kg == 0) {
+        const QAttnArgs& a = args_again();
         for (int k2 = 1; k2 < KG; ++k2) {
           const float* const z = join + ((k2 - 1) * RG + rg) * 16 * MT * JR;
 #pragma unroll
@@ -949,7 +977,7 @@ QAttnArgs device_args(const sd_quant_attention_args_t* p) {
 // The shape for `rows` packed rows a KV head.
 template <int D, typename F>
 auto with_shape(int rows, F&& f) {
-  if (rows <= 16) return f(Shape<D, 1, 1, 4, 4>{});
+  if (rows <= 16) return f(Shape<D, 1, 1, 4, 2>{});
   if (rows <= 32) return f(Shape<D, 2, 1, 4, 2>{});
   return f(Shape<D, 2, 2, 4, 2>{});
 }
