@@ -44,12 +44,11 @@ using sdq::QuantCache;
 namespace {
 
 constexpr int KEYS = 32;      // keys of a wave's step
+constexpr int TREE = 8;       // units that the tree of a row tile counts as
 constexpr float LIFT = 7.0f, LOG2E = 1.4426950408889634f;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef const __attribute__((address_space(1))) char global_char;
 typedef __attribute__((address_space(1))) u32x2 global_u32x2;
-typedef __attribute__((address_space(1))) uint32_t global_u32;
 typedef __attribute__((address_space(1))) s16x8 global_s16x8;
 
 struct QAttnArgs {
@@ -70,9 +69,11 @@ struct QAttnArgs {
 // ---- the unit list ----
 
 // What the lanes of a wave hold of up to 64 requests, one each: slots in use,
-// nodes, row tiles, key tiles (the tree's is the last) and units, for all KV
+// nodes, row tiles, key tiles with the tree behind them, and units, for all KV
 // heads, up to and including the lane's own.  Key tile t is the cache's tile t
-// below `head`, t + skip from there on.
+// below `head`, t + skip from there on.  The tree, with what begins and ends a row
+// tile's part, takes as long as TREE key tiles and counts as so many, the first
+// of which stands for it.
 struct Requests {
   int ctx, first, T, mts, nt, head, skip, incl;
   uint32_t st;
@@ -95,7 +96,7 @@ __device__ __forceinline__ Requests requests(const QAttnArgs& a, int b) {
       r.head = min((min(a.sinks, r.ctx) + KT - 1) / KT, tiles);
       r.skip = max(0, min(from, tiles) - r.head);
     }
-    r.nt = tiles - r.skip + 1;
+    r.nt = tiles - r.skip + TREE;
   }
   r.incl = wave_incl_scan_int(r.mts * r.nt * a.c.H);
   return r;
@@ -324,6 +325,11 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       const int seg = in / nt, t0 = in - seg * nt;
       const int h = seg / mts, mt = seg - h * mts;
       const int t1 = min(nt, t0 + (stop - u0));
+      u0 += t1 - t0;
+      in += t1 - t0;
+      if (t0 > nt - TREE) continue;      // nothing but what the tree counts for
+      const int cached = nt - TREE, cached_end = min(t1, cached);
+      const bool tree = t1 > cached;
       const int row0 = mt * RT + rg * 16 * MT;
       const QAttnArgs& a = args_again();
 
@@ -332,6 +338,11 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       // .. + 7.  bf16 queries become fp16 ones times a power of 2 that takes the row's
       // largest to 2^14: exact down to 2^-30 of it.
       int node[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int r = row0 + 16 * m + n;
+        node[m] = r < rows ? row_node(a, r) : 0;
+      }
       // (loads are unconditional: rows that are not there read the first one's)
       auto queries = [&](const QAttnArgs& a, int m, s16x8 (&x)[KS]) {
         const int r = row0 + 16 * m + n;
@@ -344,13 +355,109 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
           for (int ks = 0; ks < KS; ++ks) x[ks] = s16x8{};
         }
       };
+      f32x4 o[MT][CB], norm[MT];            // norm: sums of the weights as the product sees them
+      float ref[MT], sum[MT], limit[MT];    // weights are taken against ref, moved where one passes 2^limit
+
+      const uint64_t kh = (uint64_t)(a.c.k + h * a.c.head_stride), vh = (uint64_t)(a.c.v + h * a.c.head_stride);
+      auto slot_of = [&](int t) { return (t < head ? t : t + skip) * KT + kg * KEYS; };
+
+      // What there is to know about the next 32 tiles' slots, 16 a lane: lane 2 i + s
+      // has those of tile base + i, half s.
+      int base;
+      int at_lo, at_hi;              // byte offset in the head's keys and values
+      int bytes, there;              // of the slots that are there; 256 more where their values are 0 altogether
+      float key_scale, value_log, value_inv;
+      const float *key_at, *value_at;
+      auto look_up = [&](int t0) {
+        const QAttnArgs& a = args_again();
+        const int32_t* const tab = a.c.table + (b0 + f) * a.c.ld_table;
+        base = t0;
+        const int t = t0 + l / 2, slot = slot_of(t) + (l & 1) * 16;
+        const int page = t < cached && slot < ctx ? tab[slot >> a.c.page_shift] : -1;
+        const bool found = (unsigned)page < (unsigned)a.c.num_pages;
+        const uint32_t p = found ? page : 0, place = found ? slot & a.c.page_mask : 0;
+        const uint64_t at = p * (uint64_t)a.c.page_stride + place * (uint32_t)a.c.slot_stride;      // (a page's: below 2^30)
+        at_lo = (int)(uint32_t)at, at_hi = (int)(uint32_t)(at >> 32);
+        const int64_t sc = p * a.c.scale_page + h * a.c.scale_head + (place >> a.c.block_shift);
+        there = found ? min(16, ctx - slot) : 0;
+        bytes = there * (int)slot_stride;
+        key_at = a.c.ks + sc, value_at = a.c.vs + sc;
+      };
+      auto look_up_scales = [&]() {
+        const float k = *key_at, v = *value_at;
+        const bool sound = sdq::scale_ok(k) && sdq::scale_ok(v), none = v == 0.0f;
+        const float x = sound && !none ? v : sdq::MIN_SCALE;
+        key_scale = sound ? k : 0.0f;
+        value_log = __builtin_amdgcn_logf(x);
+        value_inv = __builtin_amdgcn_rcpf(x);
+        there = (sound ? there : 0) | (none ? 256 : 0);
+      };
+      // Buffers over the 16 slots (those in use, none where they are not there): what
+      // lies past them reads as zeros, without a memory access.
+      struct Rows {
+        uint64_t at;
+        int bytes;
+      };
+      auto rows_of = [&](int t, int s) {
+        const int i = 2 * (t - base) + s;
+        return Rows{(uint64_t)(uint32_t)lane_read(at_hi, i) << 32 | (uint32_t)lane_read(at_lo, i), lane_read(bytes, i)};
+      };
+      auto buffer = [](uint64_t at, int bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)at, (short)0, bytes, 0x00020000);
+      };
+      u32x4 rk[2][KW];
+      uint32_t rv[2][4][VW];
+      auto load_k = [&](int s, const Rows& x) {
+        const __amdgpu_buffer_rsrc_t rs = buffer(kh + x.at, x.bytes);
+#pragma unroll
+        for (int i = 0; i < KW; ++i) rk[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rs, kat + i * 64, 0, 0);
+      };
+      auto load_v = [&](int s, const Rows& x) {
+        const __amdgpu_buffer_rsrc_t rs = buffer(vh + x.at, x.bytes);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (VW == 2) {
+            const u32x2 y = __builtin_amdgcn_raw_buffer_load_b64(rs, vat, r * slot_stride, 0);
+            rv[s][r][0] = y[0], rv[s][r][1] = y[1];
+          } else {
+            rv[s][r][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, vat, r * slot_stride, 0);
+          }
+        }
+      };
+      auto begin = [&]() {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) load_k(s, rows_of(t0, s));
+#pragma unroll
+        for (int s = 0; s < 2; ++s) load_v(s, rows_of(t0, s));
+      };
+
+      // Everything that is first needed, on its way at once.
+      if (t0 < cached_end) look_up(t0);
       s16x8 q[MT][KS];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) queries(a, m, q[m]);
+      if (t0 < cached_end) begin(), look_up_scales();
+      // the first slot that the rows' windows show; slots below all_from are past some
+      // row's
+      int from[MT];
+      uint64_t vis[MT];
+      if (tree || a.window) {
+        const Seen seen = seen_by_lane(a, first, T, ctx);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          vis[m] = st ? 0 : __shfl(seen.nodes, node[m]);
+          from[m] = a.window ? first_seen(ctx + __shfl(seen.depth, node[m]), a.window) : 0;
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) vis[m] = 0, from[m] = 0;
+      }
+      const int all_from = a.window ? first_seen(ctx + T - 1, a.window) : 0, sinks = a.sinks;
+      if (tid == 0) odd_value = 0;
+
       float cr[MT], bias[MT];      // what a product is times, and what it holds too much
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int r = row0 + 16 * m + n;
-        node[m] = r < rows ? row_node(a, r) : 0;
-        queries(a, m, q[m]);
         float up = 1.0f;
         if constexpr (DT == SD_BF16) {
           float top = 0.0f;
@@ -374,87 +481,6 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
         cr[m] = a.scale * LOG2E * UNIT / up;      // scores in base 2
         bias[m] = CODE == SD_I8 ? quad_sum(sum) * (BIAS / UNIT) : 0.0f;
       }
-      // the first slot that the rows' windows show; slots below all_from are past some
-      // row's
-      int from[MT];
-      uint64_t vis[MT];
-      const bool tree = t1 == nt;
-      if (tree || a.window) {
-        const Seen seen = seen_by_lane(a, first, T, ctx);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          vis[m] = st ? 0 : __shfl(seen.nodes, node[m]);
-          from[m] = a.window ? first_seen(ctx + __shfl(seen.depth, node[m]), a.window) : 0;
-        }
-      } else {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) vis[m] = 0, from[m] = 0;
-      }
-      const int all_from = a.window ? first_seen(ctx + T - 1, a.window) : 0, sinks = a.sinks;
-      if (tid == 0) odd_value = 0;
-
-      f32x4 o[MT][CB], norm[MT];            // norm: sums of the weights as the product sees them
-      float ref[MT], sum[MT], limit[MT];    // weights are taken against ref, moved where one passes 2^limit
-
-      const uint64_t kh = (uint64_t)(a.c.k + h * a.c.head_stride), vh = (uint64_t)(a.c.v + h * a.c.head_stride);
-      auto slot_of = [&](int t) { return (t < head ? t : t + skip) * KT + kg * KEYS; };
-
-      // What there is to know about the next 32 tiles' slots, 16 a lane: lane 2 i + s
-      // has those of tile base + i, half s.  What is not there reads the pool's first
-      // rows and is masked.
-      int base;
-      int at_lo, at_hi;              // byte offset in the head's keys and values
-      int there;                     // slots that are there; 256 where their values are 0 altogether
-      float key_scale, value_log, value_inv;
-      const float *key_at, *value_at;
-      auto look_up = [&](int t0) {
-        const QAttnArgs& a = args_again();
-        const int32_t* const tab = a.c.table + (b0 + f) * a.c.ld_table;
-        base = t0;
-        const int t = t0 + l / 2, slot = slot_of(t) + (l & 1) * 16;
-        const int page = t < nt - 1 && slot < ctx ? tab[slot >> a.c.page_shift] : -1;
-        const bool found = (unsigned)page < (unsigned)a.c.num_pages;
-        const uint32_t p = found ? page : 0, place = found ? slot & a.c.page_mask : 0;
-        const uint64_t at = p * (uint64_t)a.c.page_stride + place * (uint32_t)a.c.slot_stride;      // (a page's: below 2^30)
-        at_lo = (int)(uint32_t)at, at_hi = (int)(uint32_t)(at >> 32);
-        const int64_t sc = p * a.c.scale_page + h * a.c.scale_head + (place >> a.c.block_shift);
-        there = found ? min(16, ctx - slot) : 0;
-        key_at = a.c.ks + sc, value_at = a.c.vs + sc;
-      };
-      auto look_up_scales = [&]() {
-        const float k = *key_at, v = *value_at;
-        const bool sound = sdq::scale_ok(k) && sdq::scale_ok(v), none = v == 0.0f;
-        const float x = sound && !none ? v : sdq::MIN_SCALE;
-        key_scale = sound ? k : 0.0f;
-        value_log = __builtin_amdgcn_logf(x);
-        value_inv = __builtin_amdgcn_rcpf(x);
-        there = (sound ? there : 0) | (none ? 256 : 0);
-      };
-      auto at_of = [&](int t, int s) {
-        const int i = 2 * (t - base) + s;
-        return (uint64_t)(uint32_t)lane_read(at_hi, i) << 32 | (uint32_t)lane_read(at_lo, i);
-      };
-      u32x4 rk[2][KW];
-      uint32_t rv[2][4][VW];
-      auto load_k = [&](int s, uint64_t at) {
-        global_char* const p = (global_char*)(kh + at);
-#pragma unroll
-        for (int i = 0; i < KW; ++i) rk[s][i] = *(const global_u32x4*)(p + kat + i * 64);
-      };
-      auto load_v = [&](int s, uint64_t at) {
-        global_char* p = (global_char*)(vh + at);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (VW == 2) {
-            const u32x2 y = *(const global_u32x2*)(p + vat);
-            rv[s][r][0] = y[0], rv[s][r][1] = y[1];
-          } else {
-            rv[s][r][0] = *(const global_u32*)(p + vat);
-          }
-          p += slot_stride;
-        }
-      };
-
       // Scores z, relative to ref, to weights 2^z as elements of type PT.
       auto weigh = [&](auto type, f32x4 (&z)[2][MT], const float (&iv)[2], s16x8 (&p)[MT]) {
         constexpr int PT = decltype(type)::value;
@@ -600,7 +626,6 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       // The cache's key tiles of this run.  An e4m3 code that is not a number counts as
       // 0; looking for them costs a fifth, so it is done only where a result came out
       // as none (the second pass).
-      const int cached_end = min(t1, nt - 1);
       for (int strict = 0;; ++strict) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -608,14 +633,6 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
           norm[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int d = 0; d < CB; ++d) o[m][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        if (t0 < cached_end) {
-          look_up(t0);
-#pragma unroll
-          for (int s = 0; s < 2; ++s) load_k(s, at_of(t0, s));
-#pragma unroll
-          for (int s = 0; s < 2; ++s) load_v(s, at_of(t0, s));
-          look_up_scales();
         }
         // A tile's keys are loaded behind the products of the one before, its values
         // behind the weighted sums.  (Loads are not skipped behind the last tile: a wait
@@ -653,11 +670,11 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
             ks[s] = lane_read(key_scale, i), lv[s] = lane_read(value_log, i), iv[s] = lane_read(value_inv, i);
           }
           if (t + 1 - base == 32) look_up(t + 1), look_up_scales();
-          uint64_t at[2];
+          Rows next[2];
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            at[s] = at_of(t + 1, s);
-            load_k(s, at[s]);
+            next[s] = rows_of(t + 1, s);
+            load_k(s, next[s]);
           }
 #pragma unroll
           for (int m = 0; m < MT; ++m)
@@ -679,14 +696,12 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
           }
           s16x8 p[MT];
           weigh(std::integral_constant<int, SD_F16>{}, z, iv, p);
-          if (valid != 0xFFFFFFFFu || none) {
-            // a weight of 0 times a code that is not a number would not be 0; a block
-            // whose scale is 0 has no values
+          if (none) {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
+              if (none >> s & 1)
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if ((none >> s & 1) || !(valid >> (16 * s + g4 * 4 + r) & 1))
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
                   for (int j = 0; j < VW; ++j) rv[s][r][j] = 0;
           }
@@ -715,7 +730,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
           }
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            load_v(s, at[s]);
+            load_v(s, next[s]);
           }
         }
         if constexpr (CODE == SD_I8) {
@@ -736,7 +751,8 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
 #pragma unroll
               for (int r = 0; r < 4; ++r) nan |= o[m][d][r] != o[m][d][r];
           }
-          if (strict || !__any(nan)) break;
+          if (strict || !__any(nan) || t0 >= cached_end) break;
+          look_up(t0), begin(), look_up_scales();
         }
       }
       __syncthreads();      // odd_value; the join's LDS is free
@@ -798,7 +814,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
                 }
             }
         }
-        const bool whole = t0 == 0 && t1 == nt;
+        const bool whole = t0 == 0 && tree;
         float* const part = a.part + (int64_t)(run * 2 + (t0 == 0)) * S::SLOT;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -836,8 +852,6 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
         }
       }
       __syncthreads();      // the join's LDS and odd_value are the next segment's
-      u0 += t1 - t0;
-      in += t1 - t0;
     }
     in = 0;
     if (++f == WAVE && u0 < u1) {
@@ -865,7 +879,7 @@ __global__ __launch_bounds__(256) void k_quant_join(QAttnArgs a, int runs) {
   if (mt >= mts) return;
   if (f) before += lane_read(rq.incl, f - 1);
   const int s = before + (h * mts + mt) * nt;
-  const int w0 = (int)((unsigned)s / (unsigned)per), w1 = (int)((unsigned)(s + nt - 1) / (unsigned)per);
+  const int w0 = (int)((unsigned)s / (unsigned)per), w1 = (int)((unsigned)(s + nt - TREE) / (unsigned)per);      // (the tree's)
   const int lin = blockIdx.x * 256 + threadIdx.x, lr = lin / GPR, col = lin % GPR, r = mt * RT + lr;
   if (w0 == w1 || lr >= RT || r >= lane_read(rq.T, f) * a.G) return;
   float m = -INFINITY, sum = 0.0f;
@@ -979,7 +993,7 @@ template <int D, typename F>
 auto with_shape(int rows, F&& f) {
   if (rows <= 16) return f(Shape<D, 1, 1, 4, 2>{});
   if (rows <= 32) return f(Shape<D, 2, 1, 4, 2>{});
-  return f(Shape<D, 2, 2, 4, 2>{});
+  return f(Shape<D, 2, 2, 2, 2>{});
 }
 
 // Workgroups that share the unit list: two a CU of 4 waves, one of 8.
@@ -990,7 +1004,7 @@ constexpr int run_count() {
 
 // Where there are no more key tiles than this, splitting them and joining the
 // parts in a second launch costs more than it saves.
-constexpr int WHOLE_TILES = 8;
+constexpr int WHOLE_TILES = 7;
 
 // How a call is cut up.
 struct Plan {
@@ -1006,12 +1020,12 @@ Plan plan(const sd_quant_attention_args_t* p) {
   Plan r;
   r.mts_max = (rows + S::RT - 1) / S::RT;
   r.segments = (int64_t)c.B * c.H_kv * r.mts_max;
-  r.tiles = ((int64_t)c.max_pages * c.page_size + S::KT - 1) / S::KT + 1;
+  r.tiles = ((int64_t)c.max_pages * c.page_size + S::KT - 1) / S::KT + TREE;
   if (p->window)
-    r.tiles = std::min(r.tiles, ((int64_t)p->sinks + S::KT - 1) / S::KT + ((int64_t)p->window + S::KT - 1) / S::KT + 2);
+    r.tiles = std::min(r.tiles, ((int64_t)p->sinks + S::KT - 1) / S::KT + ((int64_t)p->window + S::KT - 1) / S::KT + 1 + TREE);
   r.fits = r.segments <= 0x7FFFFFFF / r.tiles;      // units are counted in 32 bits
   // (and a grid dimension holds less than 2^32 threads)
-  r.whole = r.tiles <= WHOLE_TILES && r.segments * S::NT <= UINT32_MAX;
+  r.whole = r.tiles - TREE <= WHOLE_TILES && r.segments * S::NT <= UINT32_MAX;
   return r;
 }
 
