@@ -10,21 +10,22 @@
 // walk, and one for the draw where nothing was rejected at its last node.  Bound
 // by those rows' bytes in large batches, by a pass's latency in small ones.
 //
-// k_sample_begin    one wave per request: the walk up to its first pass.
-// k_sample_passes   teams of workgroups make the passes, one slice of the
-//                   vocabulary each; every wave leaves the sum of its own
-//                   stretch.  The last workgroup of a pass to do so goes on with
-//                   the walk, and at its end finds the stretch and the token that
-//                   the draw falls on.
+// k_sample_begin    clears what the teams share.
+// k_sample_passes   teams of workgroups, one a slice of the vocabulary; each of their
+//                   waves sums up a stretch of its own.  Every member leaves its
+//                   slice's sum for the others, reads theirs, and follows the walk by
+//                   itself, so a pass costs one store and one look at it.  A sum
+//                   carries its pass in its 7 lowest bits, and the sums of two passes
+//                   have places of their own: who writes the third has read the first.
+//                   The member whose slice the draw falls on finds the token.
 //
-// Teams meet through tickets: ticket k of a request is slice k % slices of its
-// pass number k / slices.  A ticket is only waited for by later ones, and whoever
-// holds an earlier one is running, so every wait ends however few workgroups of a
-// team the chip holds at a time.  (Calls that overlap on one workspace, which the
-// interface forbids, could take each other's tickets: waits are bounded, and such a
+// A slice is claimed before its sum is left, by the workgroup that it belongs to or,
+// when that does not come, by one that waits for it and has it from then on; who
+// loses its last slice ends.  So every wait is for a workgroup that runs, however few
+// of a team the chip holds at a time.  (Calls that overlap on one workspace, which the
+// interface forbids, could take each other's slices: waits are bounded, and such a
 // request keeps the -1 and SD_ST_UNFINISHED that its results begin with.)  What a
-// team shares is only touched by relaxed agent-scope atomics, with a wait for the
-// ones before where order matters.
+// team shares is only touched by relaxed agent-scope atomics, a value each.
 #include <algorithm>
 
 #include "sd_serve.h"
@@ -38,17 +39,18 @@ namespace {
 constexpr int NT = 512;               // threads of a workgroup
 constexpr int WV = NT / WAVE;
 constexpr int US = 4;                 // vectors of each row that a lane loads at once
-constexpr uint32_t DONE = 0xFFFFFFFFu;
+constexpr int MAX_SLICES = WAVE;      // (a lane looks at each)
+constexpr uint64_t TAG = 127;         // of a sum; passes are SD_MAX_NODES + 1 at most: every node's
+                                      // rejection but the root's, a draw, one more after a total of 0
 constexpr int MAX_POLLS = 1 << 21;    // about two seconds; a wait takes microseconds
+constexpr int STEAL = 24;             // looks at a pass before its unclaimed slices are taken over, some 20 us
 
-// Where a walk stands, and what its next pass sums up.
 struct Team {
-  uint32_t ticket, left, pass, place;       // pass: its number, or DONE; place: count << 16 | next child << 8 | node
-  double cut, Z, gone;
-  uint32_t mode, st;
-  uint8_t path[SD_MAX_NODES];
+  uint64_t sums[2][MAX_SLICES];       // of the even passes and the odd ones; their tag is the pass + 1
+  uint32_t claims[MAX_SLICES];        // passes for which a slice was claimed
 };
-enum : uint32_t { RESIDUAL, PLAIN };        // max(p - cut q, 0), or p without the rejected tokens
+enum Mode : uint32_t { RESIDUAL, PLAIN };      // weights max(p - cut q, 0), or p without the rejected tokens
+enum Next { STOP, DRAW, PASS };
 
 struct SampleArgs {
   const float *p, *q;
@@ -59,7 +61,6 @@ struct SampleArgs {
   uint32_t flags;
   int slices, stretch;      // stretch: vectors of 4 that a wave sums up
   int polls;
-  double* part;             // [B][slices * WV]
   Team* team;               // [B]
   int32_t *accepted, *path, *out_tokens;
   uint32_t* status;
@@ -73,16 +74,10 @@ template <typename T>
 __device__ __forceinline__ void shared_store(T* p, T v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ uint32_t shared_add(uint32_t* p) {
-  return __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Whether *p was `from`; it is `from + 1` then.
+__device__ __forceinline__ bool shared_claim(uint32_t* p, uint32_t from) {
+  return __hip_atomic_compare_exchange_strong(p, &from, from + 1, __ATOMIC_RELAXED, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// All memory operations of this wave before are done, and none after begun.
-__device__ __forceinline__ void settle() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0);
-  asm volatile("" ::: "memory");
-}
-
 __device__ __forceinline__ bool bad_prob(double x) { return !(x >= 0.0 && x < INFINITY); }
 
 // A request's tree and walk in a wave: lane l holds node l.
@@ -91,6 +86,7 @@ struct Walk {
   uint32_t st;
   int tok, up;
   double px, qx, u;      // of the lane's token in its parent's rows
+  float v;
   int cur = 0, child = 0, count = 0, my_path = -1;
   double cut = 0.0, Z = 1.0, gone = 0.0;
   uint32_t mode;
@@ -115,6 +111,7 @@ struct Walk {
       px = a.p[row * a.ld_p + tok];
       if (a.q && tok < a.Vd) qx = a.q[row * a.ld_q + tok];
     }
+    v = a.v[b];
     if (l == 0) my_path = 0;
   }
   __device__ bool valid() const { return !(st & SD_ST_TREE_INVALID_MASK); }
@@ -184,43 +181,44 @@ struct Walk {
     }
   }
 
-  // Into and out of what the team shares.
-  __device__ void leave(Team& t, uint32_t pass) const {
+  // Goes on after a pass with this total.
+  __device__ Next resume(const SampleArgs& a, double total) {
     const int l = threadIdx.x % WAVE;
-    shared_store(&t.path[l], (uint8_t)my_path);
-    if (l == 0) {
-      shared_store(&t.cut, cut), shared_store(&t.Z, Z), shared_store(&t.gone, gone);
-      shared_store(&t.mode, mode), shared_store(&t.st, st);
-      shared_store(&t.place, (uint32_t)(count << 16 | child << 8 | cur));
+    if (!(total < INFINITY)) {      // (NaN: an element that is no probability)
+      st |= SD_ST_NONFINITE;
+      return STOP;
     }
-    settle();
-    if (l == 0) shared_store(&t.pass, pass);
-  }
-  __device__ void enter(const Team& t) {
-    const int l = threadIdx.x % WAVE;
-    const uint32_t p = shared_load(&t.place);
-    cur = (int)(p & 63u), child = (int)(p >> 8 & 127u), count = (int)(p >> 16 & 63u);
-    cut = shared_load(&t.cut), Z = shared_load(&t.Z), gone = shared_load(&t.gone);
-    mode = shared_load(&t.mode) & 1u, st = shared_load(&t.st);
-    const uint8_t m = shared_load(&t.path[l]);
-    my_path = l <= count ? (int)(m & 63u) : -1;
+    if (mode == RESIDUAL && !(total > 0.0)) {
+      // p = q but for rounding: the draw is from p, after one more pass
+      st |= SD_ST_RESID_ZERO;
+      mode = PLAIN, child = WAVE;
+      return PASS;
+    }
+    if (mode == RESIDUAL && __ballot(up == cur && l >= child)) {
+      Z = total;
+      return advance(a) ? PASS : STOP;
+    }
+    if (!(total > 0.0)) st |= SD_ST_NONFINITE;
+    else if (!(v >= 0.0f && v < 1.0f)) st |= SD_ST_BAD_PARAM;
+    else return DRAW;
+    return STOP;
   }
 };
 
+// Requests as they are until their walks end, one wave each.
 __global__ __launch_bounds__(WAVE) void k_sample_begin(SampleArgs a) {
   const int b = blockIdx.x, l = threadIdx.x;
-  Walk w(a, b, true);
-  const bool go = w.valid() && w.advance(a);
   Team& t = a.team[b];
-  if (l == 0) t.ticket = t.left = 0;
-  if (go) {
-    Walk none = w;
-    none.st |= SD_ST_UNFINISHED;
-    none.write(a, b, -1);
-  } else {
-    w.write(a, b, -1);
+  t.sums[0][l] = t.sums[1][l] = 0;
+  t.claims[l] = 0;
+  if (l < a.max_nodes) {
+    a.path[(int64_t)b * a.max_nodes + l] = -1;
+    a.out_tokens[(int64_t)b * a.max_nodes + l] = -1;
   }
-  w.leave(t, go ? 0 : DONE);
+  if (l == 0) {
+    a.accepted[b] = -1;
+    if (a.status) a.status[b] = SD_ST_UNFINISHED;
+  }
 }
 
 // Vector k of a row of n elements of which `full` vectors are whole.  Loads are
@@ -246,8 +244,7 @@ struct Rows {
   double cut;
   bool pair;
 
-  __device__ Rows(const SampleArgs& a, const Nodes& nd, uint32_t place, uint32_t mode, double c) {
-    const int64_t row = nd.first + min((int)(place & 63u), nd.T - 1);
+  __device__ Rows(const SampleArgs& a, int64_t row, uint32_t mode, double c) {
     pair = mode == RESIDUAL && a.q;
     p = a.p + row * a.ld_p;
     q = pair ? a.q + row * a.ld_q : p;
@@ -297,159 +294,185 @@ struct Rows {
 
 __device__ __forceinline__ float at(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-__global__ __launch_bounds__(NT) void k_sample_passes(SampleArgs a) {
-  __shared__ uint32_t ticket_sh, pass_sh, place_sh, mode_sh;
-  __shared__ int last_sh, gone_n, gone_sh[SD_MAX_NODES], go_sh, piece_sh, token_sh, spare_sh;
-  __shared__ double cut_sh, total_sh[WV], base_sh;
-  const int b = blockIdx.y, tid = threadIdx.x, l = tid % WAVE;
+// The sum of a lane's weights, NaN where one of its elements is no probability.
+template <int U>
+__device__ __forceinline__ void add_up(const Rows& rows, const float4 (&x)[U], const float4 (&y)[U], double& sum, bool& bad) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float lowest = fminf(fminf(fminf(x[u].x, x[u].y), fminf(x[u].z, x[u].w)),
+                               fminf(fminf(y[u].x, y[u].y), fminf(y[u].z, y[u].w)));
+    const float all = (x[u].x + x[u].y) + (x[u].z + x[u].w) + ((y[u].x + y[u].y) + (y[u].z + y[u].w));
+    bad |= !(lowest >= 0.0f) || !(all < INFINITY);
+    sum += rows.weight(x[u].x, y[u].x);
+    sum += rows.weight(x[u].y, y[u].y);
+    sum += rows.weight(x[u].z, y[u].z);
+    sum += rows.weight(x[u].w, y[u].w);
+  }
+}
+
+__global__ __launch_bounds__(NT, 4) void k_sample_passes(SampleArgs a) {
+  __shared__ uint32_t mode_sh;
+  __shared__ int cur_sh, go_sh, got_sh, draw_sh, gone_n, gone_sh[SD_MAX_NODES], token_sh, spare_sh;
+  __shared__ double cut_sh, t_sh, sums_sh[WV], run_sh[WV];
+  __shared__ uint64_t missing_sh;
+  const int b = blockIdx.y, own = blockIdx.x, tid = threadIdx.x, l = tid % WAVE;
   const int wv = __builtin_amdgcn_readfirstlane(tid / WAVE);
   Team& team = a.team[b];
-  const int pieces = a.slices * WV;
-  double* const part = a.part + (int64_t)b * pieces;
-  uint32_t next = tid == 0 ? shared_add(&team.ticket) : 0;
-  Walk w(a, b, wv == 0);      // (its loads are on their way while the first pass is waited for)
   const int nvec = (a.V + 3) / 4;
+  Walk w(a, b, wv == 0);      // wave 0 walks
 
-  for (;;) {
-    if (tid == 0) {
-      const uint32_t want = next / (uint32_t)a.slices;
-      uint32_t r = DONE;
-      for (int i = 0; i < a.polls; ++i) {
-        r = shared_load(&team.pass);
-        if (r == DONE || r >= want) break;
-        r = DONE;
-        __builtin_amdgcn_s_sleep(1);
-      }
-      settle();
-      place_sh = shared_load(&team.place), mode_sh = shared_load(&team.mode), cut_sh = shared_load(&team.cut);
-      ticket_sh = next, pass_sh = r;
+  // Wave 0: how it goes on, for the others.
+  auto tell = [&](Next go) {
+    if (l == 0) go_sh = go;
+    if (go != PASS) return;
+    if (l == 0) mode_sh = w.mode, cur_sh = w.cur, cut_sh = w.cut;
+    if (a.q) return;
+    // tokens that a draw without draft rows leaves out, each once
+    bool no = w.up == w.cur && l < w.child;
+    for (int i = 0; i < WAVE - 1; ++i) {
+      const int t = __builtin_amdgcn_readlane(w.tok, i);
+      if (__builtin_amdgcn_readlane((int)no, i) && l > i && w.tok == t) no = false;
     }
-    __syncthreads();
-    const uint32_t pass = pass_sh;
-    if (pass == DONE) return;
-    const int sl = (int)(ticket_sh % (uint32_t)a.slices);
-    const Rows rows(a, w.nd, place_sh, mode_sh, cut_sh);
-    if (tid < WAVE && !a.q) {
-      // tokens that a draw without draft rows leaves out, each once
-      const int cur = (int)(place_sh & 63u), child = (int)(place_sh >> 8 & 127u);
-      bool no = w.up == cur && l < child;
-      for (int i = 0; i < WAVE - 1; ++i) {
-        const int t = __builtin_amdgcn_readlane(w.tok, i);
-        if (__builtin_amdgcn_readlane((int)no, i) && l > i && w.tok == t) no = false;
-      }
-      const uint64_t m = __ballot(no);
-      if (no) gone_sh[__popcll(m & ((1ull << l) - 1))] = w.tok;
-      if (l == 0) gone_n = __popcll(m);
-    }
-    if (tid == 0) next = shared_add(&team.ticket);      // on its way while the rows are read
-    if (!a.q) __syncthreads();
+    const uint64_t m = __ballot(no);
+    if (no) gone_sh[__popcll(m & ((1ull << l) - 1))] = w.tok;
+    if (l == 0) gone_n = __popcll(m);
+  };
+  if (wv == 0) tell(w.valid() && w.advance(a) ? PASS : STOP);
+  __syncthreads();
+  if (go_sh == STOP) {
+    if (own == 0 && wv == 0) w.write(a, b, -1);
+    return;
+  }
+
+  uint64_t mine = 1ull << own;      // slices that this workgroup sums up
+  for (uint32_t pass = 0;; ++pass) {
     const int out = a.q ? 0 : gone_n;
+    const Rows rows(a, w.nd.first + cur_sh, mode_sh, cut_sh);
+    const uint32_t tag = pass + 1;
+    int held = -1;                  // the slice whose stretches' sums are in sums_sh
 
-    const int lo = min(nvec, (sl * WV + wv) * a.stretch), hi = min(nvec, lo + a.stretch);
-    double sum = 0.0;
-    bool bad = false;
-    for (int k0 = lo; k0 < hi; k0 += WAVE * US) {
-      float4 x[US], y[US];
-      rows.load<US>(k0 + l, WAVE, hi, x, y);
-      rows.rest<US>(k0, k0 + WAVE * US, k0 + l, WAVE, hi, x, y);
-      rows.drop<US>(gone_sh, out, k0, k0 + WAVE * US, k0 + l, WAVE, x);
-#pragma unroll
-      for (int u = 0; u < US; ++u) {
-        const float lowest = fminf(fminf(fminf(x[u].x, x[u].y), fminf(x[u].z, x[u].w)),
-                                   fminf(fminf(y[u].x, y[u].y), fminf(y[u].z, y[u].w)));
-        const float all = (x[u].x + x[u].y) + (x[u].z + x[u].w) + ((y[u].x + y[u].y) + (y[u].z + y[u].w));
-        bad |= !(lowest >= 0.0f) || !(all < INFINITY);
-        sum += rows.weight(x[u].x, y[u].x);
-        sum += rows.weight(x[u].y, y[u].y);
-        sum += rows.weight(x[u].z, y[u].z);
-        sum += rows.weight(x[u].w, y[u].w);
+    // A slice's stretches, one a wave.
+    auto sum_up = [&](int s) {
+      const int lo = min(nvec, (s * WV + wv) * a.stretch), hi = min(nvec, lo + a.stretch);
+      double sum = 0.0;
+      bool bad = false;
+      for (int k0 = lo; k0 < hi; k0 += WAVE * US) {
+        float4 x[US], y[US];
+        rows.load<US>(k0 + l, WAVE, hi, x, y);
+        rows.rest<US>(k0, k0 + WAVE * US, k0 + l, WAVE, hi, x, y);
+        rows.drop<US>(gone_sh, out, k0, k0 + WAVE * US, k0 + l, WAVE, x);
+        add_up<US>(rows, x, y, sum, bad);
       }
-    }
-    sum = wave_sum(bad ? (double)NAN : sum);
-    if (l == 0) shared_store(&part[sl * WV + wv], sum);
-    settle();
-    __syncthreads();
-    if (tid == 0) last_sh = shared_add(&team.left) == (pass + 1) * (uint32_t)a.slices - 1;
-    __syncthreads();
-    if (!last_sh) continue;
-
-    // The last of the pass.  Its total, in the order of the stretches.
-    const double mine = tid < pieces ? shared_load(&part[tid]) : 0.0;
-    const bool nan = __syncthreads_or(!(mine < INFINITY));
-    const double incl = wave_incl_scan(mine);
-    if (l == WAVE - 1) total_sh[wv] = incl;
-    __syncthreads();
-    double before = 0.0, total = 0.0;
+      sum = wave_sum(bad ? (double)NAN : sum);
+      if (l == 0) sums_sh[wv] = sum;
+      held = s;
+    };
+    auto slice_sum = [&] {          // in every thread, with its tag
+      double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < WV; ++i) {
-      if (i < wv) before += total_sh[i];
-      total += total_sh[i];
-    }
-    if (tid < WAVE) {
-      w.enter(team);
-      enum { STOP, DRAW, AGAIN } go = STOP;
-      const double v = (double)a.v[b];
-      if (nan) w.st |= SD_ST_NONFINITE;
-      if (w.valid()) {
-        if (w.mode == RESIDUAL && !(total > 0.0)) {
-          // p = q but for rounding: the draw is from p, after one more pass
-          w.st |= SD_ST_RESID_ZERO;
-          w.mode = PLAIN, w.child = WAVE;
-          go = AGAIN;
-        } else if (w.mode == RESIDUAL && __ballot(w.up == w.cur && l >= w.child)) {
-          w.Z = total;
-          if (w.advance(a)) go = AGAIN;
-        } else if (!(total > 0.0)) {
-          w.st |= SD_ST_NONFINITE;
-        } else {
-          if (!(v >= 0.0 && v < 1.0)) w.st |= SD_ST_BAD_PARAM;
-          else go = DRAW;
+      for (int i = 0; i < WV; ++i) sum += sums_sh[i];
+      return (__builtin_bit_cast(uint64_t, sum) & ~TAG) | tag;
+    };
+
+    uint64_t want = mine;
+    mine = 0;
+    for (int looks = 0, most = min(STEAL, a.polls);;) {
+      for (; want; want &= want - 1) {
+        const int s = __builtin_ctzll(want);
+        // the claim is under way while the slice is summed up
+        bool got = true;
+        if (tid == 0 && a.slices > 1) got = shared_claim(&team.claims[s], pass);
+        sum_up(s);
+        if (tid == 0) got_sh = got;
+        __syncthreads();
+        if (got_sh) {
+          mine |= 1ull << s;
+          if (tid == 0 && a.slices > 1) shared_store(&team.sums[pass % 2][s], slice_sum());
+        }
+        if (want & (want - 1)) __syncthreads();
+      }
+      if (!mine) return;
+      if (wv == 0) {
+        uint64_t bits = tag, missing = 0;
+        bool late = false;
+        for (;;) {
+          if (a.slices == 1) bits = l == 0 ? slice_sum() : tag;
+          else if (l < a.slices) bits = shared_load(&team.sums[pass % 2][l]);
+          late = __any((bits & TAG) > tag);
+          missing = __ballot((bits & TAG) != tag);
+          if (!missing || late || ++looks > most) break;
+          __builtin_amdgcn_s_sleep(1);
+        }
+        if (l == 0) missing_sh = missing;
+        // (others have gone on without this one, or it has given up)
+        if (late || (missing && most == a.polls)) {
+          if (l == 0) missing_sh = 0, go_sh = STOP, draw_sh = -1;
+        } else if (!missing) {
+          const double x = __builtin_bit_cast(double, bits & ~TAG);
+          const double incl = wave_incl_scan(x);
+          const double total = lane_read(incl, WAVE - 1);
+          const Next go = w.resume(a, __any(!(x < INFINITY)) ? (double)NAN : total);
+          tell(go);
+          // the draw: the slice whose sum takes the running one past t first (the
+          // last one with a weight, where rounding leaves t at the total)
+          int s = 0;
+          if (go == DRAW) {
+            const double t = (double)w.v * total;
+            const uint64_t past = __ballot(x > 0.0 && incl > t), some = __ballot(x > 0.0);
+            s = past ? __builtin_ctzll(past) : WAVE - 1 - __builtin_clzll(some);
+            const double before = lane_read(incl - x, s);
+            if (l == 0) t_sh = t - before, token_sh = INT_MAX, spare_sh = -1;
+          }
+          if (l == 0) draw_sh = s;
         }
       }
-      if (go == AGAIN) w.leave(team, pass + 1);
-      if (go == STOP) {
-        w.write(a, b, -1);
-        if (l == 0) shared_store(&team.pass, DONE);
-      }
-      if (l == 0) go_sh = go, piece_sh = INT_MAX, spare_sh = -1, token_sh = INT_MAX;
+      __syncthreads();
+      want = missing_sh;
+      if (!want) break;
+      most = a.polls;
+      __syncthreads();
     }
-    __syncthreads();
-    if (go_sh == 2) continue;
-    if (go_sh == 0) return;
+    if (go_sh == PASS) continue;
+    const int s = draw_sh;
+    if (s < 0 || !(mine >> s & 1)) return;      // another one's to finish
+    if (go_sh == STOP) {
+      if (wv == 0) w.write(a, b, -1);
+      return;
+    }
 
-    // The draw: the stretch whose part of the cumulative sum passes t first (the
-    // last one with a weight, where rounding leaves t at the total) ...
-    const double t = (double)a.v[b] * total;
-    if (mine > 0.0) {
-      if (before + incl > t) atomicMin(&piece_sh, tid);
-      atomicMax(&spare_sh, tid);
+    // The token: first its stretch ...
+    if (held != s) sum_up(s);
+    __syncthreads();
+    const double t = t_sh;
+    double base = 0.0, run = 0.0;
+    int piece = 0;
+#pragma unroll
+    for (int i = 0; i < WV; ++i) {
+      const double x = sums_sh[i];
+      // (once the running sum is past t, the stretch is found)
+      if (x > 0.0 && !(run > t)) base = run, piece = i;
+      run += x;
     }
-    __syncthreads();
-    const int piece = piece_sh < INT_MAX ? piece_sh : spare_sh;
-    __syncthreads();
-    if (tid == piece) base_sh = before + incl - mine, spare_sh = -1;
-    __syncthreads();
-    // ... and its token, a vector a thread at a time
-    double base = base_sh;
-    const int end = min(nvec, (piece + 1) * a.stretch);
-    for (int k0 = piece * a.stretch; k0 < end && token_sh == INT_MAX; k0 += NT) {
+    // ... and in it a vector a thread at a time
+    const int lo = min(nvec, (s * WV + piece) * a.stretch), hi = min(nvec, lo + a.stretch);
+    for (int k0 = lo; k0 < hi && token_sh == INT_MAX; k0 += NT) {
       float4 x[1], y[1];
       const int k = k0 + tid;
-      rows.load<1>(k, 0, end, x, y);
-      rows.rest<1>(k0, k0 + NT, k, 0, end, x, y);
+      rows.load<1>(k, 0, hi, x, y);
+      rows.rest<1>(k0, k0 + NT, k, 0, hi, x, y);
       rows.drop<1>(gone_sh, out, k0, k0 + NT, k, 0, x);
       double g[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) g[i] = rows.weight(at(x[0], i), at(y[0], i));
-      const double own = (g[0] + g[1]) + (g[2] + g[3]);
-      const double run = wave_incl_scan(own);
-      if (l == WAVE - 1) total_sh[wv] = run;
+      const double sum = (g[0] + g[1]) + (g[2] + g[3]);
+      const double incl = wave_incl_scan(sum);
+      if (l == WAVE - 1) run_sh[wv] = incl;
       __syncthreads();
-      double c = base + run - own, all = 0.0;
+      double c = base + incl - sum, all = 0.0;
 #pragma unroll
       for (int i = 0; i < WV; ++i) {
-        if (i < wv) c += total_sh[i];
-        all += total_sh[i];
+        if (i < wv) c += run_sh[i];
+        all += run_sh[i];
       }
       int pick = INT_MAX, some = -1;
 #pragma unroll
@@ -465,10 +488,7 @@ __global__ __launch_bounds__(NT) void k_sample_passes(SampleArgs a) {
       base += all;
       __syncthreads();
     }
-    if (tid < WAVE) {
-      w.write(a, b, token_sh < INT_MAX ? token_sh : spare_sh);
-      if (l == 0) shared_store(&team.pass, DONE);
-    }
+    if (wv == 0) w.write(a, b, token_sh < INT_MAX ? token_sh : spare_sh);
     return;
   }
 }
@@ -486,14 +506,12 @@ int check(const sd_tree_sample_args_t* p) {
   return SD_OK;
 }
 
-// Workgroups that share a request's rows: about two a CU in all, none with less
-// than 64 vectors a wave, and a stretch for every thread of the last at most.
+// Workgroups that share a request's rows: two a CU in all; none with less than 64
+// vectors a wave.
 int slices_of(const sd_tree_sample_args_t* p) {
   const int nvec = (p->V + 3) / 4;
-  return std::max(1, std::min({(512 + p->B - 1) / p->B, (nvec + NT - 1) / NT, NT / WV}));
+  return std::max(1, std::min({512 / p->B, (nvec + NT - 1) / NT, MAX_SLICES}));
 }
-
-size_t parts_bytes(const sd_tree_sample_args_t* p) { return (size_t)p->B * slices_of(p) * WV * sizeof(double); }
 
 }  // namespace
 
@@ -501,7 +519,7 @@ extern "C" int sd_tree_sample_workspace_bytes(const sd_tree_sample_args_t* args,
   if (!bytes) return SD_EINVAL;
   const int rc = check(args);
   if (rc) return rc;
-  *bytes = parts_bytes(args) + (size_t)args->B * sizeof(Team);
+  *bytes = (size_t)args->B * sizeof(Team);
   return SD_OK;
 }
 
@@ -542,8 +560,7 @@ extern "C" int sd_debug_tree_sample_polls(const sd_tree_sample_args_t* args, voi
   const int pieces = a.slices * WV;
   a.stretch = ((a.V + 3) / 4 + pieces - 1) / pieces;
   a.polls = polls;
-  a.part = static_cast<double*>(workspace);
-  a.team = reinterpret_cast<Team*>(static_cast<char*>(workspace) + parts_bytes(args));
+  a.team = static_cast<Team*>(workspace);
   a.accepted = out_accepted, a.path = out_path, a.out_tokens = out_tokens, a.status = out_status;
   hipStream_t st = static_cast<hipStream_t>(stream);
   hipLaunchKernelGGL(k_sample_begin, dim3(a.B), dim3(WAVE), 0, st, a);
