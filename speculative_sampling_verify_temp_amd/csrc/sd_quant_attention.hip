@@ -270,11 +270,15 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
   // int8 codes enter as (code + 128) 2^-24, the fp16 number whose bits they are
   // with the sign turned
   constexpr float UNIT = CODE == SD_I8 ? 0x1p24f : 1.0f, BIAS = CODE == SD_I8 ? 128.0f : 0.0f;
+  // 3 row tiles' queries would not fit the registers: they lie in LDS, which the join
+  // takes over
+  constexpr bool QL = MT > 2;
+  static_assert(!QL || RT * D / 2 <= (KG - 1) * RT * JR);
   __shared__ __align__(16) float join[(KG - 1) * RT * JR];
   __shared__ int odd_value;      // a node's value is infinite or not a number
-  const int tid = threadIdx.x, l = tid % WAVE, n = l & 15, g4 = l >> 4;
+  const int tid = threadIdx.x, lane = tid % WAVE;
   const int w = __builtin_amdgcn_readfirstlane(tid / WAVE), rg = w % RG, kg = w / RG;
-  Requests rq = requests<RT, KT>(a, l);
+  Requests rq = requests<RT, KT>(a, lane);
   int run, u0, u1;
   if (a.whole) {
     run = 0, u0 = 0, u1 = 0;
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
   if (a.whole) {
     const int b = blockIdx.x / (a.c.H * a.mts_max), seg = blockIdx.x % (a.c.H * a.mts_max);
     b0 = b & ~(WAVE - 1), f = b & (WAVE - 1);
-    if (b0) rq = requests<RT, KT>(a, b0 + l);
+    if (b0) rq = requests<RT, KT>(a, b0 + lane);
     const int mts = lane_read(rq.mts, f), nt = lane_read(rq.nt, f);
     if (seg % a.mts_max >= mts) return;
     in = (seg / a.mts_max * mts + seg % a.mts_max) * nt;
@@ -303,15 +307,11 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
     while (left >= lane_units(rq)) {
       left -= lane_units(rq);
       b0 += WAVE;
-      rq = requests<RT, KT>(a, b0 + l);
+      rq = requests<RT, KT>(a, b0 + lane);
     }
     f = __builtin_ctzll(__ballot(left < rq.incl));
     in = left - (f ? lane_read(rq.incl, f - 1) : 0);
   }
-
-  // offsets of a lane within 16 slots
-  const uint32_t slot_stride = (uint32_t)a.c.slot_stride;
-  const uint32_t kat = n * slot_stride + g4 * 16, vat = g4 * 4 * slot_stride + n * CB;
 
   while (u0 < u1) {
     const int units = lane_read(rq.incl, f) - (f ? lane_read(rq.incl, f - 1) : 0);
@@ -332,6 +332,14 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       const bool tree = t1 > cached;
       const int row0 = mt * RT + rg * 16 * MT;
       const QAttnArgs& a = args_again();
+      // (As if it were new: what follows from the lane alone would be kept over all
+      // loops, in more registers than there are.)
+      int l = lane;
+      asm volatile("" : "+v"(l));
+      const int n = l & 15, g4 = l >> 4;
+      // offsets of a lane within 16 slots
+      const uint32_t slot_stride = (uint32_t)a.c.slot_stride;
+      const uint32_t kat = n * slot_stride + g4 * 16, vat = g4 * 4 * slot_stride + n * CB;
 
       // The wave's rows: their nodes; queries as the B operand, lane (n, g4) holding
       // of row n the columns that it loads of a key, 64 (ks / 2) + 16 g4 + 8 (ks % 2)
@@ -455,6 +463,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       const int all_from = a.window ? first_seen(ctx + T - 1, a.window) : 0, sinks = a.sinks;
       if (tid == 0) odd_value = 0;
 
+      s16x8* const lds_q = (s16x8*)join + rg * MT * KS * WAVE + l;
       float cr[MT], bias[MT];      // what a product is times, and what it holds too much
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -478,9 +487,14 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
             if constexpr (DT == SD_BF16) q[m][ks][i] = (short)from_f32<SD_F16>(x);
             if constexpr (CODE == SD_I8) sum += x;
           }
+        if (QL && kg == m % KG) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) lds_q[(m * KS + ks) * WAVE] = q[m][ks];
+        }
         cr[m] = a.scale * LOG2E * UNIT / up;      // scores in base 2
         bias[m] = CODE == SD_I8 ? quad_sum(sum) * (BIAS / UNIT) : 0.0f;
       }
+      if constexpr (QL) __syncthreads();
       // Scores z, relative to ref, to weights 2^z as elements of type PT.
       auto weigh = [&](auto type, f32x4 (&z)[2][MT], const float (&iv)[2], s16x8 (&p)[MT]) {
         constexpr int PT = decltype(type)::value;
@@ -569,12 +583,12 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           s16x8 qf[KS];
-          if constexpr (DT == SD_BF16) queries(a, m, qf);
+          if constexpr (DT == SD_BF16 || QL) queries(a, m, qf);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             z[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) z[s][m] = mfma<DT>(kf[s][ks], DT == SD_BF16 ? qf[ks] : q[m][ks], z[s][m]);
+            for (int ks = 0; ks < KS; ++ks) z[s][m] = mfma<DT>(kf[s][ks], DT == SD_BF16 || QL ? qf[ks] : q[m][ks], z[s][m]);
           }
         }
 #pragma unroll
@@ -648,15 +662,22 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
                 for (int j = 0; j < 4; ++j) rk[s][i][j] = numbers(rk[s][i][j]);
           }
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
+          for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int m = 0; m < MT; ++m) z[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              const u32x2 e = widen<CODE>(rk[s][ks / 2][ks % 2 * 2]), g = widen<CODE>(rk[s][ks / 2][ks % 2 * 2 + 1]);
-              const s16x8 kf = __builtin_bit_cast(s16x8, u32x4{e[0], e[1], g[0], g[1]});
+          for (int ks = 0; ks < KS; ++ks) {
+            s16x8 kf[2];
 #pragma unroll
-              for (int m = 0; m < MT; ++m) z[s][m] = mfma<SD_F16>(kf, q[m][ks], z[s][m]);
+            for (int s = 0; s < 2; ++s) {
+              const u32x2 e = widen<CODE>(rk[s][ks / 2][ks % 2 * 2]), g = widen<CODE>(rk[s][ks / 2][ks % 2 * 2 + 1]);
+              kf[s] = __builtin_bit_cast(s16x8, u32x4{e[0], e[1], g[0], g[1]});
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const s16x8 x = QL ? lds_q[(m * KS + ks) * WAVE] : q[m][ks];
+#pragma unroll
+              for (int s = 0; s < 2; ++s) z[s][m] = mfma<SD_F16>(kf[s], x, z[s][m]);
             }
           }
           const int s0 = slot_of(t);
@@ -856,7 +877,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
     in = 0;
     if (++f == WAVE && u0 < u1) {
       f = 0, b0 += WAVE;
-      rq = requests<RT, KT>(a, b0 + l);
+      rq = requests<RT, KT>(a, b0 + lane);
     }
   }
 }
@@ -993,7 +1014,8 @@ template <int D, typename F>
 auto with_shape(int rows, F&& f) {
   if (rows <= 16) return f(Shape<D, 1, 1, 4, 2>{});
   if (rows <= 32) return f(Shape<D, 2, 1, 4, 2>{});
-  return f(Shape<D, 2, 2, 2, 2>{});
+  if ((rows + 95) / 96 * 5 > (rows + 63) / 64 * 4) return f(Shape<D, 2, 2, 2, 2>{});
+  return f(Shape<D, 3, 2, 2, 2>{});
 }
 
 // Workgroups that share the unit list: two a CU of 4 waves, one of 8.
