@@ -160,7 +160,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     N, _, D = q.shape
     qp, qn, qh, Hq = _heads(q, "q", q, N, D)
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out_q = q.new_empty(q.shape)
     elif out_q.shape != q.shape:
         raise ValueError("out_q must have q's shape")
     oqp, oqn, oqh, _ = _heads(out_q, "out_q", q, N, D)
@@ -172,7 +172,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     else:
         key = _heads(k, "k", q, N, D)
         if out_k is None:
-            out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            out_k = k.new_empty(k.shape)
         elif out_k.shape != k.shape:
             raise ValueError("out_k must have k's shape")
         okp, okn, okh, _ = _heads(out_k, "out_k", q, N, D)
