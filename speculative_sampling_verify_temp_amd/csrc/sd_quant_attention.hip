@@ -6,10 +6,11 @@
 // of its block.
 //
 // The rows that share a KV head (nodes x heads of its group) are packed into one
-// matrix.  A workgroup is four waves over the same 16 MT rows, each with keys of its
-// own, 32 slots at a time straight from the cache into registers: nothing is staged,
-// so the waves meet only at the end of a run.  Blocks and pages hold whole multiples
-// of 16 slots, so what addresses 16 of them is in scalar registers.
+// matrix.  A workgroup is four waves, in groups: those of one share 16 MT rows, and
+// each has keys of its own, 32 slots at a time straight from the cache into registers.
+// Nothing is staged, so the waves meet only at the end of a run; two groups read the
+// same keys at nearly the same time, one of them out of the L1.  Blocks and pages hold
+// whole multiples of 16 slots, so what addresses 16 of them is in scalar registers.
 //
 //   S^T = K . Q^T   a lane loads 16 bytes of a key and makes two operands of them;
 //                   the queries' columns are in the same order.
@@ -32,6 +33,17 @@
 // The (request, KV head, row tile, key tile) units form one list that is cut into
 // equal runs, one per workgroup; parts are joined in a fixed order.  Through a
 // window only the key tiles that it (or the sinks) touches are units.
+//
+// What bounds it is the issue of two waves a SIMD, 330 instructions for 32 keys of 32
+// rows: a third of them widen codes (each once a wave), half are the softmax, 34 matrix
+// products.  So rows are cheap where they share a widened key: 48 of them a wave do 400.
+//   32 chains of 9, 28/4 heads of 128, e4m3, 500-16384 slots    80 us + join 7   (bytes: 55)
+//   23 trees of 21, 16/8 heads, int8, fp16, window 4099         60 + 6           (bytes: 35)
+//   16 trees of 64, 28/4 heads, int8, 16384-32768 slots         440 + 11         (products: 251)
+//   1 token, 14/2 heads of 64, 517 slots                        8.6, latency
+// Tried without gain: three waves a SIMD (spills), two tiles on their way, keys widened
+// once into LDS for both groups, the products of a tile under the softmax of the one
+// before, loads that pass the caches by (98 instead of 82), 8 or 16 waves on one token.
 #include <algorithm>
 #include <type_traits>
 
@@ -45,6 +57,7 @@ namespace {
 
 constexpr int KEYS = 32;      // keys of a wave's step
 constexpr int TREE = 8;       // units that the tree of a row tile counts as
+constexpr int RUNS = 512;     // workgroups that share the unit list: two a CU, a multiple of 8
 constexpr float LIFT = 7.0f, LOG2E = 1.4426950408889634f;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -120,14 +133,14 @@ struct Cut {
 };
 
 template <int RT, int KT>
-__device__ __forceinline__ Cut cut_units(const QAttnArgs& a, const Requests& r, int runs) {
+__device__ __forceinline__ Cut cut_units(const QAttnArgs& a, const Requests& r) {
   int total = lane_units(r), nt = r.nt;
   for (int b0 = WAVE; b0 < a.c.B; b0 += WAVE) {
     const Requests q = requests<RT, KT>(a, b0 + (int)threadIdx.x % WAVE);
     total += lane_units(q);
     nt = max(nt, q.nt);
   }
-  return Cut{total, max((int)(((unsigned)total + runs - 1) / (unsigned)runs), (wave_max_int(nt) + 31) / 32)};
+  return Cut{total, max((int)(((unsigned)total + RUNS - 1) / (unsigned)RUNS), (wave_max_int(nt) + 31) / 32)};
 }
 
 // r / G for a packed row (exact: r < 2^11, G <= 32).
@@ -249,8 +262,7 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 }
 
 // MT row tiles of 16 a wave, RG groups of KG waves over the rows, each wave of a
-// group with 32 keys of a unit's.
-// OCC waves a SIMD at least.
+// group with 32 keys of a unit's.  OCC waves a SIMD at least.
 template <int D_, int MT_, int RG_, int KG_, int OCC_>
 struct Shape {
   static constexpr int OCC = OCC_;
@@ -285,9 +297,8 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
   } else {
     // Workgroups of one XCD take neighbouring runs: row tiles of one KV head
     // find each other's keys in its L2.
-    const int runs = gridDim.x;
-    const auto [total, per] = cut_units<RT, KT>(a, rq, runs);
-    run = (int)(blockIdx.x % 8) * (runs / 8) + (int)(blockIdx.x / 8);      // runs is a multiple of 8
+    const auto [total, per] = cut_units<RT, KT>(a, rq);
+    run = (int)(blockIdx.x % 8) * (RUNS / 8) + (int)(blockIdx.x / 8);
     if ((int64_t)run * per >= total) return;
     u0 = run * per, u1 = u0 + min(per, total - u0);
   }
@@ -886,11 +897,11 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
 // runs, JN at a time.  grid (4-column groups of a row tile / 256, H * row
 // tiles, B).
 template <int DT, typename S>
-__global__ __launch_bounds__(256) void k_quant_join(QAttnArgs a, int runs) {
+__global__ __launch_bounds__(256) void k_quant_join(QAttnArgs a) {
   constexpr int D = S::D, RT = S::RT, KT = S::KT, GPR = D / 4, JN = 8, SLOT = S::SLOT;
   const int b = blockIdx.z, h = blockIdx.y / a.mts_max, mt = blockIdx.y % a.mts_max, l = threadIdx.x % WAVE;
   Requests rq = requests<RT, KT>(a, l);
-  const int per = cut_units<RT, KT>(a, rq, runs).per;
+  const int per = cut_units<RT, KT>(a, rq).per;
   int before = 0;
   for (int b0 = 0; b0 + WAVE <= b; b0 += WAVE) {
     before += lane_units(rq);
@@ -1009,7 +1020,14 @@ QAttnArgs device_args(const sd_quant_attention_args_t* p) {
   return a;
 }
 
-// The shape for `rows` packed rows a KV head.
+// The shape for `rows` packed rows a KV head: the fewest row tiles that hold them,
+// the waves on different keys where they are few.  Above 64 rows 96 at a time take
+// 1.25 times as long as 64.  us for contexts of 500-16384 slots, 28/4 heads of 128:
+//   14 rows, 32 requests    55 (one token of 14/2 heads, 517 slots: 8.8), with 32-row tiles 58 (10.5)
+//   28 rows, 32 requests    58, with 64-row tiles 75
+//   42 rows, 24 requests    60, with 96-row tiles 77
+//   84 rows, 16 requests    63, with 64-row tiles 68
+//   126 rows, 16 requests   70, with 96-row tiles 89
 template <int D, typename F>
 auto with_shape(int rows, F&& f) {
   if (rows <= 16) return f(Shape<D, 1, 1, 4, 2>{});
@@ -1018,15 +1036,11 @@ auto with_shape(int rows, F&& f) {
   return f(Shape<D, 3, 2, 2, 2>{});
 }
 
-// Workgroups that share the unit list: two a CU of 4 waves, one of 8.
-template <typename S>
-constexpr int run_count() {
-  return S::NT == 512 ? 256 : 512;
-}
-
 // Where there are no more key tiles than this, splitting them and joining the
-// parts in a second launch costs more than it saves.
-constexpr int WHOLE_TILES = 7;
+// parts in a second launch costs more than it saves.  One token, tiles of 128 slots:
+// 1000 slots 9.9 us whole and 10.4 split, 2000 slots 14.4 and 13.3; 64 requests of 4
+// nodes and 500-900 slots 19 and 27.
+constexpr int WHOLE_TILES = 11;
 
 // How a call is cut up.
 struct Plan {
@@ -1055,16 +1069,15 @@ template <int DT, int CODE, int D>
 int launch(QAttnArgs a, const sd_quant_attention_args_t* p, hipStream_t st) {
   return with_shape<D>(a.max_nodes * a.G, [&](auto s) {
     using S = decltype(s);
-    constexpr int runs = run_count<S>();
     const Plan r = plan<S>(p);
     a.mts_max = r.mts_max;
     a.whole = r.whole;
-    hipLaunchKernelGGL((k_quant_tiles<DT, CODE, S>), dim3(a.whole ? (unsigned)r.segments : (unsigned)runs),
+    hipLaunchKernelGGL((k_quant_tiles<DT, CODE, S>), dim3(a.whole ? (unsigned)r.segments : (unsigned)RUNS),
                        dim3(S::NT), 0, st, a);
     if (hipGetLastError() != hipSuccess) return SD_EHIP;
     if (a.whole) return SD_OK;
     const dim3 grid((S::RT * (D / 4) + 255) / 256, a.c.H * a.mts_max, a.c.B);
-    hipLaunchKernelGGL((k_quant_join<DT, S>), grid, dim3(256), 0, st, a, runs);
+    hipLaunchKernelGGL((k_quant_join<DT, S>), grid, dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? SD_OK : SD_EHIP;
   });
 }
@@ -1079,7 +1092,7 @@ extern "C" int sd_quant_attention_workspace_bytes(const sd_quant_attention_args_
   auto size = [&](auto s) {
     using S = decltype(s);
     const Plan p = plan<S>(args);
-    *bytes = p.whole ? 0 : (size_t)run_count<S>() * 2 * S::SLOT * sizeof(float);
+    *bytes = p.whole ? 0 : (size_t)RUNS * 2 * S::SLOT * sizeof(float);
     return p.fits ? SD_OK : SD_EUNSUPPORTED;
   };
   return args->cache.D == 64 ? with_shape<64>(rows, size) : with_shape<128>(rows, size);

@@ -8,6 +8,8 @@
 // and cosines are computed once, into LDS, while the rows are on their way.
 // D / 16 lanes share a row, 16 elements each: a lane's two vectors hold both
 // elements of its pairs, so a row needs no exchange but the sum of squares.
+// 16411 tokens of 28 + 4 heads of 128: 49 us, 5.5 TB/s; 288 tokens of 16 + 8 heads:
+// 4.2 us; one token of 14 + 2 heads of 64: 2.4 us.
 #include <algorithm>
 
 #include "sd_serve.h"

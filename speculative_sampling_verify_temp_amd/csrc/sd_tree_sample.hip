@@ -8,7 +8,11 @@
 //
 // So a request makes one pass over the rows of a node for each rejection on its
 // walk, and one for the draw where nothing was rejected at its last node.  Bound
-// by those rows' bytes in large batches, by a pass's latency in small ones.
+// by the latency of passes that follow each other: at a pass's end what a wave sums up
+// travels to the others and back, some 4 us, and the longest walk of a batch has
+// several.  Rows of 151936: 1 tree of 16 nodes 15 us; 64 trees of 20, draws without
+// replacement, up to 4 passes, 40 us (their bytes alone: 15); 48 trees of a beam, one
+// pass each, 21 us (6).
 //
 // k_sample_begin    clears what the teams share.
 // k_sample_passes   teams of workgroups, one a slice of the vocabulary; each of their
@@ -38,7 +42,8 @@ namespace {
 
 constexpr int NT = 512;               // threads of a workgroup
 constexpr int WV = NT / WAVE;
-constexpr int US = 4;                 // vectors of each row that a lane loads at once
+constexpr int US = 4;                 // vectors of each row that a lane loads at once (2: 39-22 us in the
+                                      // last two cases above, 8: 44-22; two such rounds on their way: 42-22)
 constexpr int MAX_SLICES = WAVE;      // (a lane looks at each)
 constexpr uint64_t TAG = 127;         // of a sum; passes are SD_MAX_NODES + 1 at most: every node's
                                       // rejection but the root's, a draw, one more after a total of 0
@@ -506,8 +511,8 @@ int check(const sd_tree_sample_args_t* p) {
   return SD_OK;
 }
 
-// Workgroups that share a request's rows: two a CU in all; none with less than 64
-// vectors a wave.
+// Workgroups that share a request's rows: two a CU in all (one: 45 instead of 40 us
+// in the case of 64 trees); none with less than 64 vectors a wave.
 int slices_of(const sd_tree_sample_args_t* p) {
   const int nvec = (p->V + 3) / 4;
   return std::max(1, std::min({512 / p->B, (nvec + NT - 1) / NT, MAX_SLICES}));
