@@ -64,7 +64,7 @@ typedef struct sd_qk_norm_rope_args {
   const int32_t *positions;      /* [N]                                         */
   const float   *inv_freq;       /* [rot / 2]                                   */
   int32_t        dtype;          /* SD_BF16 or SD_F16                           */
-  int32_t        N;              /* >= 1                                        */
+  int32_t        N;              /* >= 1; from 2^24 on only with few heads      */
   int32_t        H_q;            /* >= 1; H_q + H_k <= 65535                    */
   int32_t        H_k;            /* >= 0                                        */
   int32_t        D;              /* 64, 128 or 256                              */
@@ -180,7 +180,7 @@ typedef struct sd_quant_append_args {
   int32_t        dtype;          /* of the new rows: SD_BF16 or SD_F16          */
   int32_t        N;
   int32_t        max_new;        /* nodes of a request, at most; with a path
-                                    <= SD_MAX_NODES                             */
+                                    <= SD_MAX_NODES; less than 2^24 blocks      */
 } sd_quant_append_args_t;
 
 int sd_quant_append(const sd_quant_append_args_t *args, int32_t *out_context,

@@ -144,6 +144,7 @@ __global__ __launch_bounds__(NT) void k_append(AppendArgs a) {
   if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
     a.out_ctx[b] = (nw.st & SD_ST_BAD_LEN) ? a.c.lens[b] : nw.ctx + nw.m;
   const int block = 1 << a.c.block_shift;
+  if (nw.m <= 0 || (int)blockIdx.x > ((nw.m - 1) >> a.c.block_shift) + 1) return;      // past what the rows can touch
   const int start = (nw.ctx & -block) + blockIdx.x * block;
   const int lo = max(nw.ctx, start) - start, hi = min(nw.ctx + nw.m - start, block);      // the block's new slots
   if (lo >= hi) return;
@@ -265,10 +266,9 @@ int check(const sd_quant_append_args_t* p) {
 
 // One wave a block where its rows fit the registers of one.
 template <int DT, int CODE, int D>
-void launch(const AppendArgs& a, hipStream_t st) {
+void launch(const AppendArgs& a, unsigned blocks, hipStream_t st) {
   const int block = 1 << a.c.block_shift;
-  const int most = std::min(a.max_new, a.c.cap);
-  const dim3 grid((unsigned)((most - 1) / block + 2), 2 * a.c.H, a.c.B);
+  const dim3 grid(blocks, 2 * a.c.H, a.c.B);
   if (block * (D / 8) <= WAVE * UA)
     hipLaunchKernelGGL((k_append<DT, CODE, D, WAVE>), grid, dim3(WAVE), 0, st, a);
   else
@@ -292,14 +292,17 @@ extern "C" int sd_quant_append(const sd_quant_append_args_t* p, int32_t* out_con
   a.path = p->path, a.ld_path = p->ld_path, a.path_lens = p->path_lens;
   a.N = p->N, a.max_new = p->max_new;
   a.out_ctx = out_context, a.status = out_status;
+  // a grid dimension holds less than 2^32 threads
+  const int blocks = ((std::min(a.max_new, a.c.cap) - 1) >> a.c.block_shift) + 2;
+  if (blocks >= 1 << 24) return SD_EUNSUPPORTED;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (out_status) {
     hipLaunchKernelGGL(k_append_status, dim3(a.c.B), dim3(WAVE), 0, st, a);
     if (hipGetLastError() != hipSuccess) return SD_EHIP;
   }
   auto go = [&](auto dt, auto code) {
-    if (p->cache.D == 64) launch<decltype(dt)::value, decltype(code)::value, 64>(a, st);
-    else launch<decltype(dt)::value, decltype(code)::value, 128>(a, st);
+    if (p->cache.D == 64) launch<decltype(dt)::value, decltype(code)::value, 64>(a, (unsigned)blocks, st);
+    else launch<decltype(dt)::value, decltype(code)::value, 128>(a, (unsigned)blocks, st);
   };
   using BF = std::integral_constant<int, SD_BF16>;
   using HF = std::integral_constant<int, SD_F16>;

@@ -195,6 +195,8 @@ extern "C" int sd_qk_norm_rope(const sd_qk_norm_rope_args_t* p, void* stream) {
   // than the table holds
   const int rpp = NT_R / (p->D / 16);
   a.tokens = std::max(1, std::min(rpp / a.H, MAX_TURNS / (a.rot / 2)));
+  // a grid dimension holds less than 2^32 threads
+  if (p->N / a.tokens >= (1 << 24) - 1) return SD_EUNSUPPORTED;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool bf = p->dtype == SD_BF16, pairs = p->interleaved != 0;
   if (p->D == 64) bf ? launch<SD_BF16, 64>(a, pairs, st) : launch<SD_F16, 64>(a, pairs, st);

@@ -161,6 +161,17 @@ def test_bad_arguments_are_refused(sdv, kind, field, value, code):
     assert _call(sdv, kind, a) == code
 
 
+def test_grids_beyond_the_limits_are_refused(sdv):
+    """More workgroups than a grid holds: neither call writes anything."""
+    a = _rope()
+    a.N = 2 ** 31 - 1
+    assert _call(sdv, "rope", a) == -4
+    a = _append()
+    a.path, a.max_new = None, 2 ** 28
+    a.cache.max_pages = a.cache.ld_table = 2 ** 26
+    assert _call(sdv, "append", a) == -4
+
+
 def test_sizes_beyond_the_limits_are_refused(sdv):
     a = _append()
     a.max_new = a.ld_path = 65
