@@ -234,3 +234,57 @@ def test_results_repeat_and_graphs_replay():
             g.replay()
         torch.cuda.synchronize()
         assert torch.equal(want[0], res[0]) and torch.equal(want[1], res[1])
+
+
+@pytest.mark.parametrize("far", ["pages", "heads"])
+def test_caches_past_4_gib(far):
+    """Pages, or heads, further apart than 32 bits reach: appended to and attended as
+    the same cache close together, on a stream of its own."""
+    import torch
+    sdv = _sdv()
+    names = ("k_cache", "v_cache", "k_scale", "v_scale")
+    s = Quantised(19, [150, 61], [9, 5], Hq=4, Hkv=2, D=128, page=32, block=16, room=16)
+    near = s.d
+    pool, H, page, D = near["k_cache"].shape
+    wide = dict(near)
+    stride = (5 << 30) // (pool if far == "pages" else 1) & -16
+    strides = (stride, page * D, D, 1) if far == "pages" else (page * D, stride, D, 1)
+    for n in names[:2]:
+        buf = torch.empty(stride * ((pool if far == "pages" else H) - 1) + pool * H * page * D, dtype=torch.int8, device="cuda")
+        wide[n] = buf.as_strided(near[n].shape, strides)
+        wide[n].copy_(near[n])
+    for n in names[2:]:
+        wide[n] = near[n].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    res = []
+    for d, st in ((near, None), (wide, side)):
+        lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        sdv.quant_append(d["k_new"], d["v_new"], *(d[n] for n in names), d["page_table"], d["context_lens"],
+                         d["node_offsets"], 9, lens, stream=st)
+        res.append(sdv.quant_attention(d["q"], d["k_new"], d["v_new"], *(d[n] for n in names), d["page_table"], lens,
+                                       d["node_offsets"], 9, want_lse=True, stream=st))
+        torch.cuda.synchronize()
+        assert lens.tolist() == [159, 66]
+    for n in names:
+        assert torch.equal(near[n].contiguous().view(torch.uint8), wide[n].contiguous().view(torch.uint8)), n
+    assert all(torch.equal(a, b) for a, b in zip(*res)) and torch.isfinite(res[0][0]).all()
+
+
+def test_requests_that_share_pages_and_calls_at_once():
+    """A prefix held once for all requests, and calls on streams and workspaces of
+    their own at the same time."""
+    import torch
+    s = Quantised(20, [700] * 5, [3] * 5, Hq=14, Hkv=2, D=64, page=64, block=64, code="e4m3")
+    s.table[:, :6] = s.table[0, :6]
+    s.d["page_table"].copy_(dev(s.table))
+    out, lse = _run(s)
+    s.check(out, lse, s.reference())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(3):
+        got = [_run(s, stream=st) for st in streams]
+        torch.cuda.synchronize()
+        for o, e in got:
+            assert torch.equal(o, out) and torch.equal(e, lse)

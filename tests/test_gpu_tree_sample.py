@@ -338,3 +338,21 @@ def test_in_a_graph_and_on_a_stream():
             g.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(w, out[n]) for w, n in zip(want, ("accepted", "path", "tokens")))
+
+
+def test_rows_past_2_to_the_32_elements():
+    import torch
+    t = Trees(14, [5, 1], 1500, "again")
+    d = t.device()
+    ref = _sdv().tree_verify_sample(**d)
+    ld = (1 << 30) + 4      # row 4 begins past 2^32 elements, row 1 past 2^32 bytes
+    buf = torch.empty(5 * ld + 4096, dtype=torch.float32, device="cuda")
+    for name, at in (("target_probs", 0), ("draft_probs", 2048)):
+        x = buf.as_strided((t.N, 1500), (ld, 1), at)
+        x.copy_(d[name])
+        d[name] = x
+    for flags in (0, 1):
+        got = _sdv().tree_verify_sample(**d, flags=flags)
+        want = _sdv().tree_verify_sample(**{**d, "target_probs": _padded(t.p), "draft_probs": t.device()["draft_probs"]}, flags=flags)
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    assert all(torch.equal(g, w) for g, w in zip(_sdv().tree_verify_sample(**d), ref))
