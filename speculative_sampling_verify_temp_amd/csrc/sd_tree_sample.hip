@@ -12,7 +12,7 @@
 // travels to the others and back, some 4 us, and the longest walk of a batch has
 // several.  Rows of 151936: 1 tree of 16 nodes 15 us; 64 trees of 20, draws without
 // replacement, up to 4 passes, 40 us (their bytes alone: 15); 48 trees of a beam, one
-// pass each, 21 us (6).
+// pass each, 19 us (6).
 //
 // k_sample_begin    clears what the teams share.
 // k_sample_passes   teams of workgroups, one a slice of the vocabulary; each of their
@@ -281,9 +281,10 @@ struct Rows {
   // The weights of the n tokens `gone` taken out of the vectors [first, last).
   template <int U>
   __device__ static void drop(const int* gone, int n, int first, int last, int k0, int step, float4 (&x)[U]) {
-    for (int j = 0; j < n; ++j) {
-      const int e = gone[j];
-      if (e / 4 < first || e / 4 >= last) continue;
+    if (!n) return;
+    const int l = threadIdx.x % WAVE, mine = l < n ? gone[l] : -1;
+    for (uint64_t in = __ballot(mine >= 0 && mine / 4 >= first && mine / 4 < last); in; in &= in - 1) {
+      const int e = __builtin_amdgcn_readlane(mine, __builtin_ctzll(in));
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = e - 4 * (k0 + u * step);
@@ -334,9 +335,9 @@ __global__ __launch_bounds__(NT, 4) void k_sample_passes(SampleArgs a) {
     if (a.q) return;
     // tokens that a draw without draft rows leaves out, each once
     bool no = w.up == w.cur && l < w.child;
-    for (int i = 0; i < WAVE - 1; ++i) {
-      const int t = __builtin_amdgcn_readlane(w.tok, i);
-      if (__builtin_amdgcn_readlane((int)no, i) && l > i && w.tok == t) no = false;
+    for (uint64_t some = __ballot(no); some; some &= some - 1) {
+      const int i = __builtin_ctzll(some);
+      if (l > i && w.tok == __builtin_amdgcn_readlane(w.tok, i)) no = false;
     }
     const uint64_t m = __ballot(no);
     if (no) gone_sh[__popcll(m & ((1ull << l) - 1))] = w.tok;
