@@ -42,8 +42,8 @@ namespace {
 
 constexpr int NT = 512;               // threads of a workgroup
 constexpr int WV = NT / WAVE;
-constexpr int US = 4;                 // vectors of each row that a lane loads at once (2: 39-22 us in the
-                                      // last two cases above, 8: 44-22; two such rounds on their way: 42-22)
+constexpr int US = 4;                 // vectors of each row that a lane loads at once (in the last two cases
+                                      // above 2 take 1 us less and 1 more, 8 take 5 and 2 more)
 constexpr int MAX_SLICES = WAVE;      // (a lane looks at each)
 constexpr uint64_t TAG = 127;         // of a sum; passes are SD_MAX_NODES + 1 at most: every node's
                                       // rejection but the root's, a draw, one more after a total of 0
