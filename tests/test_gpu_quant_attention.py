@@ -288,3 +288,33 @@ def test_requests_that_share_pages_and_calls_at_once():
         torch.cuda.synchronize()
         for o, e in got:
             assert torch.equal(o, out) and torch.equal(e, lse)
+
+
+@pytest.mark.parametrize("nodes,Hq,Hkv", [([13, 20, 27], 14, 2), ([64, 33, 5], 8, 2), ([64, 1, 50], 3, 1)])
+def test_more_rows_than_a_row_tile(nodes, Hq, Hkv):
+    """65 to 256 rows a KV head: codes that are not numbers in the cache, infinities
+    and NaN in nodes that only their descendants see, in place of the queries."""
+    import torch
+    s = Quantised(21, [900, 300, 2000], nodes, Hq=Hq, Hkv=Hkv, D=128, code="e4m3", page=32, block=32)
+    parents = _parents(s)
+    for b in range(3):      # the last node: nobody else sees it
+        parents[s.offsets[b + 1] - 1] = 0 if nodes[b] > 1 else -1
+    p = s.table
+    s.k[p[0, 3], 0, 5, 7] = np.nan
+    s.v[p[2, 40], Hkv - 1, 30, 127] = np.nan
+    s.d["k_cache"], s.d["v_cache"] = code_dev(s.k, "e4m3"), code_dev(s.v, "e4m3")
+    ref = s.reference(parents)
+    last = [int(o) - 1 for o in s.offsets[1:]]
+    s.vn[last[0], 0, 5], s.vn[last[2], Hkv - 1, 127] = np.inf, np.nan
+    s.d["v_new"] = dev(s.vn, torch.bfloat16)
+    out, lse = _run(s, parents)
+    o = out.double().cpu().numpy()
+    G = Hq // Hkv
+    touched = np.zeros(o.shape, dtype=bool)
+    touched[last[0], :G, 5] = touched[last[2], Hq - G:, 127] = True
+    assert (o[last[0], :G, 5] == np.inf).all() and np.isnan(o[last[2], Hq - G:, 127]).all()
+    s.vn = np.nan_to_num(s.vn, posinf=1)
+    s.check(torch.from_numpy(np.where(touched, ref[0], o)), lse, ref)
+    q = s.d["q"] = s.d["q"].contiguous()
+    got, again = _run(s, parents, out=q)
+    assert torch.equal(got.nan_to_num(), out.nan_to_num()) and torch.equal(again, lse)
