@@ -206,14 +206,16 @@ int sd_quant_append(const sd_quant_append_args_t *args, int32_t *out_context,
  * draft_probs NULL: children are not drawn but given (a beam's).  A child with
  * token x is accepted if u * Z < p(x), where Z = 1 - the sum of p over the tokens
  * rejected so far at c (a rejected token has p = 0 from then on); the last token
- * is drawn from p without the rejected tokens.
+ * is drawn from p without the rejected tokens.  Where they were all that p holds (its
+ * numbers sum to 1 only within rounding, so even the last of them can be rejected),
+ * SD_ST_RESID_ZERO is set and the token is drawn from p.
  * Arithmetic is in 64 bits.  Outputs as in sd_tree_verify_greedy: out_accepted
  * [B], out_path [B][max_nodes], out_tokens [B][max_nodes]; with SD_NO_BONUS the
  * last token is left out where the walk ends at a node without children.
  * Only what the walk uses is examined.  Invalid: SD_ST_BAD_NODES,
  * SD_ST_BAD_DRAFT_ID (a drafted token outside [0, V)), SD_ST_BAD_PARAM (a used
  * random number outside [0, 1)), SD_ST_NONFINITE (a used probability that is
- * negative or not finite, or a total of 0 at the last draw), SD_ST_UNFINISHED:
+ * negative or not finite, or a total of 0 of p itself), SD_ST_UNFINISHED:
  * -1 everywhere.
  * ------------------------------------------------------------------------ */
 typedef struct sd_tree_sample_args {

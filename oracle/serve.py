@@ -172,10 +172,12 @@ def tree_sample_ref(p, q, tokens, parents, offsets, max_nodes, u, v, no_bonus=Fa
                     Z -= left[x]
                     left[x] = 0.0
             if took is None:
+                if kids and not left.any():      # (without draft rows: all that p holds was given and rejected)
+                    left = P.copy()
                 C = np.cumsum(left)
                 t = float(v[b]) * C[-1]
                 out[b, n] = min(int(np.searchsorted(C, t, side="right")), V - 1)
-                while left[out[b, n]] == 0:      # rounding at the last of the sum
+                while out[b, n] > 0 and left[out[b, n]] == 0:      # rounding at the last of the sum
                     out[b, n] -= 1
                 if v[b] > 0:
                     margin[b] = min(margin[b], np.abs(C[C > 0] - t).min())

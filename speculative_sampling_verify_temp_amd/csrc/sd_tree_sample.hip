@@ -193,13 +193,17 @@ struct Walk {
       st |= SD_ST_NONFINITE;
       return STOP;
     }
-    if (mode == RESIDUAL && !(total > 0.0)) {
-      // p = q but for rounding: the draw is from p, after one more pass
+    const bool resid = mode == RESIDUAL;
+    if (!(total > 0.0) && (resid || (!a.q && __any(up == cur && l < child)))) {
+      // p = q but for rounding, or every token that p holds was given and rejected, since
+      // its numbers sum to 1 only within rounding: the draw is from all of p, after
+      // one more pass
       st |= SD_ST_RESID_ZERO;
-      mode = PLAIN, child = WAVE;
+      mode = PLAIN;
+      child = resid ? WAVE : 0;      // (without draft rows the tokens before it are left out)
       return PASS;
     }
-    if (mode == RESIDUAL && __ballot(up == cur && l >= child)) {
+    if (resid && __ballot(up == cur && l >= child)) {
       Z = total;
       return advance(a) ? PASS : STOP;
     }

@@ -356,3 +356,42 @@ def test_rows_past_2_to_the_32_elements():
         want = _sdv().tree_verify_sample(**{**d, "target_probs": _padded(t.p), "draft_probs": t.device()["draft_probs"]}, flags=flags)
         assert all(torch.equal(g, w) for g, w in zip(got, want))
     assert all(torch.equal(g, w) for g, w in zip(_sdv().tree_verify_sample(**d), ref))
+
+
+@pytest.mark.parametrize("V", [1003, 20011])
+def test_a_beams_row_whose_whole_support_was_drafted(V):
+    """Without draft rows Z is 1 less the rejected p, and a row's fp32 numbers sum to 1
+    only within rounding: the last of its tokens can be rejected too, and nothing is left
+    to draw from.  Reported, and the draw is from p."""
+    import torch
+    sdv = _sdv()
+    B, T = 40, 4
+    last = np.float32(1 - 2.0 ** -24)
+    p = np.zeros((B * T, V), dtype=np.float32)
+    a, b = 3, V - 2
+    p[:, a], p[:, b] = 0.5, np.float32(0.5 - 2.0 ** -25)
+    parents = np.tile([-1, 0, 0, 0], B).astype(np.int32)
+    tokens = np.tile([0, a, b, a], B).astype(np.int32)      # (one of them twice)
+    u = np.full(B * T, last, dtype=np.float32)
+    for r in range(0, B, 4):       # the same below the root's first child
+        parents[r * T + 2], parents[r * T + 3] = 1, 1
+        u[r * T + 1] = 0.0
+        tokens[r * T + 2:r * T + 4] = a, b
+    rows = p.copy()                # the oracle's
+    p[7 * T] = 0                   # nothing to draw from even so
+    off = (np.arange(B + 1) * T).astype(np.int32)
+    v = np.random.default_rng(15).random(B).astype(np.float32)
+    st = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    for B2 in (B, 2):
+        n = B2 * T
+        acc, path, tok = sdv.tree_verify_sample(_padded(p[:n]), dev(tokens[:n]), dev(parents[:n]), dev(off[:B2 + 1]), T,
+                                                dev(u[:n]), dev(v[:B2]), status=st[:B2])
+        want = oracle.tree_sample_ref(rows[:n], None, tokens[:n], parents[:n], off[:B2 + 1], T, u[:n], v[:B2])
+        ok = np.arange(B2) != 7
+        for g, w in zip((acc, path, tok), want):
+            assert np.array_equal(g.cpu().numpy()[ok], w[ok])
+            assert (g.cpu().numpy()[~ok] == -1).all()
+        assert (st[:B2].cpu().numpy()[ok] == sdv.SD_ST_RESID_ZERO).all()
+        assert all(s & sdv.SD_ST_NONFINITE for s in st[:B2].cpu().numpy()[~ok])
+        deep = np.arange(B2) % 4 == 0
+        assert (want[0] == deep)[ok].all() and set(want[2][np.arange(B2), want[0]][ok]) <= {a, b}

@@ -183,3 +183,13 @@ def test_given_children_keep_the_law():
     assert call(0.51, 0.21, 0.51)[2][0, 0] == 3
     acc, path, out, _ = oracle.tree_sample_ref(p, None, tok, up, off, 3, np.array([0, 0.1, 0]), np.array([0.6]), no_bonus=True)
     assert acc[0] == 1 and path[0].tolist() == [0, 1, -1] and out[0].tolist() == [0, -1, -1]
+
+
+def test_given_children_that_are_all_of_p():
+    """The last of them can be rejected where p sums up to less than 1: the draw is from p."""
+    p = np.array([[0.5, 0.0, 0.5 - 2.0 ** -25]] * 3)
+    tok, up, off = np.array([0, 0, 2]), np.array([-1, 0, 0]), np.array([0, 3])
+    u = np.array([0, 1 - 2.0 ** -24, 1 - 2.0 ** -24])
+    for v, want in ((0.0, 0), (0.4, 0), (0.6, 2), (1 - 2.0 ** -24, 2)):
+        acc, path, out, _ = oracle.tree_sample_ref(p, None, tok, up, off, 3, u, np.array([v]))
+        assert acc[0] == 0 and path[0].tolist() == [0, -1, -1] and out[0].tolist() == [want, -1, -1]
