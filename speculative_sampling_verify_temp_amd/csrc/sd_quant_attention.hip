@@ -403,10 +403,12 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
         key_at = a.c.ks + sc, value_at = a.c.vs + sc;
       };
       auto look_up_scales = [&]() {
-        const float k = *key_at, v = *value_at;
+        // the key's scale with all that a product is times but the row's 1 / up, which passes
+        // fp32's range beside 2^24 for queries near the largest of their type
+        const float k = *key_at, v = *value_at, c = args_again().scale * LOG2E;
         const bool sound = sdq::scale_ok(k) && sdq::scale_ok(v), none = v == 0.0f;
         const float x = sound && !none ? v : sdq::MIN_SCALE;
-        key_scale = sound ? k : 0.0f;
+        key_scale = sound ? k * UNIT * c : 0.0f;
         value_log = __builtin_amdgcn_logf(x);
         value_inv = __builtin_amdgcn_rcpf(x);
         there = (sound ? there : 0) | (none ? 256 : 0);
@@ -475,7 +477,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
       if (tid == 0) odd_value = 0;
 
       s16x8* const lds_q = (s16x8*)join + rg * MT * KS * WAVE + l;
-      float cr[MT], bias[MT];      // what a product is times, and what it holds too much
+      float cr[MT], bias[MT];      // what a product is times beside the key's scale, and what it holds too much
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         float up = 1.0f;
@@ -502,7 +504,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) lds_q[(m * KS + ks) * WAVE] = q[m][ks];
         }
-        cr[m] = a.scale * LOG2E * UNIT / up;      // scores in base 2
+        cr[m] = 1.0f / up;
         bias[m] = CODE == SD_I8 ? quad_sum(sum) * (BIAS / UNIT) : 0.0f;
       }
       if constexpr (QL) __syncthreads();

@@ -2,8 +2,9 @@
 import numpy as np
 import pytest
 
+import oracle
 from servetools import Quantised, code_dev
-from treetools import dev, random_tree, torch_dtype
+from treetools import dev, random_tree, rounded, torch_dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -318,3 +319,28 @@ def test_more_rows_than_a_row_tile(nodes, Hq, Hkv):
     q = s.d["q"] = s.d["q"].contiguous()
     got, again = _run(s, parents, out=q)
     assert torch.equal(got.nan_to_num(), out.nan_to_num()) and torch.equal(again, lse)
+
+
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_near_the_largest_of_their_type(D, code):
+    """bf16 queries of up to 2^126 over small keys: scores of 2^80 and more, but numbers.
+    One key has all the weight: its value, off by half a step of the result and of the
+    weight in fp16, 2^-20 for the rest; lse within the scores' error."""
+    import torch
+    s = Quantised(30, [300, 45], [3, 1], Hq=8, Hkv=2, D=D, code=code, page=32, block=16)
+    for x in (s.ks, s.vs):
+        x[~np.isfinite(x)] = 1.0
+    s.ks = (s.ks * np.float32(2.0 ** -43)).astype(np.float32)
+    big = 2.0 ** np.array([110.0, 121.0, 123.0, 124.0])
+    s.q = rounded(s.q * big[:, None, None], "bf16")
+    s.kn = rounded(s.kn * 2.0 ** -100, "bf16")
+    s.d.update(q=dev(s.q, torch.bfloat16), k_new=dev(s.kn, torch.bfloat16), k_scale=dev(s.ks))
+    out, lse = _run(s)
+    o, e, mag = s.reference()
+    es = (D + 8) * 2.0 ** -24 * s.scale * D * np.abs(s.q).max(-1) * s.ks.max() * oracle.serve.TOP[code]
+    assert (e > 2.0 ** 60).all() and np.isfinite(e).all()
+    assert (np.abs(mag - np.abs(o)) <= 2.0 ** -40 * mag).all()       # one key alone, by far
+    got = out.double().cpu().numpy()
+    assert (np.abs(got - o) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20) * np.abs(o)).all()
+    assert (np.abs(lse.double().cpu().numpy() - e) <= es + 2.0 ** -22 * e).all()
