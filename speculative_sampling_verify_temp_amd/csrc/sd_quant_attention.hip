@@ -27,8 +27,9 @@
 // fp16, whatever the queries' type: 11 bits, held at 2^7 of the running maximum, so
 // that a long tail beside one dominating key keeps its precision down to 2^-21 of
 // it.  Those of the nodes, whose values may pass fp16's range, are of the queries'
-// type.  They are divided by their fp32 sum: the rounded ones' would miss tokens whose
-// weight is large but whose w is not, beside values of a far larger scale.
+// type, in two parts: one node often dominates its row.  They are divided by their
+// fp32 sum: the rounded ones' would miss tokens whose weight is large but whose w is
+// not, beside values of a far larger scale.
 //
 // The (request, KV head, row tile, key tile) units form one list that is cut into
 // equal runs, one per workgroup; parts are joined in a fixed order.  Through a
@@ -508,7 +509,8 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
         bias[m] = CODE == SD_I8 ? quad_sum(sum) * (BIAS / UNIT) : 0.0f;
       }
       if constexpr (QL) __syncthreads();
-      // Scores z, relative to ref, to weights 2^z as elements of type PT.
+      // Scores z, relative to ref, to weights 2^z as elements of type PT; z holds what the
+      // rounding of them left.
       auto weigh = [&](auto type, f32x4 (&z)[2][MT], const float (&iv)[2], s16x8 (&p)[MT]) {
         constexpr int PT = decltype(type)::value;
         bool grown = false;
@@ -548,7 +550,9 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               y[r] = fast_exp2(z[s][m][r]);
-              p[m][s * 4 + r] = (short)from_f32<PT>(y[r]);
+              const uint16_t u = from_f32<PT>(y[r]);
+              p[m][s * 4 + r] = (short)u;
+              z[s][m][r] = y[r] - to_f32<PT>(u);
             }
             sum[m] = fmaf((y[0] + y[1]) + (y[2] + y[3]), iv[s], sum[m]);
           }
@@ -595,13 +599,14 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
         f32x4 z[2][MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
+          // (as they are, and read again: held over the key loop they would be spilled)
           s16x8 qf[KS];
-          if constexpr (DT == SD_BF16 || QL) queries(a, m, qf);
+          queries(a, m, qf);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             z[s][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) z[s][m] = mfma<DT>(kf[s][ks], DT == SD_BF16 || QL ? qf[ks] : q[m][ks], z[s][m]);
+            for (int ks = 0; ks < KS; ++ks) z[s][m] = mfma<DT>(kf[s][ks], qf[ks], z[s][m]);
           }
         }
 #pragma unroll
@@ -613,8 +618,17 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
           mask(z, m, (uint32_t)(vis[m] >> (kg * KEYS)));
         }
         const float one[2] = {1.0f, 1.0f};
-        s16x8 p[MT];
+        s16x8 p[MT], rest[MT];
         weigh(std::integral_constant<int, DT>{}, z, one, p);
+        // A node may dominate its row, and the sum that it is divided by holds its weight as
+        // it is: the 8 bits of a bf16 weight would be half a step of the result.  So what
+        // the rounding left enters too: weights of 16 bits, of 22 in fp16.
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) rest[m][s * 4 + r] = (short)from_f32<DT>(z[s][m][r]);
         // 0 x infinity in the product would reach rows that do not see this node:
         // such values are added at the end instead
         bool odd = false;
@@ -645,6 +659,8 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_quant_tiles(QAttnArgs a) {
           for (int m = 0; m < MT; ++m) {
             o[m][2 * i] = mfma<DT>(__builtin_bit_cast(s16x8, e), p[m], o[m][2 * i]);
             o[m][2 * i + 1] = mfma<DT>(__builtin_bit_cast(s16x8, g), p[m], o[m][2 * i + 1]);
+            o[m][2 * i] = mfma<DT>(__builtin_bit_cast(s16x8, e), rest[m], o[m][2 * i]);
+            o[m][2 * i + 1] = mfma<DT>(__builtin_bit_cast(s16x8, g), rest[m], o[m][2 * i + 1]);
           }
         }
         if (odd) odd_value = 1;

@@ -344,3 +344,49 @@ def test_queries_near_the_largest_of_their_type(D, code):
     got = out.double().cpu().numpy()
     assert (np.abs(got - o) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20) * np.abs(o)).all()
     assert (np.abs(lse.double().cpu().numpy() - e) <= es + 2.0 ** -22 * e).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("lens,nodes,Hq,Hkv,D", [
+    ([0, 0, 0], [2, 5, 64], 4, 2, 64), ([0, 0], [64, 33], 14, 2, 128), ([0, 0], [1, 40], 6, 2, 128),
+    ([1, 3, 20], [1, 4, 16], 14, 2, 64), ([2000, 40], [9, 64], 28, 4, 128)])
+def test_values_that_are_all_alike_are_their_average(lens, nodes, Hq, Hkv, D, dtype):
+    """Whatever the weights are: those of the nodes are exact to 16 bits and those of the
+    cache to fp16's 11, far from what half a step of the values' type would need."""
+    import torch
+    s = Quantised(31, lens, nodes, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, sigma=1.2)
+    dt = torch_dtype(dtype)
+    if max(lens):
+        if dtype == "f16":       # (its cached weights may be off by more than half a step)
+            lens = s.lens = [0] * len(lens)
+            s.d["context_lens"].zero_()
+        s.d["k_scale"].mul_(0.5)
+        s.d["v_cache"].fill_(64)
+        s.d["v_scale"].fill_(2.0 ** -6)
+        values = torch.ones(D)
+    else:
+        values = torch.tensor(rounded(s.rng.uniform(0.25, 4, D), dtype))
+    s.d["v_new"] = values.to(dt).cuda().expand(s.N, Hkv, D).contiguous()
+    for parents in (None, _parents(s)):
+        out, _ = _run(s, parents)
+        assert torch.equal(out, values.to(dt).cuda().expand_as(out))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_node_that_dominates_is_as_exact_as_its_value(D, dtype):
+    """One slot whose score is 0 and a node, both of value 127: their average is 127
+    whatever the weights, so a weight that is off by more than half a step of the
+    result's type shows."""
+    import torch
+    s = Quantised(38, [1] * 20, [1] * 20, Hq=28, Hkv=4, D=D, dtype=dtype, sigma=4.0)
+    dt = torch_dtype(dtype)
+    s.d["k_scale"].zero_()
+    s.d["v_cache"].fill_(127)
+    s.d["v_scale"].fill_(1.0)
+    s.d["v_new"].fill_(127)
+    out, lse = _run(s)
+    x = np.einsum("nhgd,nhd->nhg", s.q.reshape(20, 4, 7, D), s.kn).reshape(20, 28) * s.scale
+    assert ((x > 2) & (x < 5.5)).mean() > 0.1        # nodes of 2^3 to 2^8 times the slot's weight
+    assert torch.equal(out, torch.full_like(out, 127))
+    assert (np.abs(lse.double().cpu().numpy() - np.logaddexp(0, x)) <= s.score_error() + 2.0 ** -20).all()
