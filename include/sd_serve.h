@@ -116,9 +116,11 @@ typedef struct sd_quant_cache {
  * k_new and v_new are of the queries' type and enter as they are.
  * out = softmax(scores) . v, rounded once to the queries' type; out_lse (may be
  * NULL) = log sum exp(scores).  A row that sees nothing gets zeros and -inf.
- * Keys and values that a row does not see never reach its result.  Rows of a
- * request of wrong length get zeros and -inf; rows of one whose node offsets are
- * wrong, and rows of packed nodes that belong to no request, are left as they were.
+ * Keys and values that a row does not see never reach its result.  Pages and blocks
+ * of slots outside the sinks and the root's window are not looked at and report
+ * nothing.  Rows of a request of wrong length get zeros and -inf; rows of one whose
+ * node offsets are wrong, and rows of packed nodes that belong to no request, are left
+ * as they were.
  * out [N][H_q][D] and out_lse [N][H_q] are contiguous; out may be q where q is.
  * ------------------------------------------------------------------------ */
 typedef struct sd_quant_attention_args {

@@ -976,10 +976,12 @@ __global__ __launch_bounds__(WAVE) void k_quant_status(QAttnArgs a) {
   const int ctx = sdq::request_ctx(a.c, b, st);
   const int32_t* tab = a.c.table + b * a.c.ld_table;
   bool bad_page = false, bad_scale = false, bad_tree = false;
+  // slots that no row sees, between the sinks and what the root's window shows first, are
+  // not looked at
   const int last = first_seen(ctx, a.window ? a.window : INT_MAX);
+  auto hidden = [&](int slot, int shift) { return a.window && slot >= a.sinks && slot + (1 << shift) <= last; };
   for (int p = l; p < (ctx + a.c.page_mask) >> a.c.page_shift; p += WAVE) {
-    // pages that no row sees are not looked at
-    if (a.window && (p << a.c.page_shift) >= a.sinks && ((p + 1) << a.c.page_shift) <= last) continue;
+    if (hidden(p << a.c.page_shift, a.c.page_shift)) continue;
     const int page = tab[p];
     if ((unsigned)page >= (unsigned)a.c.num_pages) {
       bad_page = true;
@@ -988,6 +990,7 @@ __global__ __launch_bounds__(WAVE) void k_quant_status(QAttnArgs a) {
     const int used = min(ctx - (p << a.c.page_shift), a.c.page_mask + 1);
     for (int h = 0; h < a.c.H; ++h)
       for (int k = 0; k << a.c.block_shift < used; ++k) {
+        if (hidden((p << a.c.page_shift) + (k << a.c.block_shift), a.c.block_shift)) continue;
         const int64_t at = page * a.c.scale_page + h * a.c.scale_head + k;
         bad_scale |= !sdq::scale_ok(a.c.ks[at]) || !sdq::scale_ok(a.c.vs[at]);
       }

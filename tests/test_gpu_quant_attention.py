@@ -390,3 +390,31 @@ def test_a_node_that_dominates_is_as_exact_as_its_value(D, dtype):
     assert ((x > 2) & (x < 5.5)).mean() > 0.1        # nodes of 2^3 to 2^8 times the slot's weight
     assert torch.equal(out, torch.full_like(out, 127))
     assert (np.abs(lse.double().cpu().numpy() - np.logaddexp(0, x)) <= s.score_error() + 2.0 ** -20).all()
+
+
+def test_unsound_scales_that_no_row_sees_are_not_reported():
+    """Blocks outside the window and the sinks, on pages of which a part is seen."""
+    import torch
+    sdv = _sdv()
+    s = Quantised(32, [400, 400, 400, 120], [3, 1, 2, 2], Hq=4, Hkv=2, D=64, page=128, block=16)
+    # the window of 100 shows slots from 301 on (block 2 of page 2), the 20 sinks blocks 0 and 1
+    t = s.table
+    ref = s.reference(None, 100, 20)
+    for p, blk in ((0, 2), (0, 7), (2, 1), (1, 3)):
+        s.ks[t[0, p], 1, blk] = np.nan
+        s.vs[t[0, p], 0, blk] = -2.0
+    s.vs[t[1, 2], 1, 2] = np.inf             # seen by the window
+    s.ks[t[2, 0], 0, 1] = -1.0               # seen among the sinks
+    s.ks[t[3, 0], 0, 7] = np.inf             # the last one in use
+    s.d["k_scale"], s.d["v_scale"] = dev(s.ks), dev(s.vs)
+    st = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    out, lse = _run(s, window=100, sinks=20, status=st)
+    bad = sdv.SD_ST_BAD_SCALE
+    assert st.tolist() == [0, bad, bad, bad]
+    rows = slice(0, int(s.offsets[1]))
+    s2 = Quantised(32, [400, 400, 400, 120], [3, 1, 2, 2], Hq=4, Hkv=2, D=64, page=128, block=16)
+    clean, clean_lse = _run(s2, window=100, sinks=20)
+    assert torch.equal(out[rows], clean[rows]) and torch.equal(lse[rows], clean_lse[rows])
+    s2.check(clean, clean_lse, ref)
+    _run(s, status=st)                       # without a window everything is seen
+    assert st.tolist() == [bad] * 4
