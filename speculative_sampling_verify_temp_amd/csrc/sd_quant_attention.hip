@@ -1129,7 +1129,8 @@ extern "C" int sd_quant_attention(const sd_quant_attention_args_t* args, void* w
   if (out == args->k_new || out == args->v_new || out == args->cache.k || out == args->cache.v) return SD_EINVAL;
   // a query row is read by the workgroups of its own result alone, before they
   // write it or before the join does
-  if (out == args->q && (args->q_head != args->cache.D || args->q_node != (int64_t)args->H_q * args->cache.D))
+  if (out == args->q && ((args->H_q > 1 && args->q_head != args->cache.D) ||
+                         (args->N > 1 && args->q_node != (int64_t)args->H_q * args->cache.D)))
     return SD_EINVAL;
   if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return SD_EWORKSPACE;
   QAttnArgs a = device_args(args);

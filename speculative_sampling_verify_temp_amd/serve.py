@@ -21,8 +21,8 @@ import struct
 import torch
 
 from . import SD_BF16
-from .tree import (SD_F16, _done, _entry, _here, _on, _output, _plain, _rows, _size_entry, _status,
-                   _stream, _workspace)
+from .tree import (SD_F16, _done, _entry, _here, _on, _output, _plain, _size_entry, _status, _stream,
+                   _workspace)
 
 SD_I8, SD_E4M3 = 3, 4
 SD_MIN_BLOCK = 16
@@ -97,40 +97,6 @@ def _element(t, name):
     raise TypeError(f"{name} must be bfloat16 or float16 (got {t.dtype})")
 
 
-def _cache(k, v, k_scale, v_scale, table, lens):
-    """The fields of sd_quant_cache_t."""
-    if k.dtype is torch.int8:
-        code = SD_I8
-    elif k.dtype is torch.float8_e4m3fn:
-        code = SD_E4M3
-    else:
-        raise TypeError(f"the cache must be int8 or float8_e4m3fn (got {k.dtype})")
-    strides = k.stride()
-    if len(strides) != 4 or k.shape != v.shape or v.dtype is not k.dtype or strides != v.stride():
-        raise ValueError("k_cache and v_cache must be [pages][H_kv][page_size][D] with the same "
-                         "type, shape and strides")
-    pages, H, page, D = k.shape
-    ps, hs, ss, es = strides
-    if es != 1 and D > 1:
-        raise ValueError("the elements of a cache row must be contiguous")
-    sst = k_scale.stride()
-    if (k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 or len(sst) != 3 or
-            k_scale.shape != v_scale.shape or sst != v_scale.stride() or k_scale.shape[:2] != (pages, H)):
-        raise ValueError("k_scale and v_scale must be float32 [pages][H_kv][page_size / block] with "
-                         "the same shape and strides")
-    blocks = k_scale.shape[2]
-    if blocks < 1 or page % blocks or (blocks > 1 and sst[2] != 1):
-        raise ValueError("the scales of a page and head must be contiguous and divide the page")
-    if table.dtype is not torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("page_table must be int32 [B][max_pages] with contiguous rows")
-    B, cols = table.shape
-    return (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), ps, hs, ss, sst[0], sst[1],
-            table.data_ptr(), table.stride(0) if B > 1 else max(cols, table.stride(0)),
-            _plain(lens, torch.int32, "context_lens", (B,)), code, B, H, D, page, page // blocks, pages, cols)
-
-
-# ---- norms and rotation ----
-
 def _heads(t, name, like, N, D):
     """Rows [N][H][D] of this type: (pointer, strides, H); strides of axes of one
     say nothing."""
@@ -142,6 +108,58 @@ def _heads(t, name, like, N, D):
     H = t.shape[1]
     return t.data_ptr(), (node if N > 1 else H * D), (head if H > 1 else D), H
 
+
+def _rows(t, name, like, N, H, D):
+    """Rows [N][H][D] of this type and number of heads: (pointer, strides)."""
+    p, node, head, heads = _heads(t, name, like, N, D)
+    if heads != H:
+        raise ValueError(f"{name} must be {like.dtype} of shape {[N, H, D]}")
+    return p, node, head
+
+
+def _alike(a, b):
+    """Whether strides are the same; those of axes of one say nothing."""
+    return a.stride() == b.stride() or all(x == y for x, y, n in zip(a.stride(), b.stride(), a.shape) if n > 1)
+
+
+def _cache(k, v, k_scale, v_scale, table, lens):
+    """The fields of sd_quant_cache_t."""
+    if k.dtype is torch.int8:
+        code = SD_I8
+    elif k.dtype is torch.float8_e4m3fn:
+        code = SD_E4M3
+    else:
+        raise TypeError(f"the cache must be int8 or float8_e4m3fn (got {k.dtype})")
+    strides = k.stride()
+    if len(strides) != 4 or k.shape != v.shape or v.dtype is not k.dtype or not _alike(k, v):
+        raise ValueError("k_cache and v_cache must be [pages][H_kv][page_size][D] with the same "
+                         "type, shape and strides")
+    pages, H, page, D = k.shape
+    ps, hs, ss, es = strides
+    if es != 1 and D > 1:
+        raise ValueError("the elements of a cache row must be contiguous")
+    sst = k_scale.stride()
+    if (k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 or len(sst) != 3 or
+            k_scale.shape != v_scale.shape or not _alike(k_scale, v_scale) or k_scale.shape[:2] != (pages, H)):
+        raise ValueError("k_scale and v_scale must be float32 [pages][H_kv][page_size / block] with "
+                         "the same shape and strides")
+    blocks = k_scale.shape[2]
+    if blocks < 1 or page % blocks or (blocks > 1 and sst[2] != 1):
+        raise ValueError("the scales of a page and head must be contiguous and divide the page")
+    if table.dtype is not torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("page_table must be int32 [B][max_pages] with contiguous rows")
+    B, cols = table.shape
+    scale_page, scale_head, _ = sst
+    if pages == 1:
+        ps = scale_page = 0
+    if H == 1:
+        hs = scale_head = 0
+    return (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), ps, hs, ss, scale_page, scale_head,
+            table.data_ptr(), table.stride(0) if B > 1 else max(cols, table.stride(0)),
+            _plain(lens, torch.int32, "context_lens", (B,)), code, B, H, D, page, page // blocks, pages, cols)
+
+
+# ---- norms and rotation ----
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
                  interleaved=False, out_q=None, out_k=None, stream=None):

@@ -418,3 +418,35 @@ def test_unsound_scales_that_no_row_sees_are_not_reported():
     s2.check(clean, clean_lse, ref)
     _run(s, status=st)                       # without a window everything is seen
     assert st.tolist() == [bad] * 4
+
+
+def test_strides_of_axes_of_one_say_nothing():
+    """One node of a fused projection in place; a cache of one head and one page whose
+    strides along them are anything."""
+    import torch
+    s = Quantised(33, [90], [1], Hq=4, Hkv=2, D=64, packed=True)
+    out, lse = _run(s)
+    s.check(out, lse, s.reference())
+    q = s.d["q"]
+    assert q.is_contiguous() and q.stride(0) != q.shape[1] * q.shape[2]
+    got, again = _run(s, out=q)
+    assert got is q and torch.equal(got, out) and torch.equal(lse, again)
+    s = Quantised(34, [50], [3], Hq=4, Hkv=1, D=64, page=64, block=32, packed=True)
+    s.table[:] = 0
+    s.k, s.v, s.ks, s.vs = (x[:1] for x in (s.k, s.v, s.ks, s.vs))
+    d = s.d
+    d["page_table"].zero_()
+    for n, x in (("k_cache", s.k), ("v_cache", s.v), ("k_scale", s.ks), ("v_scale", s.vs)):
+        d[n] = code_dev(x, "i8") if "cache" in n else dev(x)
+    out, lse = _run(s)
+    s.check(out, lse, s.reference())
+    for n in ("k_cache", "v_cache"):
+        d[n] = d[n].as_strided((1, 1, 64, 64), (3, 5, 64, 1))
+    for n in ("k_new", "v_new"):
+        d[n] = d[n].contiguous().as_strided((3, 1, 64), (64, 7, 1))
+    got, again = _run(s)
+    assert torch.equal(got, out) and torch.equal(lse, again)
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _sdv().quant_append(*(d[n] for n in ("k_new", "v_new", "k_cache", "v_cache", "k_scale", "v_scale", "page_table",
+                                         "context_lens", "node_offsets")), 3, lens)
+    assert lens.tolist() == [53]

@@ -281,3 +281,33 @@ def test_the_binding_refuses_what_it_can_see(sdv):
                                                 torch.zeros(6, dtype=torch.int32), off, 3, torch.zeros(6), torch.zeros(2))):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_strides_of_axes_of_one_are_not_looked_at(sdv):
+    """One packed node in place of its query, wherever it lies; the binding's strides of
+    axes of one are those of no tensor."""
+    import torch
+    n = ctypes.c_size_t()
+    a = _attention()
+    a.N, a.max_nodes, a.q_node = 1, 1, 2048
+    a.cache.max_pages = a.cache.ld_table = 1000
+    assert _call(sdv, "attention", a, out=P(a.q), ws=None) == sdv.SD_EWORKSPACE      # all but the workspace is fine
+    a.N = 2
+    assert _call(sdv, "attention", a, out=P(a.q), ws=None) == -1
+    k = torch.zeros(64 * 64, dtype=torch.int8)
+    kc, vc = k.as_strided((1, 1, 64, 64), (3, 5, 64, 1)), k.as_strided((1, 1, 64, 64), (48, 7, 64, 1))
+    sc = torch.zeros(2)
+    x = torch.zeros(1, 3, 2, 64, dtype=torch.bfloat16)
+    got = sdv.make_quant_attention_args(
+        x[0, :1], x[0, :1, :1].as_strided((1, 1, 64), (3, 5, 1)), x[0, :1, :1], kc, vc, sc.as_strided((1, 1, 2), (9, 4, 1)),
+        sc.as_strided((1, 1, 2), (2, 6, 1)), torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
+        torch.tensor([0, 1], dtype=torch.int32), 1)
+    c = got.cache
+    assert (c.page_stride, c.head_stride, c.slot_stride, c.scale_page, c.scale_head) == (0, 0, 64, 0, 0)
+    assert got.k_node % 8 == got.k_head % 8 == 0
+    assert sdv.lib.sd_quant_attention_workspace_bytes(ctypes.byref(got), ctypes.byref(n)) == 0
+    for bad in (kc.as_strided((1, 1, 32, 64), (3, 5, 128, 1)), kc[:, :, :32]):      # strides of other axes
+        with pytest.raises(ValueError):
+            sdv.make_quant_attention_args(x[0, :1], x[0, :1, :1], x[0, :1, :1], kc, bad, sc.reshape(1, 1, 2), sc.reshape(1, 1, 2),
+                                          torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
+                                          torch.tensor([0, 1], dtype=torch.int32), 1)
