@@ -1126,7 +1126,18 @@ extern "C" int sd_quant_attention(const sd_quant_attention_args_t* args, void* w
   int rc = sd_quant_attention_workspace_bytes(args, &need);
   if (rc) return rc;
   if (!out || !aligned16(out)) return SD_EINVAL;
-  if (out == args->k_new || out == args->v_new || out == args->cache.k || out == args->cache.v) return SD_EINVAL;
+  const sd_quant_cache_t& c = args->cache;
+  const void* const outs[] = {out, out_lse, out_status};
+  const void* const ins[] = {args->k_new, args->v_new, c.k, c.v, c.k_scale, c.v_scale, c.page_table, c.context_lens,
+                             args->node_offsets, args->parents, need ? workspace : nullptr};
+  for (int i = 0; i < 3; ++i) {
+    if (!outs[i]) continue;
+    for (const void* in : ins)
+      if (outs[i] == in) return SD_EINVAL;
+    if (i && outs[i] == args->q) return SD_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (outs[i] == outs[j]) return SD_EINVAL;
+  }
   // a query row is read by the workgroups of its own result alone, before they
   // write it or before the join does
   if (out == args->q && ((args->H_q > 1 && args->q_head != args->cache.D) ||

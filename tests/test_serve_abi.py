@@ -311,3 +311,20 @@ def test_strides_of_axes_of_one_are_not_looked_at(sdv):
             sdv.make_quant_attention_args(x[0, :1], x[0, :1, :1], x[0, :1, :1], kc, bad, sc.reshape(1, 1, 2), sc.reshape(1, 1, 2),
                                           torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
                                           torch.tensor([0, 1], dtype=torch.int32), 1)
+
+
+def test_outputs_of_the_attention_that_may_not_be_inputs_are_refused(sdv):
+    """Every output against every input, the other outputs and the workspace."""
+    a = _attention()
+    a.parents = 0x440000
+    a.cache.max_pages = a.cache.ld_table = 1000
+    ws, out, lse, st = 0xA00000, 0x900000, 0x910000, 0x920000
+    call = lambda o, e, s: sdv.lib.sd_quant_attention(ctypes.byref(a), P(ws), 7, P(o), P(e), P(s), None)  # noqa: E731
+    assert call(out, lse, st) == sdv.SD_EWORKSPACE      # nothing but the workspace's size
+    ins = [a.k_new, a.v_new, a.cache.k, a.cache.v, a.cache.k_scale, a.cache.v_scale, a.cache.page_table,
+           a.cache.context_lens, a.node_offsets, a.parents, ws]
+    for x in ins:
+        assert call(x, lse, st) == call(out, x, st) == call(out, lse, x) == -1, hex(x)
+    assert call(out, a.q, st) == call(out, lse, a.q) == -1
+    assert call(out, out, st) == call(out, lse, out) == call(out, lse, lse) == -1
+    assert call(a.q, lse, st) == sdv.SD_EWORKSPACE
