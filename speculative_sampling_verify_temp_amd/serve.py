@@ -288,9 +288,9 @@ def quant_append(k_new, v_new, k_cache, v_cache, k_scale, v_scale, page_table, c
     B, H, D = c[13:16]
     code = _element(k_new, "k_new")
     kept = (0, 0, 0)
+    if (path is None) != (path_lens is None):
+        raise ValueError("path and path_lens are given together")
     if path is not None:
-        if path_lens is None:
-            raise ValueError("a path needs path_lens")
         cols = path.shape[-1]
         kept = (_plain(path, torch.int32, "path", (B, cols)), cols,
                 _plain(path_lens, torch.int32, "path_lens", (B,)))

@@ -178,3 +178,16 @@ def test_append_in_a_graph():
             assert torch.equal(d[n].view(torch.uint8), eager[n].view(torch.uint8)), n
         ctx.copy_(out)
     assert ctx.tolist() == [96, 96]
+
+
+def test_path_and_its_lengths_come_together():
+    """One without the other is refused, and nothing is appended."""
+    import torch
+    s = Quantised(8, [5, 9], [3, 2], Hq=2, Hkv=2, D=64, room=8)
+    before = _state(s)
+    path, m = torch.zeros((2, 3), dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    for kw in (dict(path=path), dict(path_lens=m)):
+        with pytest.raises(ValueError, match="path"):
+            _append(s, **kw)
+    for g, w in zip(_state(s), before):
+        assert _same(g, w)
