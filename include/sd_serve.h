@@ -247,7 +247,9 @@ int sd_tree_verify_sample(const sd_tree_sample_args_t *args, void *workspace,
                           uint32_t *out_status, void *stream);
 
 /* Test export: sd_tree_verify_sample with this many looks at a pass that is
- * waited for before its request is given up (SD_ST_UNFINISHED). */
+ * waited for before its request is given up (SD_ST_UNFINISHED).  Negative: with the
+ * usual number of them, and only half of the workgroups that share a request come: they
+ * take the others' slices over. */
 int sd_debug_tree_sample_polls(const sd_tree_sample_args_t *args, void *workspace,
                                size_t workspace_bytes, int32_t *out_accepted,
                                int32_t *out_path, int32_t *out_tokens,

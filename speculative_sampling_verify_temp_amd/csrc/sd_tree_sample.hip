@@ -569,12 +569,13 @@ extern "C" int sd_debug_tree_sample_polls(const sd_tree_sample_args_t* args, voi
   a.slices = slices_of(args);
   const int pieces = a.slices * WV;
   a.stretch = ((a.V + 3) / 4 + pieces - 1) / pieces;
-  a.polls = polls;
+  a.polls = polls < 0 ? MAX_POLLS : polls;
   a.team = static_cast<Team*>(workspace);
   a.accepted = out_accepted, a.path = out_path, a.out_tokens = out_tokens, a.status = out_status;
   hipStream_t st = static_cast<hipStream_t>(stream);
   hipLaunchKernelGGL(k_sample_begin, dim3(a.B), dim3(WAVE), 0, st, a);
   if (hipGetLastError() != hipSuccess) return SD_EHIP;
-  hipLaunchKernelGGL(k_sample_passes, dim3(a.slices, a.B), dim3(NT), 0, st, a);
+  // (a negative bound: half of each team stays away, the others take its slices over)
+  hipLaunchKernelGGL(k_sample_passes, dim3(polls < 0 ? (a.slices + 1) / 2 : a.slices, a.B), dim3(NT), 0, st, a);
   return hipGetLastError() == hipSuccess ? SD_OK : SD_EHIP;
 }

@@ -395,3 +395,44 @@ def test_a_beams_row_whose_whole_support_was_drafted(V):
         assert all(s & sdv.SD_ST_NONFINITE for s in st[:B2].cpu().numpy()[~ok])
         deep = np.arange(B2) % 4 == 0
         assert (want[0] == deep)[ok].all() and set(want[2][np.arange(B2), want[0]][ok]) <= {a, b}
+
+
+@pytest.mark.parametrize("drafts", ["again", "once", "beam"])
+@pytest.mark.parametrize("nodes,V", [([20], 151936), ([9] * 7, 20011), ([6] * 100, 9001), ([33] * 16, 60000)])
+def test_slices_that_are_taken_over(nodes, V, drafts):
+    """Half of a team's workgroups are not there: their slices are taken over, so that
+    workgroups hold several, lose some to each other and make sums again for the draw.
+    Without that, requests would be unfinished; the results are the oracle's."""
+    import torch
+    import speculative_sampling_verify_temp_amd.serve as serve
+    sdv = _sdv()
+    t = Trees(16, nodes, V, drafts, peak=1.5)
+    t.u[:] = 1 - (1 - t.u) * np.float32(0.25)         # many rejections
+    d = t.device()
+    B, T = len(nodes), max(nodes)
+    p, q = d["target_probs"], d["draft_probs"]
+    ld = p.stride(0) if t.N > 1 else (V + 3) // 4 * 4
+    a = serve._TREE_SAMPLE.pack(p.data_ptr(), 0 if q is None else q.data_ptr(), ld, ld, d["tokens"].data_ptr(),
+                                d["parents"].data_ptr(), d["node_offsets"].data_ptr(), d["accept_uniforms"].data_ptr(),
+                                d["draw_uniforms"].data_ptr(), B, t.N, V, V, T, sdv.SD_NO_REPLACEMENT if drafts == "once" else 0)
+    n = serve._tree_sample_bytes(a)
+    want = oracle.tree_sample_ref(t.p, t.q, t.tokens, t.parents, t.off, T, t.u, t.v, no_replacement=drafts == "once")
+    sure = want[3] > V * 2.0 ** -50
+    assert sure.mean() > 0.9
+    usual = sdv.tree_verify_sample(**d, flags=sdv.SD_NO_REPLACEMENT if drafts == "once" else 0)
+    P = ctypes.c_void_p
+    for _ in range(3):
+        ws = torch.full((n,), 0xEE, dtype=torch.uint8, device="cuda")
+        out = [torch.full(s, 7, dtype=torch.int32, device="cuda") for s in ((B,), (B, T), (B, T), (B,))]
+        rc = sdv.lib.sd_debug_tree_sample_polls(ctypes.c_char_p(a), P(ws.data_ptr()), ctypes.c_size_t(n),
+                                                *(P(o.data_ptr()) for o in out), ctypes.c_int32(-1),
+                                                P(torch.cuda.current_stream().cuda_stream))
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert not (out[3] & sdv.SD_ST_TREE_INVALID_MASK).any()
+        for o, w, x in zip(out, want, usual):
+            assert np.array_equal(o.cpu().numpy()[sure], w[sure]) and torch.equal(o, x)
+        # a slice's claims are counted: one for each pass, whoever made it
+        claims = ws.cpu().numpy().view(np.uint32).reshape(B, -1)[:, 256:320]
+        slices = int((claims[0] > 0).sum())
+        assert slices > 1 and (claims[:, :slices] == claims[:, :1]).all() and not claims[:, slices:].any()
