@@ -173,12 +173,10 @@ __device__ __forceinline__ Seen seen_by_lane(const QAttnArgs& a, int first, int 
   }
   s.depth = __popcll(s.nodes) - 1;
   if (a.window && a.window < T) {
-    const uint64_t all = s.nodes;
     for (int i = 0; i < T; ++i) {
       const int d = lane_read(s.depth, i);
       if (s.depth - d >= a.window && ctx + d >= a.sinks) s.nodes &= ~(1ull << i);
     }
-    s.nodes &= all;
   }
   return s;
 }

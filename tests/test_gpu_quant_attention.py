@@ -3,8 +3,8 @@ import numpy as np
 import pytest
 
 import oracle
-from servetools import Quantised, code_dev
-from treetools import dev, random_tree, rounded, torch_dtype
+from servetools import Quantised, code_dev, random_cache
+from treetools import EPS, dev, random_tree, rounded, torch_dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -450,3 +450,98 @@ def test_strides_of_axes_of_one_say_nothing():
     _sdv().quant_append(*(d[n] for n in ("k_new", "v_new", "k_cache", "v_cache", "k_scale", "v_scale", "page_table",
                                          "context_lens", "node_offsets")), 3, lens)
     assert lens.tolist() == [53]
+
+
+@pytest.mark.parametrize("code,dtype", [("i8", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("lens,nodes,Hq,Hkv,D,page", [
+    ([3000, 1], [1, 1], 14, 2, 64, 16), ([3000, 0, 1700, 2999], [1, 1, 1, 0], 28, 4, 128, 32),
+    ([3000, 800], [4, 2], 14, 2, 64, 64), ([1500, 3001, 77], [3, 4, 4], 28, 4, 128, 16)])
+def test_few_rows_over_many_tiles(lens, nodes, Hq, Hkv, D, page, code, dtype):
+    """Decoding in tables of more tiles than one workgroup takes: 16 and 32 rows of a KV
+    head, split over workgroups and joined."""
+    import torch
+    s = Quantised(35, lens, nodes, Hq=Hq, Hkv=Hkv, D=D, page=page, block=16, code=code, dtype=dtype, sigma=1.5)
+    n = _sdv().quant_attention_workspace_bytes(_sdv().make_quant_attention_args(**s.attention_args(), max_nodes=max(nodes)))
+    assert n > 0
+    out, lse = _run(s, workspace=torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"))
+    s.check(out, lse, s.reference())
+
+
+@pytest.mark.parametrize("code,T,Hq", [("i8", 1, 2), ("e4m3", 4, 8), ("i8", 20, 2), ("e4m3", 30, 3)])
+def test_many_requests_in_split_tables(code, T, Hq):
+    """Three times 64 requests, most of them short, some without nodes, some long."""
+    import torch
+    rng = np.random.default_rng(36)
+    B = 135
+    lens, nodes = rng.integers(0, 50, B), rng.integers(0, T + 1, B)
+    lens[[3, 63, 64, 66, 130, 134]] = [1500, 700, 1490, 64, 1333, 900]
+    nodes[[3, 64, 130, 134]] = T
+    nodes[[0, 62, 65, 127, 128]] = 0
+    s = Quantised(36, lens.tolist(), nodes.tolist(), Hq=Hq, Hkv=1, D=64, page=64, block=32, code=code)
+    n = _sdv().quant_attention_workspace_bytes(_sdv().make_quant_attention_args(**s.attention_args(), max_nodes=T))
+    assert n > 0
+    parents = _parents(s)
+    out, lse = _run(s, parents, workspace=torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"))
+    s.check(out, lse, s.reference(parents))
+
+
+@pytest.mark.parametrize("T,G", [(2, 2), (4, 7), (20, 2), (48, 2)])
+@pytest.mark.parametrize("code,dtype,D", [("i8", "bf16", 64), ("e4m3", "bf16", 128), ("i8", "f16", 128), ("e4m3", "f16", 64)])
+def test_runs_of_more_tiles_than_are_looked_up_at_once(T, G, code, dtype, D):
+    """A large batch of long contexts, whose workgroups go through more than 32 tiles on
+    end: scales that differ from block to block, unsound ones and codes that are not
+    numbers all along.  Every row against a softmax in 64 bits."""
+    import torch
+    sdv = _sdv()
+    rng = np.random.default_rng(37)
+    B, H, page, block, pool = 66, 8, 128, 32, 150
+    lens = rng.integers(4300, 6000, B)
+    nodes = rng.integers(1, T + 1, B)
+    nodes[[0, 1, 65]] = T
+    nodes[40] = 0
+    off = np.concatenate([[0], np.cumsum(nodes)]).astype(np.int32)
+    N, Hq = int(off[-1]), H * G
+    table = rng.integers(0, pool, (B, 47)).astype(np.int32)      # (requests share pages)
+    k, ks = random_cache(rng, pool, H, page, D, block, code, 0.3)
+    v, vs = random_cache(rng, pool, H, page, D, block, code, 0.3)
+    kd, vd = code_dev(k, code), code_dev(v, code)
+    if code == "e4m3":
+        kd[5, 3, 17, 9] = float("nan")
+        vd[77, 1, 100, D - 2] = float("nan")
+    for x, value in ((ks, np.nan), (ks, -1.0), (vs, np.inf), (vs, 2.0 ** -60)):
+        x[rng.random(x.shape) < 0.005] = value
+    dt = torch_dtype(dtype)
+    q, kn, vn = (dev(rng.standard_normal((N, h, D)) * sigma, dt) for h, sigma in ((Hq, 2.0), (H, 1.0), (H, 1.0)))
+    t = {n: dev(x) for n, x in (("ks", ks), ("vs", vs), ("table", table), ("lens", lens.astype(np.int32)), ("off", off))}
+    args = (q, kn, vn, kd, vd, t["ks"], t["vs"], t["table"], t["lens"], t["off"], T)
+    out, lse = sdv.quant_attention(*args, want_lse=True)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    # the definition, a request and head at a time
+    sound = lambda x: (x == 0) | ((x >= 2.0 ** -50) & (x <= 2.0 ** 50))  # noqa: E731
+    there = (sound(t["ks"]) & sound(t["vs"]))
+    key, val = (torch.nan_to_num(c.double()) * torch.where(there, x, 0).double().repeat_interleave(block, 2)[..., None]
+                for c, x in ((kd, t["ks"]), (vd, t["vs"])))
+    there = there.repeat_interleave(block, 2)
+    top = oracle.serve.TOP[code]
+    n = 6000 + T + 64
+    qmax, big = q.double().abs().max(), max(np.nanmax(np.where(np.isfinite(vs), vs, 0)) * top, vn.abs().max().item())
+    eps = EPS[dtype]
+    es = (D + 8) * 2.0 ** -24 * D ** 0.5 * qmax.item() * max(np.nanmax(ks) * top, kn.abs().max().item()) + 2.0 ** -20
+    more = n * 2.0 ** -24 * 255 * np.nanmax(np.where(np.isfinite(vs), vs, 0)) if code == "i8" else 0.0
+    for b in range(B):
+        lo, hi, m = int(off[b]), int(off[b + 1]), int(lens[b])
+        if lo == hi:
+            continue
+        at = t["table"][b].long()
+        for h in range(H):
+            rows = lambda x: x[at, h].reshape(-1, *x.shape[3:])[:m]  # noqa: E731
+            kk, vv = torch.cat([rows(key), kn[lo:hi, h].double()]), torch.cat([rows(val), vn[lo:hi, h].double()])
+            sees = torch.cat([rows(there).expand(hi - lo, m), torch.ones((hi - lo, hi - lo), device="cuda").tril().bool()], 1)
+            for g in range(h * G, (h + 1) * G):
+                x = (q[lo:hi, g].double() @ kk.t() * D ** -0.5).masked_fill(~sees, -np.inf)
+                w = torch.softmax(x, 1)
+                o, mag = w @ vv, w @ vv.abs()
+                tol = eps * o.abs() + (eps + 2 * es + n * 2.0 ** -24) * (1 + eps) * mag + n * 2.0 ** -32 * big + 2.0 ** -24 + more
+                assert ((out[lo:hi, g].double() - o).abs() <= tol).all(), (b, h, g)
+                e = torch.logsumexp(x, 1)
+                assert ((lse[lo:hi, g].double() - e).abs() <= es + n * 2.0 ** -24 + 2.0 ** -22 * (1 + e.abs())).all(), (b, h, g)
