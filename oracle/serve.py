@@ -7,6 +7,7 @@ row and node by node from the definitions in include/sd_serve.h.  Parity: pinned
 by closed forms, identities and brute force in tests/test_oracle_serve.py.
 """
 import math
+from fractions import Fraction
 
 import numpy as np
 
@@ -14,6 +15,17 @@ from .tree import attend, visible_nodes
 
 TOP = {"i8": 127.0, "e4m3": 448.0}
 MIN_SCALE, MAX_SCALE = np.float32(2.0 ** -50), np.float32(2.0 ** 50)
+
+
+# 2 pi times 2^200, to the nearest (pi to 64 digits).
+TWO_PI = round(2 * Fraction("3.141592653589793238462643383279502884197169399375105820974944592") * 2 ** 200)
+
+
+def turned(position, freq):
+    """position * freq (an fp32 number) reduced to one turn, in whole numbers: products of
+    far positions lose bits in fp64."""
+    num, den = (int(position) * Fraction(float(freq))).as_integer_ratio()
+    return ((num << 200) // den % TWO_PI) / 2 ** 200
 
 
 def norm_rope_ref(x, weight, positions, inv_freq, eps, interleaved=False):
@@ -26,7 +38,7 @@ def norm_rope_ref(x, weight, positions, inv_freq, eps, interleaved=False):
     for n, pos in enumerate(positions):
         for j in range(half):
             a, b = (2 * j, 2 * j + 1) if interleaved else (j, j + half)
-            t = int(pos) * float(inv_freq[j])
+            t = turned(pos, inv_freq[j])
             c, s = math.cos(t), math.sin(t)
             out[n, :, a] = y[n, :, a] * c - y[n, :, b] * s
             out[n, :, b] = y[n, :, b] * c + y[n, :, a] * s

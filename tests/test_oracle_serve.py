@@ -33,6 +33,23 @@ def test_norm_and_rotation_identities():
     assert np.allclose((n * n).mean(-1), 4.0)
 
 
+def test_rotation_of_far_positions():
+    """Sines and cosines of products that fp64 rounds, against 64-bit mantissas, which hold
+    positions of 31 bits times fp32 frequencies exactly; 2 pi in them is off by 2^-63, so
+    2^29 turns by 2^-34."""
+    assert np.finfo(np.longdouble).nmant >= 63
+    two_pi = 8 * np.arctan(np.longdouble(1))
+    rng = np.random.default_rng(3)
+    pos = np.concatenate([rng.integers(2 ** 30, 2 ** 31, 40), [2 ** 31 - 1, -2 ** 31]])
+    freq = rng.uniform(0.5, 1.0, 8).astype(np.float32)
+    x = np.zeros((len(pos), 1, 16))
+    x[..., :8] = 1
+    y = oracle.norm_rope_ref(x, None, pos, freq, 0.0)[:, 0]
+    t = pos[:, None].astype(np.longdouble) * freq.astype(np.longdouble)
+    t = t - np.rint(t / two_pi) * two_pi
+    assert (np.abs(y[:, :8] - np.cos(t)) < 2.0 ** -32).all() and (np.abs(y[:, 8:] - np.sin(t)) < 2.0 ** -32).all()
+
+
 def test_e4m3_values_against_the_whole_format():
     """Nearest of all 253 finite values, ties to the even code, by brute force."""
     import torch
