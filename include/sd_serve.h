@@ -59,7 +59,8 @@ typedef struct sd_qk_norm_rope_args {
   int64_t        q_node, q_head, k_node, k_head;
   int64_t        q_out_node, q_out_head, k_out_node, k_out_head;   /* no two rows
                                     of an output share memory                   */
-  const void    *q_weight;       /* [D] of the element type, or NULL            */
+  const void    *q_weight;       /* [D] of the element type, 16-byte aligned, or
+                                    NULL                                        */
   const void    *k_weight;
   const int32_t *positions;      /* [N]                                         */
   const float   *inv_freq;       /* [rot / 2]                                   */
@@ -211,7 +212,8 @@ int sd_quant_append(const sd_quant_append_args_t *args, int32_t *out_context,
  * is drawn from p without the rejected tokens.  Where they were all that p holds (its
  * numbers sum to 1 only within rounding, so even the last of them can be rejected),
  * SD_ST_RESID_ZERO is set and the token is drawn from p.
- * Arithmetic is in 64 bits.  Outputs as in sd_tree_verify_greedy: out_accepted
+ * Arithmetic is in 64 bits, but the sums of up to 64 slices that a row is cut into
+ * are kept to 46 bits (2^-45 of themselves).  Outputs as in sd_tree_verify_greedy: out_accepted
  * [B], out_path [B][max_nodes], out_tokens [B][max_nodes]; with SD_NO_BONUS the
  * last token is left out where the walk ends at a node without children.
  * Only what the walk uses is examined.  Invalid: SD_ST_BAD_NODES,

@@ -35,16 +35,23 @@
 // equal runs, one per workgroup; parts are joined in a fixed order.  Through a
 // window only the key tiles that it (or the sinks) touches are units.
 //
-// What bounds it is the issue of two waves a SIMD, 330 instructions for 32 keys of 32
-// rows: a third of them widen codes (each once a wave), half are the softmax, 34 matrix
-// products.  So rows are cheap where they share a widened key: 48 of them a wave do 400.
-//   32 chains of 9, 28/4 heads of 128, e4m3, 500-16384 slots    80 us + join 7   (bytes: 55)
-//   23 trees of 21, 16/8 heads, int8, fp16, window 4099         60 + 6           (bytes: 35)
-//   16 trees of 64, 28/4 heads, int8, 16384-32768 slots         440 + 11         (products: 251)
-//   1 token, 14/2 heads of 64, 517 slots                        8.6, latency
-// Tried without gain: three waves a SIMD (spills), two tiles on their way, keys widened
-// once into LDS for both groups, the products of a tile under the softmax of the one
-// before, loads that pass the caches by (98 instead of 82), 8 or 16 waves on one token.
+// A wave issues 320 instructions for 32 int8 keys of 32 rows: 96 widen codes (each once
+// a wave), 80 are the softmax, 34 matrix products, 12 loads, the rest broadcasts, scalar
+// work and waits; 400 for 48 rows, so rows are cheap where they share a widened key.  On
+// long contexts the vector units issue 59% of the time and the matrix units work 36%, one
+// after the other; the smaller cases wait besides, for loads and at the runs' ends
+// (41% and 17%, 38% and 16%).  Medians of the trace, in us:
+//   32 chains of 9, 28/4 heads of 128, e4m3, 500-16384 slots    85 + join 7   (bytes: 55)
+//   23 trees of 21, 16/8 heads, int8, fp16, window 4099         60 + 6        (bytes: 35)
+//   16 trees of 64, 28/4 heads, int8, 16384-32768 slots         440 + 11      (products: 251)
+//   1 token, 14/2 heads of 64, 517 slots                        8.8, latency
+// Registers: nothing is spilled by up to 64 rows a workgroup (one register by 32 fp16
+// rows over e4m3 codes of 128 columns); the 96-row shape of 128 columns spills 84 to
+// 103, outside the key loop but for one or two moves where slots are looked up.
+// Tried without gain: three waves a SIMD (spills), four row tiles a wave (spills), two
+// tiles on their way, keys widened once into LDS for both groups, the products of a tile
+// under the softmax of the one before, loads that pass the caches by (98 instead of 82),
+// 8 or 16 waves on one token.
 #include <algorithm>
 #include <type_traits>
 

@@ -86,8 +86,10 @@ __global__ __launch_bounds__(NT_R) void k_norm_rope(RopeArgs a) {
   int r = tid / LPR;
   if (r < rows) load(r);
 
-  // the angle in turns: a product of 24 and 31 bits and one of 53, so off by
-  // 2^-52 of itself, far below fp32's step of the fraction that is left
+  // the angle in turns: two products and a constant, each rounded to 53 bits, so off
+  // by at most 3 2^-53 of itself.  That is below fp32's own rounding of the fraction
+  // that is left, 2^-26, for angles of up to 2^25 turns, and 2^-23 turns at the
+  // farthest positions
   for (int i = tid; i < nt * half; i += NT_R) {
     const int t = i / half, j = i - t * half;
     const double turns = (double)a.pos[t0 + t] * (double)a.freq[j] * 0.15915494309189533577;

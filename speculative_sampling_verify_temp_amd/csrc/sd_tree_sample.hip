@@ -8,11 +8,11 @@
 //
 // So a request makes one pass over the rows of a node for each rejection on its
 // walk, and one for the draw where nothing was rejected at its last node.  Bound
-// by the latency of passes that follow each other: at a pass's end what a wave sums up
-// travels to the others and back, some 4 us, and the longest walk of a batch has
-// several.  Rows of 151936: 1 tree of 16 nodes 15 us; 64 trees of 20, draws without
-// replacement, up to 4 passes, 40 us (their bytes alone: 15); 48 trees of a beam, one
-// pass each, 19 us (6).
+// by passes that follow each other: each reads its rows (again, where only cut has
+// changed since the one before), and at its end what a wave sums up travels to the
+// others and back, some 4 us; the longest walk of a batch has several.  Rows of 151936:
+// 1 tree of 16 nodes 15 us; 64 trees of 20, draws without replacement, up to 4 passes,
+// 40 us (the bytes of one pass: 15); 48 trees of a beam, one pass each, 18 us (6).
 //
 // k_sample_begin    clears what the teams share.
 // k_sample_passes   teams of workgroups, one a slice of the vocabulary; each of their
@@ -517,7 +517,7 @@ int check(const sd_tree_sample_args_t* p) {
 }
 
 // Workgroups that share a request's rows: two a CU in all (one: 45 instead of 40 us
-// in the case of 64 trees); none with less than 64 vectors a wave.
+// in the case of 64 trees); where they are several, none with less than 32 vectors a wave.
 int slices_of(const sd_tree_sample_args_t* p) {
   const int nvec = (p->V + 3) / 4;
   return std::max(1, std::min({512 / p->B, (nvec + NT - 1) / NT, MAX_SLICES}));
